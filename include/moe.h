@@ -145,6 +145,103 @@ moe_status moe_topk_from_logits(const moe_config* cfg, const float* logits, int 
                                 int32_t* idx, float* w, cudaStream_t stream);
 
 /* ------------------------------------------------------------------------
+ * Expert choice from router logits, beyond the softmax top-K above: the forms
+ * that models with a balance bias and groups of experts use.  Per token, with
+ * l the E logits (a NaN ranks as -inf, +inf counts as the largest finite
+ * float):
+ *   score      s_e = softmax(l)_e over all E, or sigmoid(l_e)
+ *   value      v_e = s_e + select_bias_e (fp32 [E]; NULL: no bias).  The bias
+ *              takes part in the choice only, never in the weights; -inf takes
+ *              an expert out of service (it is chosen only when nothing else is
+ *              left); a NaN sum ranks as -inf
+ *   groups     the E experts are n_groups equal runs; a group's value is the
+ *              largest v of its experts (MOE_GROUP_MAX) or the sum of its two
+ *              largest (MOE_GROUP_TOP2; one expert: that one); the topk_groups
+ *              groups of largest value are kept, ties to the lower index
+ *   idx        the K kept experts of largest v, descending, ties to the lower
+ *              index
+ *   w          scale * s_idx, or scale * s_idx / sum of the K chosen s with
+ *              renormalise (0 when that sum is 0, as for a row of -inf)
+ * Values are compared in fp64 (without a bias and within a group the order is
+ * that of the logits), so the choice does not hang on how an fp32 sigmoid
+ * rounds; weights are rounded to fp32 once.
+ * Limits: E <= 2048, K <= 32, n_groups <= 32, K <= topk_groups * E / n_groups. */
+enum { MOE_SCORE_SOFTMAX = 0, MOE_SCORE_SIGMOID = 1 };
+enum { MOE_GROUP_MAX = 0, MOE_GROUP_TOP2 = 1 };
+typedef struct {
+  int n_experts, top_k;
+  int score;                  /* MOE_SCORE_* */
+  int n_groups, topk_groups;  /* 1, 1: no groups */
+  int group_score;            /* MOE_GROUP_* */
+  int renormalise;            /* 0 or 1 */
+  float scale;                /* finite */
+} moe_route_config;
+
+/* Element types of the calls below. */
+enum { MOE_BF16 = 0, MOE_F16 = 1, MOE_F32 = 2 };
+
+/* logits [T][E] (device, MOE_F32, MOE_BF16 or MOE_F16), rows ldl >= E elements
+ * apart; idx int32 [T][K], w fp32 [T][K] (device).  T == 0 is a no-op. */
+moe_status moe_route_from_logits(const moe_route_config* cfg, const void* logits, int dtype, int64_t ldl,
+                                 const float* select_bias, int T, int32_t* idx, float* w, cudaStream_t stream);
+
+/* The router projection and the choice: logits = x . Wr^T + router_bias (fp32,
+ * moe_linear_forward's product), then moe_route_from_logits.  x bf16
+ * [T][hidden] and wr bf16 [E][hidden] 16-byte aligned, hidden a multiple of 8;
+ * router_bias fp32 [E] or NULL.  The logits go to logits_out (fp32 [T][E]) or,
+ * when that is NULL, to the workspace (moe_route_workspace_bytes). */
+size_t moe_route_workspace_bytes(const moe_route_config* cfg, int T);
+moe_status moe_route_topk(const moe_route_config* cfg, int hidden, const void* x_bf16, const void* wr_bf16,
+                          const float* router_bias, const float* select_bias, int T, int32_t* idx, float* w,
+                          float* logits_out, void* workspace, size_t ws_bytes, cudaStream_t stream);
+
+/* ------------------------------------------------------------------------
+ * Dense product with its epilogue: the layer's neighbours (the projection
+ * that writes the residual stream before the layer, router logits, a dense or
+ * shared FFN of any width), as the pages' GPU command before the experts runs
+ * output projection, norm, routing and shared expert together (hakusoku,
+ * section "パイプライン概要").
+ *   y[t][n] = act(sum_k x[t][k] w[n][k] + bias[n])
+ *               [* (sum_k x[t][k] w_up[n][k] + bias_up[n])   when gated]
+ *               [+ residual[t][n]]
+ * fp32 accumulation and epilogue, one rounding to the output type.
+ *   act: MOE_ACT_NONE v; SILU v / (1 + e^-v); GELU v * Phi(v) (normal CDF);
+ *        GELU_TANH 0.5 v (1 + tanh(sqrt(2/pi) (v + 0.044715 v^3))); RELU max(v, 0)
+ * x [T][K] and w, w_up [N][K] of one 16-bit type (dtype MOE_BF16 or MOE_F16);
+ * bias, bias_up fp32 [N] or NULL; residual and out [T][N] of out_dtype (dtype
+ * or MOE_F32).  Rows are ldx, ldw, ldw_up, ldr, ldo elements apart.  x, w and
+ * w_up must start on a 16-byte boundary with row strides that are multiples of
+ * 8; residual and out need their element's alignment only (16-byte aligned
+ * rows are written faster).  K and N are any positive numbers up to 2^20.
+ * out may be the residual buffer itself (same address and stride: the result
+ * replaces it); otherwise out must not overlap any input.  T == 0 is a no-op.
+ * Needs no workspace; results are the same from run to run (sums split over
+ * blocks are joined in a fixed order).  A bounded device wait that expires is
+ * reported by moe_linear_device_error. */
+enum { MOE_ACT_NONE = 0, MOE_ACT_SILU = 1, MOE_ACT_GELU = 2, MOE_ACT_GELU_TANH = 3, MOE_ACT_RELU = 4 };
+typedef struct {
+  int in_features, out_features; /* K, N */
+  int dtype, out_dtype;
+  int act;
+  int gated; /* 0 or 1 */
+} moe_linear_config;
+typedef struct {
+  const void* w;
+  const void* w_up;     /* gated only */
+  const float* bias;    /* fp32 [N] or NULL */
+  const float* bias_up; /* gated only; fp32 [N] or NULL */
+  int64_t ldw, ldw_up;
+} moe_linear_weights;
+moe_status moe_linear_forward(const moe_linear_config* cfg, const moe_linear_weights* wts, const void* x, int64_t ldx,
+                              const void* residual, int64_t ldr, int T, void* out, int64_t ldo, cudaStream_t stream);
+
+/* The device-side error of the moe_linear_forward calls (and moe_route_topk's
+ * products) on the current device since the last read: synchronises the
+ * stream, returns MOE_OK or MOE_ERR_TIMEOUT and clears the word; *detail (may
+ * be NULL) gets the raw code. */
+moe_status moe_linear_device_error(uint32_t* detail, cudaStream_t stream);
+
+/* ------------------------------------------------------------------------
  * Whole layer.
  * ------------------------------------------------------------------------ */
 typedef struct {
@@ -269,6 +366,19 @@ moe_status moe_layer_forward_routed(const moe_config* cfg, const moe_layer_weigh
                                     const int32_t* idx, const float* w, void* h_out_bf16,
                                     void* y_norm_bf16, void* workspace, size_t ws_bytes,
                                     cudaStream_t stream);
+
+/* The batched path (moe_layer_forward_batched) with the routing given: the
+ * prompt-side call behind a router of the caller's own (moe_route_topk).
+ * Arguments as moe_layer_forward_routed, workspace
+ * moe_layer_batched_workspace_bytes; the router weights are not read and may be
+ * NULL.  A token may name one expert more than once.  An id outside [0, E) or a
+ * bad pointer for a chosen expert leaves MOE_ERR_DEVICE in the workspace
+ * (moe_device_error) and the outputs unspecified. */
+moe_status moe_layer_forward_routed_batched(const moe_config* cfg, const moe_layer_weights* wts,
+                                            const void* x_bf16, const void* residual_bf16, int T,
+                                            const int32_t* idx, const float* w, void* h_out_bf16,
+                                            void* y_norm_bf16, void* workspace, size_t ws_bytes,
+                                            cudaStream_t stream);
 
 /* Allocation-free variant of moe_layer_forward.  The pages have no
  * counterpart: their engine owns all of its buffers.  It is for callers that

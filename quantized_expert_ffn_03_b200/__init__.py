@@ -49,6 +49,21 @@ class MoeLayerWeights(C.Structure):
                 ("gamma", C.c_void_p), ("shared_out_gate", C.c_void_p), ("shared_packed", C.c_void_p)]
 
 
+class MoeLinearConfig(C.Structure):
+    _fields_ = [("in_features", C.c_int), ("out_features", C.c_int), ("dtype", C.c_int), ("out_dtype", C.c_int),
+                ("act", C.c_int), ("gated", C.c_int)]
+
+
+class MoeLinearWeights(C.Structure):
+    _fields_ = [("w", C.c_void_p), ("w_up", C.c_void_p), ("bias", C.c_void_p), ("bias_up", C.c_void_p),
+                ("ldw", C.c_int64), ("ldw_up", C.c_int64)]
+
+
+class MoeRouteConfig(C.Structure):
+    _fields_ = [("n_experts", C.c_int), ("top_k", C.c_int), ("score", C.c_int), ("n_groups", C.c_int),
+                ("topk_groups", C.c_int), ("group_score", C.c_int), ("renormalise", C.c_int), ("scale", C.c_float)]
+
+
 EXPORTS = {
     "moe_last_error": (C.c_char_p, []),
     "moe_packed_expert_bytes": (C.c_size_t, [C.c_void_p]),
@@ -94,6 +109,17 @@ EXPORTS = {
     "moe_layer_forward_routed": (C.c_int, [C.c_void_p, C.c_void_p, C.c_void_p, C.c_void_p, C.c_int,
                                            C.c_void_p, C.c_void_p, C.c_void_p, C.c_void_p, C.c_void_p,
                                            C.c_size_t, C.c_void_p]),
+    "moe_layer_forward_routed_batched": (C.c_int, [C.c_void_p, C.c_void_p, C.c_void_p, C.c_void_p, C.c_int,
+                                                   C.c_void_p, C.c_void_p, C.c_void_p, C.c_void_p, C.c_void_p,
+                                                   C.c_size_t, C.c_void_p]),
+    "moe_route_from_logits": (C.c_int, [C.c_void_p, C.c_void_p, C.c_int, C.c_int64, C.c_void_p, C.c_int,
+                                        C.c_void_p, C.c_void_p, C.c_void_p]),
+    "moe_route_workspace_bytes": (C.c_size_t, [C.c_void_p, C.c_int]),
+    "moe_route_topk": (C.c_int, [C.c_void_p, C.c_int, C.c_void_p, C.c_void_p, C.c_void_p, C.c_void_p, C.c_int,
+                                 C.c_void_p, C.c_void_p, C.c_void_p, C.c_void_p, C.c_size_t, C.c_void_p]),
+    "moe_linear_forward": (C.c_int, [C.c_void_p, C.c_void_p, C.c_void_p, C.c_int64, C.c_void_p, C.c_int64, C.c_int,
+                                     C.c_void_p, C.c_int64, C.c_void_p]),
+    "moe_linear_device_error": (C.c_int, [C.c_void_p, C.c_void_p]),
     "moe_stream_create": (C.c_int, [C.c_void_p, C.c_int, C.c_void_p, C.c_size_t, C.c_int, C.c_void_p]),
     "moe_stream_inject_fault": (C.c_int, [C.c_void_p, C.c_int, C.c_int]),
     "moe_stream_create_file": (C.c_int, [C.c_void_p, C.c_int, C.c_char_p, C.c_int, C.c_int, C.c_int,
@@ -342,6 +368,173 @@ def moe_layer_forward_host_packed(cfg, wts, xr, hy, workspace, stream=None):
     T = xr.shape[1]
     _check(_lib.moe_layer_forward_host_packed(C.byref(cfg), C.byref(wts), _ptr(xr), T, _ptr(hy), _ptr(workspace),
                                               workspace.numel() * workspace.element_size(), _stream(stream)))
+
+
+def moe_layer_forward_routed_batched(cfg, wts, x, residual, idx, w, h_out, y_norm, workspace, stream=None):
+    """The batched path with the routing given: idx int32 [T][K], w float32 [T][K] (CUDA)."""
+    T = x.shape[0]
+    _check(_lib.moe_layer_forward_routed_batched(C.byref(cfg), C.byref(wts), _ptr(x), _ptr(residual), T, _ptr(idx),
+                                                 _ptr(w), _ptr(h_out), _ptr(y_norm), _ptr(workspace),
+                                                 workspace.numel() * workspace.element_size(), _stream(stream)))
+
+
+# ---- expert choice and dense products ----------------------------------------------
+# Unlike the calls above these take strided rows, so they check the tensors'
+# shapes, types, strides and device and raise MoeError(MOE_ERR_INVALID_ARG).
+
+MOE_ERR_INVALID_ARG = 1
+MOE_BF16, MOE_F16, MOE_F32 = 0, 1, 2
+MOE_ACT_NONE, MOE_ACT_SILU, MOE_ACT_GELU, MOE_ACT_GELU_TANH, MOE_ACT_RELU = 0, 1, 2, 3, 4
+MOE_SCORE_SOFTMAX, MOE_SCORE_SIGMOID = 0, 1
+MOE_GROUP_MAX, MOE_GROUP_TOP2 = 0, 1
+
+_DTYPE_NAMES = {MOE_BF16: ("bfloat16", "int16", "uint16"), MOE_F16: ("float16", "int16", "uint16"),
+                MOE_F32: ("float32",)}
+_dtype_sets = {}
+
+
+def _is_dtype(t, code):
+    """Whether tensor t holds elements of the code (16-bit types also as integer views)."""
+    s = _dtype_sets.get(code)
+    if s is None:
+        import torch
+        s = _dtype_sets[code] = frozenset(getattr(torch, n) for n in _DTYPE_NAMES[code])
+    return t.dtype in s
+
+
+def _bad(what):
+    raise MoeError(MOE_ERR_INVALID_ARG, what)
+
+
+def _rows(t, name, shape, code, dev):
+    """Row stride of a 2-d CUDA tensor with adjacent columns; raises otherwise."""
+    if t.shape != shape or not _is_dtype(t, code):
+        _bad("%s must be %s of type %s, got %s %s" % (name, tuple(shape), _DTYPE_NAMES[code][0], tuple(t.shape), t.dtype))
+    if t.get_device() != dev:
+        _bad("%s must be on the current CUDA device" % name)
+    ld, step = t.stride()
+    if step != 1 and shape[1] > 1:
+        _bad("%s must have adjacent columns" % name)
+    return ld if shape[0] > 1 else (shape[1] + 7) & ~7  # a single row: its stride is never used
+
+
+def _vec(t, name, n, dev):
+    if t.shape != (n,) or not _is_dtype(t, MOE_F32) or (n > 1 and t.stride(0) != 1):
+        _bad("%s must be a contiguous float32 vector of %d" % (name, n))
+    if t.get_device() != dev:
+        _bad("%s must be on the current CUDA device" % name)
+    return t.data_ptr()
+
+
+_torch_c = None
+
+
+def _current():
+    """(current CUDA device, raw handle of its current stream)."""
+    global _torch_c
+    if _torch_c is None:
+        import torch
+        _torch_c = torch._C
+        torch.cuda.current_stream()  # initialises CUDA
+    dev = _torch_c._cuda_getDevice()
+    return dev, _torch_c._cuda_getCurrentRawStream(dev)
+
+
+def linear_config(in_features, out_features, act=MOE_ACT_NONE, gated=False, dtype=MOE_BF16, out_dtype=None):
+    return MoeLinearConfig(in_features, out_features, dtype, dtype if out_dtype is None else out_dtype, act,
+                           1 if gated else 0)
+
+
+def linear_weights(cfg, w, bias=None, w_up=None, bias_up=None):
+    """w, w_up: CUDA tensors [out_features][in_features]; bias, bias_up: float32 [out_features] or None.
+    The result keeps the tensors alive."""
+    shape, dev = (cfg.out_features, cfg.in_features), w.get_device()
+    if (w_up is not None) != bool(cfg.gated) or (bias_up is not None and w_up is None):
+        _bad("w_up goes with a gated config, bias_up with w_up")
+    ld = _rows(w, "w", shape, cfg.dtype, dev)
+    ld_up = 0 if w_up is None else _rows(w_up, "w_up", shape, cfg.dtype, dev)
+    wts = MoeLinearWeights(w.data_ptr(), _ptr(w_up), None if bias is None else _vec(bias, "bias", shape[0], dev),
+                           None if bias_up is None else _vec(bias_up, "bias_up", shape[0], dev), ld, ld_up)
+    wts.kept = (w, bias, w_up, bias_up)
+    wts.made_for = (shape, cfg.dtype, cfg.gated, dev)
+    return wts
+
+
+def moe_linear_forward(cfg, wts, x, out, residual=None, stream=None):
+    """out = act(x w^T + bias) [* (x w_up^T + bias_up)] [+ residual] (see moe.h).  x [T][in], out and
+    residual [T][out]: CUDA tensors with adjacent columns; out may be residual itself."""
+    dev, st = _current()
+    T, N, K = x.shape[0], cfg.out_features, cfg.in_features
+    if wts.made_for != ((N, K), cfg.dtype, cfg.gated, dev):
+        _bad("the weights were made for another config or device")
+    ldx = _rows(x, "x", (T, K), cfg.dtype, dev)
+    ldo = _rows(out, "out", (T, N), cfg.out_dtype, dev)
+    res, ldr = None, 0
+    if residual is not None:
+        ldr = _rows(residual, "residual", (T, N), cfg.out_dtype, dev)
+        res = residual.data_ptr()
+    _check(_lib.moe_linear_forward(C.byref(cfg), C.byref(wts), x.data_ptr(), ldx, res, ldr, T, out.data_ptr(), ldo,
+                                   st if stream is None else _stream(stream)))
+
+
+def moe_linear_device_error(stream=None):
+    """Returns (status, detail) of the dense products on the current device and clears it."""
+    detail = C.c_uint32(0)
+    st = _lib.moe_linear_device_error(C.byref(detail), _stream(stream))
+    return st, detail.value
+
+
+def route_config(n_experts, top_k, score=MOE_SCORE_SOFTMAX, n_groups=1, topk_groups=1, group_score=MOE_GROUP_MAX,
+                 renormalise=True, scale=1.0):
+    return MoeRouteConfig(n_experts, top_k, score, n_groups, topk_groups, group_score, 1 if renormalise else 0, scale)
+
+
+def _route_out(cfg, T, idx, w, dev):
+    shape = (T, cfg.top_k)
+    if idx.shape != shape or w.shape != shape or not idx.is_contiguous() or not w.is_contiguous() \
+            or str(idx.dtype) != "torch.int32" or not _is_dtype(w, MOE_F32):
+        _bad("idx and w must be contiguous int32 and float32 tensors of %s" % (shape,))
+    if idx.get_device() != dev or w.get_device() != dev:
+        _bad("idx and w must be on the current CUDA device")
+
+
+def moe_route_from_logits(cfg, logits, idx, w, select_bias=None, stream=None):
+    """Expert choice (see moe.h).  logits: float32, bfloat16 or float16 CUDA tensor [T][E] with adjacent
+    columns; idx int32 [T][K], w float32 [T][K] (written)."""
+    dev, st = _current()
+    T = logits.shape[0]
+    code = MOE_F32 if _is_dtype(logits, MOE_F32) else MOE_BF16 if str(logits.dtype) == "torch.bfloat16" else MOE_F16
+    ld = _rows(logits, "logits", (T, cfg.n_experts), code, dev)
+    _route_out(cfg, T, idx, w, dev)
+    bias = None if select_bias is None else _vec(select_bias, "select_bias", cfg.n_experts, dev)
+    _check(_lib.moe_route_from_logits(C.byref(cfg), logits.data_ptr(), code, ld, bias, T, idx.data_ptr(),
+                                      w.data_ptr(), st if stream is None else _stream(stream)))
+
+
+def moe_route_workspace_bytes(cfg, T):
+    return _lib.moe_route_workspace_bytes(C.byref(cfg), int(T))
+
+
+def moe_route_topk(cfg, x, wr, idx, w, router_bias=None, select_bias=None, logits_out=None, workspace=None,
+                   stream=None):
+    """Router projection and expert choice (see moe.h).  x bf16 [T][H], wr bf16 [E][H], contiguous; the logits go
+    to logits_out (float32 [T][E]) or to the workspace."""
+    dev, st = _current()
+    T, H, E = x.shape[0], x.shape[1], cfg.n_experts
+    if not x.is_contiguous() or not wr.is_contiguous() or (logits_out is not None and not logits_out.is_contiguous()):
+        _bad("x, wr and logits_out must be contiguous")
+    _rows(x, "x", (T, H), MOE_BF16, dev)
+    _rows(wr, "wr", (E, H), MOE_BF16, dev)
+    if logits_out is not None:
+        _rows(logits_out, "logits_out", (T, E), MOE_F32, dev)
+    if workspace is not None and (workspace.get_device() != dev or not workspace.is_contiguous()):
+        _bad("workspace must be contiguous, on the current CUDA device")
+    _route_out(cfg, T, idx, w, dev)
+    rb = None if router_bias is None else _vec(router_bias, "router_bias", E, dev)
+    sb = None if select_bias is None else _vec(select_bias, "select_bias", E, dev)
+    _check(_lib.moe_route_topk(C.byref(cfg), H, x.data_ptr(), wr.data_ptr(), rb, sb, T, idx.data_ptr(), w.data_ptr(),
+                               _ptr(logits_out), _ptr(workspace), 0 if workspace is None else _nbytes(workspace),
+                               st if stream is None else _stream(stream)))
 
 
 # ---- expert-streaming tier -------------------------------------------------------

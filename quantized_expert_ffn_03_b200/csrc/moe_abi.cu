@@ -2,6 +2,7 @@
 // workspace carving and kernel launches.  See include/moe.h for the contract.
 #include <cuda_runtime.h>
 
+#include <cmath>
 #include <cstdarg>
 #include <cstdio>
 #include <cstring>
@@ -11,6 +12,7 @@
 #include "../../include/moe.h"
 #include "moe_grouped.h"
 #include "moe_kernels.h"
+#include "moe_linear.h"
 
 namespace moe {
 // The kernel's view of a device-resolved streaming cache (moe_stream.cu).
@@ -429,21 +431,23 @@ static moe_status layer_forward_chunk(const moe_config* cfg, const moe_layer_wei
   return ok();
 }
 
-// The batched path (moe_grouped.cu): router GEMM, top-K, grouping by
-// expert, grouped GEMMs for the routed experts, GEMMs for the shared expert,
+// The batched path (moe_grouped.cu): router GEMM, top-K (or the routing
+// given), grouping by expert, grouped GEMMs for the routed experts, GEMMs for the shared expert,
 // combine + residual + RMSNorm.
 static moe_status layer_forward_batched(const moe_config* cfg, const moe_layer_weights* wts, const void* x_bf16,
                                         const void* residual_bf16, int T, void* h_out_bf16, void* y_norm_bf16,
                                         int32_t* idx_out, float* w_out, void* workspace, size_t ws_bytes,
-                                        cudaStream_t stream) {
+                                        cudaStream_t stream, const int32_t* idx_in = nullptr,
+                                        const float* w_in = nullptr) {
   Layout L;
   moe_status s = check_cfg(cfg, &L);
   if (s != MOE_OK) return s;
   if (T < 0) return fail(MOE_ERR_INVALID_ARG, "T < 0");
   if (T == 0) return ok();
   if (!batched_ok(L)) return fail(MOE_ERR_UNSUPPORTED, "the batched path takes at most %d experts", kBatchedMaxExperts);
-  if (!wts || !wts->expert_ptr || !wts->router_w || !wts->gamma || !x_bf16 || !residual_bf16 || !h_out_bf16 ||
-      !y_norm_bf16)
+  const bool given = idx_in != nullptr;  // routing given: the router weights are not read
+  if (!wts || !wts->expert_ptr || (!given && !wts->router_w) || !wts->gamma || !x_bf16 || !residual_bf16 ||
+      !h_out_bf16 || !y_norm_bf16)
     return fail(MOE_ERR_INVALID_ARG, "NULL pointer");
   weight_opts(wts, &L);
   const bool bf16_shared = L.has_shared && !L.spacked;
@@ -451,7 +455,7 @@ static moe_status layer_forward_batched(const moe_config* cfg, const moe_layer_w
     return fail(MOE_ERR_INVALID_ARG, "has_shared=1 but a shared-expert pointer is NULL");
   if (L.spacked && !aligned(wts->shared_packed, 256))
     return fail(MOE_ERR_INVALID_ARG, "the packed shared expert must be 256-byte aligned");
-  const void* a16[] = {x_bf16, residual_bf16, h_out_bf16, y_norm_bf16, wts->router_w, wts->gamma,
+  const void* a16[] = {x_bf16, residual_bf16, h_out_bf16, y_norm_bf16, given ? nullptr : wts->router_w, wts->gamma,
                        bf16_shared ? wts->shared_gate : nullptr, bf16_shared ? wts->shared_up : nullptr,
                        bf16_shared ? wts->shared_down : nullptr, L.sgate ? wts->shared_out_gate : nullptr};
   for (const void* q : a16)
@@ -466,8 +470,10 @@ static moe_status layer_forward_batched(const moe_config* cfg, const moe_layer_w
   uint32_t* abort_flag = reinterpret_cast<uint32_t*>(ws) + 5;
   const int TK = T * L.K;
   const uint16_t* x = static_cast<const uint16_t*>(x_bf16);
-  int32_t* idx = idx_out ? idx_out : reinterpret_cast<int32_t*>(ws + bp.idx);
-  float* w = w_out ? w_out : reinterpret_cast<float*>(ws + bp.w);
+  int32_t* idx_made = idx_out ? idx_out : reinterpret_cast<int32_t*>(ws + bp.idx);
+  float* w_made = w_out ? w_out : reinterpret_cast<float*>(ws + bp.w);
+  const int32_t* idx = given ? idx_in : idx_made;
+  const float* w = given ? w_in : w_made;
   float* logits = reinterpret_cast<float*>(ws + bp.logits);
   int* slot_token = reinterpret_cast<int*>(ws + bp.slot_token);
   int* pair_slot = reinterpret_cast<int*>(ws + bp.pair_slot);
@@ -484,7 +490,7 @@ static moe_status layer_forward_batched(const moe_config* cfg, const moe_layer_w
   g.err = err;
   g.abort_flag = abort_flag;
   g.timeout_ns = kTimeoutNs;
-  {
+  if (!given) {
     GemmParams r = g;
     r.M = L.E;
     r.K = L.H;
@@ -495,8 +501,8 @@ static moe_status layer_forward_batched(const moe_config* cfg, const moe_layer_w
     r.bias = wts->router_bias;
     const int gr = tiles(T, L.E) < grid ? tiles(T, L.E) : grid;
     CUDA_TRY(launch_grouped_gemm(0, 1, 0, r, gr, stream));
+    CUDA_TRY(launch_topk(logits, T, L.E, L.K, idx_made, w_made, stream));
   }
-  CUDA_TRY(launch_topk(logits, T, L.E, L.K, idx, w, stream));
   CUDA_TRY(launch_group(idx, TK, L.E, L.K, slot_token, pair_slot, ch_e, ch_c0, ch_n, nch, wts->expert_ptr, err,
                         stream));
   // routed gate/up: dequantised weights x the chunk's tokens (fp16), SwiGLU -> hr
@@ -735,6 +741,15 @@ moe_status moe_layer_forward_batched(const moe_config* cfg, const moe_layer_weig
                                workspace, ws_bytes, stream);
 }
 
+moe_status moe_layer_forward_routed_batched(const moe_config* cfg, const moe_layer_weights* wts, const void* x_bf16,
+                                            const void* residual_bf16, int T, const int32_t* idx, const float* w,
+                                            void* h_out_bf16, void* y_norm_bf16, void* workspace, size_t ws_bytes,
+                                            cudaStream_t stream) {
+  if (T > 0 && (!idx || !w)) return fail(MOE_ERR_INVALID_ARG, "NULL routing");
+  return layer_forward_batched(cfg, wts, x_bf16, residual_bf16, T, h_out_bf16, y_norm_bf16, nullptr, nullptr,
+                               workspace, ws_bytes, stream, idx, w);
+}
+
 moe_status moe_layer_forward_chunked(const moe_config* cfg, const moe_layer_weights* wts,
                                      const void* x_bf16, const void* residual_bf16, int T,
                                      void* h_out_bf16, void* y_norm_bf16, int32_t* idx_out, float* w_out,
@@ -900,6 +915,154 @@ moe_status moe_selftest_bounded_wait(void* workspace, size_t ws_bytes, uint64_t 
   CUDA_TRY(launch_barrier_timeout_probe(reinterpret_cast<uint32_t*>(ws), reinterpret_cast<uint32_t*>(ws + 64),
                                         timeout_ns, stream));
   return ok();
+}
+
+// ---- dense product with its epilogue, and expert choice ------------------------------
+
+constexpr int kLinearMaxFeatures = 1 << 20;
+
+static bool is16(int dtype) { return dtype == MOE_BF16 || dtype == MOE_F16; }
+
+moe_status moe_linear_forward(const moe_linear_config* cfg, const moe_linear_weights* wts, const void* x, int64_t ldx,
+                              const void* residual, int64_t ldr, int T, void* out, int64_t ldo, cudaStream_t stream) {
+  if (!cfg) return fail(MOE_ERR_INVALID_ARG, "cfg is NULL");
+  const int K = cfg->in_features, N = cfg->out_features;
+  if (K <= 0 || N <= 0 || T < 0) return fail(MOE_ERR_INVALID_ARG, "in_features and out_features must be positive, T >= 0");
+  if (K > kLinearMaxFeatures || N > kLinearMaxFeatures)
+    return fail(MOE_ERR_UNSUPPORTED, "in_features and out_features must be <= %d", kLinearMaxFeatures);
+  if (!is16(cfg->dtype) || (cfg->out_dtype != cfg->dtype && cfg->out_dtype != MOE_F32))
+    return fail(MOE_ERR_UNSUPPORTED, "dtype must be MOE_BF16 or MOE_F16, out_dtype the same or MOE_F32");
+  if (cfg->act < MOE_ACT_NONE || cfg->act > MOE_ACT_RELU || (cfg->gated != 0 && cfg->gated != 1))
+    return fail(MOE_ERR_INVALID_ARG, "unknown act %d or gated %d", cfg->act, cfg->gated);
+  if (T == 0) return ok();
+  if (!wts || !wts->w || (cfg->gated && !wts->w_up) || !x || !out) return fail(MOE_ERR_INVALID_ARG, "NULL pointer");
+  if (!aligned(x, 16) || !aligned(wts->w, 16) || (cfg->gated && !aligned(wts->w_up, 16)))
+    return fail(MOE_ERR_INVALID_ARG, "x and the weights must be 16-byte aligned");
+  if (ldx < K || wts->ldw < K || ldx % 8 || wts->ldw % 8 || (cfg->gated && (wts->ldw_up < K || wts->ldw_up % 8)))
+    return fail(MOE_ERR_INVALID_ARG, "row strides of x and the weights must be multiples of 8 elements and >= %d", K);
+  const size_t osz = cfg->out_dtype == MOE_F32 ? 4 : 2;
+  if (ldo < N || (residual && ldr < N)) return fail(MOE_ERR_INVALID_ARG, "row strides of out and residual must be >= %d", N);
+  if (!aligned(out, osz) || !aligned(residual, osz) || !aligned(wts->bias, 4) || (cfg->gated && !aligned(wts->bias_up, 4)))
+    return fail(MOE_ERR_INVALID_ARG, "out, residual and the biases must be aligned to their elements");
+  // rows of a tensor span at most 2^40 bytes (the limit of a tensor map's stride)
+  if (ldx >= (1ll << 38) || wts->ldw >= (1ll << 38) || (cfg->gated && wts->ldw_up >= (1ll << 38)) || ldo >= (1ll << 37) ||
+      (residual && ldr >= (1ll << 37)))
+    return fail(MOE_ERR_UNSUPPORTED, "row stride too large");
+  if (out == x || out == wts->w || (cfg->gated && out == wts->w_up) || (out == residual && ldr != ldo))
+    return fail(MOE_ERR_INVALID_ARG, "out may only be the residual buffer itself, with its stride");
+  DeviceInfo di;
+  moe_status s = device_info(&di);
+  if (s != MOE_OK) return s;
+  LinearParams p = {};
+  p.T = T;
+  p.K = K;
+  p.N = N;
+  p.act = cfg->act;
+  p.out_f32 = cfg->out_dtype == MOE_F32;
+  p.x = static_cast<const uint16_t*>(x);
+  p.w = static_cast<const uint16_t*>(wts->w);
+  p.w_up = cfg->gated ? static_cast<const uint16_t*>(wts->w_up) : nullptr;
+  p.bias = wts->bias;
+  p.bias_up = cfg->gated ? wts->bias_up : nullptr;
+  p.res = residual;
+  p.out = out;
+  p.ldx = ldx;
+  p.ldw = wts->ldw;
+  p.ldw_up = wts->ldw_up;
+  p.ldr = ldr;
+  p.ldo = ldo;
+  CUDA_TRY(launch_linear(p, cfg->dtype == MOE_F16, di.sms, stream));
+  return ok();
+}
+
+moe_status moe_linear_device_error(uint32_t* detail, cudaStream_t stream) {
+  uint32_t code = 0;
+  CUDA_TRY(read_linear_error(&code, stream));
+  if (detail) *detail = code;
+  if (code == 0) return ok();
+  return fail(MOE_ERR_TIMEOUT, "a bounded device-side wait of a dense product expired");
+}
+
+static moe_status check_route(const moe_route_config* cfg) {
+  if (!cfg) return fail(MOE_ERR_INVALID_ARG, "cfg is NULL");
+  const int E = cfg->n_experts, K = cfg->top_k, G = cfg->n_groups, kg = cfg->topk_groups;
+  if (E <= 0 || K <= 0 || G <= 0 || kg <= 0)
+    return fail(MOE_ERR_INVALID_ARG, "n_experts, top_k, n_groups and topk_groups must be positive");
+  if (E > kRouteMaxExperts || K > kMaxK || G > kRouteMaxGroups)
+    return fail(MOE_ERR_UNSUPPORTED, "at most %d experts, top %d, %d groups", kRouteMaxExperts, kMaxK, kRouteMaxGroups);
+  if (E % G || kg > G || K > kg * (E / G))
+    return fail(MOE_ERR_INVALID_ARG, "%d experts in %d groups, %d kept, top %d: groups must be equal and hold top_k", E, G,
+                kg, K);
+  if ((cfg->score != MOE_SCORE_SOFTMAX && cfg->score != MOE_SCORE_SIGMOID) ||
+      (cfg->group_score != MOE_GROUP_MAX && cfg->group_score != MOE_GROUP_TOP2) ||
+      (cfg->renormalise != 0 && cfg->renormalise != 1) || !std::isfinite(cfg->scale))
+    return fail(MOE_ERR_INVALID_ARG, "unknown score, group_score or renormalise, or a scale that is not finite");
+  return MOE_OK;
+}
+
+moe_status moe_route_from_logits(const moe_route_config* cfg, const void* logits, int dtype, int64_t ldl,
+                                 const float* select_bias, int T, int32_t* idx, float* w, cudaStream_t stream) {
+  moe_status s = check_route(cfg);
+  if (s != MOE_OK) return s;
+  if (T < 0) return fail(MOE_ERR_INVALID_ARG, "T < 0");
+  if (!is16(dtype) && dtype != MOE_F32) return fail(MOE_ERR_UNSUPPORTED, "logits must be MOE_F32, MOE_BF16 or MOE_F16");
+  if (T == 0) return ok();
+  if (!logits || !idx || !w) return fail(MOE_ERR_INVALID_ARG, "NULL pointer");
+  if (ldl < cfg->n_experts) return fail(MOE_ERR_INVALID_ARG, "row stride of the logits must be >= n_experts");
+  if (!aligned(logits, dtype == MOE_F32 ? 4 : 2) || !aligned(select_bias, 4) || !aligned(idx, 4) || !aligned(w, 4))
+    return fail(MOE_ERR_INVALID_ARG, "arrays must be aligned to their elements");
+  DeviceInfo di;
+  if ((s = device_info(&di)) != MOE_OK) return s;
+  RouteParams p = {};
+  p.T = T;
+  p.E = cfg->n_experts;
+  p.K = cfg->top_k;
+  p.sigmoid = cfg->score == MOE_SCORE_SIGMOID;
+  p.n_groups = cfg->topk_groups == cfg->n_groups ? 1 : cfg->n_groups;  // all kept: no groups
+  p.topk_groups = p.n_groups == 1 ? 1 : cfg->topk_groups;
+  p.top2 = cfg->group_score == MOE_GROUP_TOP2;
+  p.renorm = cfg->renormalise;
+  p.scale = cfg->scale;
+  p.logits = logits;
+  p.ldl = ldl;
+  p.bias = select_bias;
+  p.idx = idx;
+  p.w = w;
+  CUDA_TRY(launch_route(p, dtype, di.sms, stream));
+  return ok();
+}
+
+size_t moe_route_workspace_bytes(const moe_route_config* cfg, int T) {
+  if (check_route(cfg) != MOE_OK || T < 0) return 0;
+  return (size_t)round_up_256(sizeof(float) * (size_t)T * cfg->n_experts);
+}
+
+moe_status moe_route_topk(const moe_route_config* cfg, int hidden, const void* x_bf16, const void* wr_bf16,
+                          const float* router_bias, const float* select_bias, int T, int32_t* idx, float* w,
+                          float* logits_out, void* workspace, size_t ws_bytes, cudaStream_t stream) {
+  moe_status s = check_route(cfg);
+  if (s != MOE_OK) return s;
+  if (T < 0) return fail(MOE_ERR_INVALID_ARG, "T < 0");
+  if (hidden <= 0 || hidden % 8) return fail(MOE_ERR_UNSUPPORTED, "hidden must be a positive multiple of 8");
+  if (T == 0) return ok();
+  if (!x_bf16 || !wr_bf16 || !idx || !w) return fail(MOE_ERR_INVALID_ARG, "NULL pointer");
+  if (!aligned(idx, 4) || !aligned(w, 4) || !aligned(select_bias, 4))
+    return fail(MOE_ERR_INVALID_ARG, "arrays must be aligned to their elements");
+  float* logits = logits_out;
+  if (!logits) {
+    const size_t need = moe_route_workspace_bytes(cfg, T);
+    if (!workspace || ws_bytes < need || !aligned(workspace, 16))
+      return fail(MOE_ERR_WORKSPACE, "router workspace must be 16-byte aligned and >= %zu bytes", need);
+    logits = static_cast<float*>(workspace);
+  }
+  const moe_linear_config lc = {hidden, cfg->n_experts, MOE_BF16, MOE_F32, MOE_ACT_NONE, 0};
+  moe_linear_weights lw = {};
+  lw.w = wr_bf16;
+  lw.bias = router_bias;
+  lw.ldw = hidden;
+  if ((s = moe_linear_forward(&lc, &lw, x_bf16, hidden, nullptr, 0, T, logits, cfg->n_experts, stream)) != MOE_OK)
+    return s;
+  return moe_route_from_logits(cfg, logits, MOE_F32, cfg->n_experts, select_bias, T, idx, w, stream);
 }
 
 }  // extern "C"

@@ -494,6 +494,8 @@ __global__ void __launch_bounds__(1024) group_kernel(const int32_t* __restrict__
   const int tid = threadIdx.x;
   for (int e = tid; e < E; e += blockDim.x) cnt[e] = 0, fill[e] = 0;
   __syncthreads();
+  // (an id outside [0, E), which only a routing given by the caller can hold,
+  // is the same device error)
   for (int q = tid; q < TK; q += blockDim.x) {
     const int e = idx[q];
     if (e >= 0 && e < E)
@@ -553,7 +555,10 @@ __global__ void __launch_bounds__(1024) group_kernel(const int32_t* __restrict__
   __syncthreads();
   for (int q = tid; q < TK; q += blockDim.x) {
     const int e = idx[q];
-    if (e < 0 || e >= E) continue;
+    if (e < 0 || e >= E) {
+      pair_slot[q] = 0;  // an id from the caller's routing: the combine must not follow a stale slot
+      continue;
+    }
     const int sl = off[e] + atomicAdd(&fill[e], 1);
     slot_token[sl] = q / K;
     pair_slot[q] = sl;

@@ -1,0 +1,47 @@
+// moe_linear.h -- launch parameters of the dense product with its epilogue
+// (moe_linear.cu), shared with the host code that checks the call.
+#pragma once
+
+#include <cuda_runtime.h>
+#include <stdint.h>
+
+namespace moe {
+
+// y[t][n] = act(x[t] . w[n] + bias[n]) [* (x[t] . w_up[n] + bias_up[n])] [+ res[t][n]]
+struct LinearParams {
+  int T, K, N;
+  int act;       // MOE_ACT_*
+  int out_f32;   // output (and residual) fp32, else the 16-bit input type
+  const uint16_t* x;
+  const uint16_t* w;
+  const uint16_t* w_up;  // null: not gated
+  const float* bias;
+  const float* bias_up;
+  const void* res;
+  void* out;
+  int64_t ldx, ldw, ldw_up, ldr, ldo;
+};
+
+// f16: the 16-bit type is fp16, else bf16.  sms: the device's SM count.
+cudaError_t launch_linear(const LinearParams& p, bool f16, int sms, cudaStream_t st);
+cudaError_t read_linear_error(uint32_t* code, cudaStream_t st);
+
+// Expert choice from logits (moe_route.cu).
+struct RouteParams {
+  int T, E, K;
+  int sigmoid;
+  int n_groups, topk_groups, top2;
+  int renorm;
+  float scale;
+  const void* logits;
+  int64_t ldl;
+  const float* bias;
+  int32_t* idx;
+  float* w;
+};
+constexpr int kRouteMaxExperts = 2048;
+constexpr int kRouteMaxGroups = 32;
+// dtype: MOE_BF16, MOE_F16 or MOE_F32.
+cudaError_t launch_route(const RouteParams& p, int dtype, int sms, cudaStream_t st);
+
+}  // namespace moe

@@ -1,0 +1,142 @@
+"""The routing and the dense products together with the expert layer, as a
+decoder block runs them: projection into the residual stream, choice of
+experts, a shared FFN of its own width, the routed experts; and the batched
+path under a given routing."""
+from dataclasses import replace
+
+import numpy as np
+import pytest
+
+import oracle as O
+import synth as S
+from layer_setup import (DeviceLayer, assert_outputs_close, from_dev_bits, ocfg, oracle_forward, to_dev_bits)
+
+import quantized_expert_ffn_03_b200 as M
+
+
+def routed(dl, x, res, idx, w, fn):
+    import torch
+    T = x.shape[0]
+    ws = torch.zeros(max(M.moe_layer_batched_workspace_bytes(dl.cfg, T), M.moe_layer_workspace_bytes(dl.cfg, T)),
+                     dtype=torch.uint8, device="cuda")
+    h, y = torch.full_like(x, 0x7fc0), torch.full_like(x, 0x7fc0)
+    getattr(M, fn)(dl.cfg, dl.wts, x, res, idx, w, h, y, ws)
+    torch.cuda.synchronize()
+    return h, y, M.moe_device_error(ws)[0]
+
+
+@pytest.mark.gpu
+@pytest.mark.parametrize("T,has_shared", [(1, 1), (33, 1), (150, 0)])
+def test_batched_with_given_routing_matches_oracle(T, has_shared):
+    import torch
+    s = replace(S.TINY, tokens=T, has_shared=has_shared)
+    dl = DeviceLayer(s)
+    x, res = S.activations(s, step=6)
+    r = np.random.RandomState(T)
+    idx = np.stack([r.permutation(s.n_experts)[:s.top_k] for _ in range(T)]).astype(np.int32)
+    idx[-1] = idx[-1, 0]  # one expert named twice
+    w = r.uniform(0.1, 0.9, (T, s.top_k)).astype(np.float32)
+    h, y, st = routed(dl, to_dev_bits(x), to_dev_bits(res), torch.from_numpy(idx).cuda(), torch.from_numpy(w).cuda(),
+                      "moe_layer_forward_routed_batched")
+    assert st == M.MOE_OK
+    _, _, h_ref, y_ref = oracle_forward(s, dl.oracle_blobs(), dl.dense, x, res, idx_in=idx, w_in=w.astype(np.float64))
+    assert_outputs_close(from_dev_bits(h), h_ref, "h_out")
+    assert_outputs_close(from_dev_bits(y), y_ref, "y_norm")
+
+
+@pytest.mark.gpu
+def test_batched_with_its_own_routing_is_the_batched_call():
+    """The routing that moe_layer_forward_batched finds, given back, gives its result bit for bit."""
+    import torch
+    s = replace(S.TINY, tokens=70)
+    dl = DeviceLayer(s)
+    x, res = (to_dev_bits(a) for a in S.activations(s, step=7))
+    ws = torch.zeros(M.moe_layer_batched_workspace_bytes(dl.cfg, 70), dtype=torch.uint8, device="cuda")
+    h, y = torch.empty_like(x), torch.empty_like(x)
+    idx = torch.empty((70, s.top_k), dtype=torch.int32, device="cuda")
+    w = torch.empty((70, s.top_k), device="cuda")
+    M.moe_layer_forward_batched(dl.cfg, dl.wts, x, res, h, y, idx, w, workspace=ws)
+    h2, y2, st = routed(dl, x, res, idx, w, "moe_layer_forward_routed_batched")
+    assert st == M.MOE_OK and torch.equal(h, h2) and torch.equal(y, y2)
+
+
+@pytest.mark.gpu
+def test_batched_with_a_bad_id_reports_it_and_the_next_call_is_right():
+    import torch
+    s = replace(S.TINY, tokens=40)
+    dl = DeviceLayer(s)
+    x, res = (to_dev_bits(a) for a in S.activations(s, step=8))
+    idx = torch.zeros((40, s.top_k), dtype=torch.int32, device="cuda")
+    idx[:, 1] = 3
+    w = torch.full((40, s.top_k), 0.5, device="cuda")
+    good = routed(dl, x, res, idx, w, "moe_layer_forward_routed_batched")
+    bad = idx.clone()
+    bad[5, 0], bad[7, 1], bad[9, 0] = s.n_experts, -1, 2 ** 30
+    assert routed(dl, x, res, bad, w, "moe_layer_forward_routed_batched")[2] == M.MOE_ERR_DEVICE
+    again = routed(dl, x, res, idx, w, "moe_layer_forward_routed_batched")
+    assert good[2] == again[2] == M.MOE_OK and torch.equal(good[0], again[0])
+
+
+def test_batched_routed_refusals_on_the_host():
+    import ctypes as C
+    lib, cfg = M.lib(), M.config(256, 128, 16, 2)
+    wts = M.MoeLayerWeights()
+    args = lambda idx, w: (C.byref(cfg), C.byref(wts), 16, 16, 40, idx, w, 16, 16, 256, 1 << 20, None)  # noqa: E731
+    assert lib.moe_layer_forward_routed_batched(*args(None, 16)) == 1
+    assert lib.moe_layer_forward_routed_batched(*args(16, None)) == 1
+    assert lib.moe_layer_forward_routed_batched(*args(16, 16)) == 1 and "NULL" in M.last_error()
+    assert lib.moe_layer_forward_routed_batched(C.byref(cfg), C.byref(wts), 16, 16, 0, None, None, 16, 16, 256, 0,
+                                                None) == 0
+
+
+@pytest.mark.gpu
+@pytest.mark.parametrize("T", [1, 6, 90])
+def test_a_block_around_the_layer(T):
+    """h = h0 + proj(a); experts by sigmoid with a balance bias and groups; a gated shared FFN three times as wide as
+    the experts whose sum enters as the layer's residual; the routed experts.  Every step is compared with 64 bits
+    on the device's own inputs of that step, the layer with the oracle."""
+    import torch
+    from test_linear import check, reference
+    s = replace(S.TINY, tokens=T, has_shared=0)
+    H, wide = s.hidden, 3 * s.inter
+    dl = DeviceLayer(s)
+    g = torch.Generator(device="cuda").manual_seed(T)
+    rnd = lambda *sh, std=1.0: (torch.randn(*sh, generator=g, device="cuda") * std).bfloat16()  # noqa: E731
+    a, h = rnd(T, 512), rnd(T, H)
+    wo, wr = rnd(H, 512, std=0.02), rnd(s.n_experts, H, std=0.05)
+    wg, wu, wd = rnd(wide, H, std=0.02), rnd(wide, H, std=0.02), rnd(H, wide, std=0.02)
+    # projection into the residual stream, in place
+    ref = reference(a, wo, None, "none", res=h)
+    cfg = M.linear_config(512, H)
+    M.moe_linear_forward(cfg, M.linear_weights(cfg, wo), a, h, residual=h)
+    check(h, *ref)
+    x = h
+    # choice
+    rc = M.route_config(s.n_experts, s.top_k, M.MOE_SCORE_SIGMOID, 4, 2, M.MOE_GROUP_TOP2, True, 1.5)
+    idx = torch.empty(T, s.top_k, dtype=torch.int32, device="cuda")
+    w = torch.empty(T, s.top_k, device="cuda")
+    sb = torch.randn(s.n_experts, generator=g, device="cuda") * 0.05
+    logits = torch.empty(T, s.n_experts, device="cuda")
+    M.moe_route_topk(rc, x, wr, idx, w, select_bias=sb, logits_out=logits)
+    from test_route import plain
+    wi, ww = plain(logits.double().cpu().numpy(), sb.cpu().numpy(), s.top_k, score="sigmoid", groups=4, keep=2,
+                   group_score="top2", scale=1.5)
+    assert np.array_equal(idx.cpu().numpy(), wi)
+    # shared FFN of its own width; its sum with h is the layer's residual
+    up = M.linear_config(H, wide, act=M.MOE_ACT_SILU, gated=True)
+    mid = torch.empty(T, wide, dtype=torch.bfloat16, device="cuda")
+    M.moe_linear_forward(up, M.linear_weights(up, wg, w_up=wu), x, mid)
+    check(mid, *reference(x, wg, None, "silu", wu))
+    down = M.linear_config(wide, H)
+    res = torch.empty_like(h)
+    M.moe_linear_forward(down, M.linear_weights(down, wd), mid, res, residual=h)
+    check(res, *reference(mid, wd, None, "none", res=h))
+    bits = lambda t: t.view(torch.int16)  # noqa: E731
+    fn = "moe_layer_forward_routed_batched" if T >= 32 else "moe_layer_forward_routed"
+    ho, yo, st = routed(dl, bits(x), bits(res), idx, w, fn)
+    assert st == M.MOE_OK and M.moe_linear_device_error() == (M.MOE_OK, 0)
+    _, _, h_ref, y_ref = oracle_forward(s, dl.oracle_blobs(), dl.dense, from_dev_bits(bits(x)),
+                                        from_dev_bits(bits(res)), idx_in=idx.cpu().numpy(),
+                                        w_in=w.cpu().numpy().astype(np.float64))
+    assert_outputs_close(from_dev_bits(ho), h_ref, "h_out")
+    assert_outputs_close(from_dev_bits(yo), y_ref, "y_norm")

@@ -1,0 +1,274 @@
+"""Dense product with its epilogue (moe_linear_forward) against the formula in
+64 bits.
+
+Tolerance of one output, from the arithmetic: the sums are fp32 sums of K
+exact products in some order, off by at most 2 K 2^-24 sum|x w| (twice the
+usual bound: a tensor core may truncate where fp32 rounds); an activation
+passes an error on with a slope of at most 1.13; the epilogue's own fp32
+steps and its exponential are within 2^-20 relative; the final rounding is at
+most half a step of the output type."""
+import ctypes as C
+
+import numpy as np
+import pytest
+
+import quantized_expert_ffn_03_b200 as M
+
+ACTS = {"none": M.MOE_ACT_NONE, "silu": M.MOE_ACT_SILU, "gelu": M.MOE_ACT_GELU, "gelu_tanh": M.MOE_ACT_GELU_TANH,
+        "relu": M.MOE_ACT_RELU}
+CODES = {"bf16": M.MOE_BF16, "f16": M.MOE_F16, "f32": M.MOE_F32}
+SENTINEL = 7.0
+
+
+def torch_type(name):
+    import torch
+    return {"bf16": torch.bfloat16, "f16": torch.float16, "f32": torch.float32}[name]
+
+
+def act64(v, act):
+    import torch
+    if act == "silu":
+        return v * torch.sigmoid(v)
+    if act == "gelu":
+        return v * torch.special.ndtr(v)
+    if act == "gelu_tanh":
+        return v * torch.sigmoid(2 * (2 / np.pi) ** 0.5 * (v + 0.044715 * v ** 3))
+    return torch.relu(v) if act == "relu" else v
+
+
+def reference(x, w, bias, act, wu=None, bias_u=None, res=None):
+    """(value, bound before the last rounding), both fp64 [T][N]."""
+    x, w = x.double(), w.double()
+    K = x.shape[1]
+
+    def product(m, b):
+        v, mag = x @ m.T, x.abs() @ m.abs().T
+        if b is not None:
+            v, mag = v + b.double(), mag + b.double().abs()
+        return v, 2 * (K + 1) * 2.0 ** -24 * mag
+
+    g, dg = product(w, bias)
+    y = act64(g, act)
+    dy = 1.13 * dg + 2.0 ** -20 * y.abs()
+    if wu is not None:
+        u, du = product(wu.double(), bias_u)
+        dy = dy * u.abs() + y.abs() * du + dy * du
+        y = y * u
+        dy = dy + 2.0 ** -24 * y.abs()
+    if res is not None:
+        y = y + res.double()
+        dy = dy + 2.0 ** -24 * y.abs()
+    return y, dy
+
+
+def check(out, ref, slack):
+    """Every output within its bound plus half a step of its type."""
+    import torch
+    half = torch.finfo(out.dtype).eps / 2
+    tiny = torch.finfo(out.dtype).smallest_normal * half * 2
+    err = (out.double() - ref).abs()
+    lim = slack + half * (ref.abs() + slack) + tiny
+    assert torch.isfinite(out).all()
+    worst = (err / lim).max().item()
+    assert worst <= 1.0, worst
+
+
+def make(T, K, N, dtype="bf16", out="bf16", act="none", gated=False, bias=False, res=False, pad=0, seed=0):
+    import torch
+    g = torch.Generator(device="cuda").manual_seed(1000 * seed + T + 7 * K + 13 * N)
+    dt = torch_type(dtype)
+
+    def rows(n, k, extra, std):
+        ld = (k + 7) // 8 * 8 + extra
+        buf = (torch.randn(n, ld, generator=g, device="cuda") * std).to(dt)
+        buf[:, k:] = float("nan")  # columns behind the last are never used
+        return buf[:, :k]
+
+    d = dict(x=rows(T, K, pad, 1.0), w=rows(N, K, 8 if pad else 0, 0.05), wu=None, bias=None, bias_u=None, res=None)
+    if gated:
+        d["wu"] = rows(N, K, 16 if pad else 0, 0.05)
+    if bias:
+        d["bias"] = torch.randn(N, generator=g, device="cuda") * 0.2
+        d["bias_u"] = torch.randn(N, generator=g, device="cuda") * 0.2 if gated else None
+    if res:
+        d["res"] = torch.randn(T, N, generator=g, device="cuda").to(torch_type(out))
+    d["cfg"] = M.linear_config(K, N, act=ACTS[act], gated=gated, dtype=CODES[dtype], out_dtype=CODES[out])
+    d["wts"] = M.linear_weights(d["cfg"], d["w"], d["bias"], d["wu"], d["bias_u"])
+    d["ref"] = reference(d["x"], d["w"], d["bias"], act, d["wu"], d["bias_u"], d["res"])
+    return d
+
+
+def run_guarded(d, T, N, out, ldo=None):
+    """The call on rows in the middle of a larger buffer: nothing around them changes."""
+    import torch
+    ldo = ldo or N
+    buf = torch.full((T + 4, ldo), SENTINEL, dtype=torch_type(out), device="cuda")
+    view = buf[2:2 + T, :N]
+    M.moe_linear_forward(d["cfg"], d["wts"], d["x"], view, residual=d["res"])
+    torch.cuda.synchronize()
+    assert M.moe_linear_device_error() == (M.MOE_OK, 0)
+    assert (buf[:2] == SENTINEL).all() and (buf[2 + T:] == SENTINEL).all()
+    assert (buf[:, N:] == SENTINEL).all()
+    return view
+
+
+# one token to long inputs; sizes below, at and above every tile and unit
+SHAPES = [(1, 1, 1), (1, 8, 3), (1, 4096, 512), (2, 64, 16), (3, 100, 17), (5, 4095, 33), (7, 72, 1024),
+          (8, 2048, 48), (9, 520, 129), (13, 2040, 1001), (16, 1024, 128), (17, 640, 200), (31, 96, 257),
+          (33, 4096, 130), (64, 1024, 512), (65, 1000, 96), (100, 33, 640), (127, 512, 256), (128, 128, 384),
+          (129, 768, 383), (200, 72, 520), (256, 2048, 1024), (257, 1000, 1000), (300, 4096, 64), (511, 65, 129),
+          (1025, 320, 640), (2048, 256, 2304), (4099, 136, 72)]
+
+
+@pytest.mark.gpu
+@pytest.mark.parametrize("T,K,N", SHAPES)
+@pytest.mark.parametrize("form", ["plain", "full", "gated"])
+def test_matches_formula(T, K, N, form):
+    kw = {"plain": dict(), "full": dict(dtype="f16", out="f16", act="gelu", bias=True, res=True, pad=8),
+          "gated": dict(act="silu", gated=True, bias=True, res=True)}[form]
+    d = make(T, K, N, **kw)
+    check(run_guarded(d, T, N, kw.get("out", "bf16")), *d["ref"])
+
+
+@pytest.mark.gpu
+@pytest.mark.parametrize("act", sorted(ACTS))
+@pytest.mark.parametrize("T,K,N", [(1, 256, 100), (40, 512, 264), (600, 192, 520)])
+@pytest.mark.parametrize("dtype,out", [("bf16", "bf16"), ("bf16", "f32"), ("f16", "f16"), ("f16", "f32")])
+def test_activations_and_types(act, T, K, N, dtype, out):
+    for gated in (False, True):
+        d = make(T, K, N, dtype, out, act, gated, bias=True, res=True, pad=24, seed=3)
+        check(run_guarded(d, T, N, out, ldo=N + 8), *d["ref"])  # rows on 16-byte boundaries, wider than N
+        check(run_guarded(d, T, N, out, ldo=N + 5), *d["ref"])  # rows that start anywhere
+
+
+@pytest.mark.gpu
+@pytest.mark.parametrize("T", [1, 20, 150, 1300])
+@pytest.mark.parametrize("out", ["bf16", "f32"])
+def test_residual_in_place_and_out_of_place_agree(T, out):
+    import torch
+    d = make(T, 512, 392, out=out, res=True, seed=4)
+    apart = torch.empty_like(d["res"])
+    M.moe_linear_forward(d["cfg"], d["wts"], d["x"], apart, residual=d["res"])
+    M.moe_linear_forward(d["cfg"], d["wts"], d["x"], d["res"], residual=d["res"])
+    assert torch.equal(apart, d["res"])
+    check(apart, *d["ref"])
+
+
+@pytest.mark.gpu
+@pytest.mark.parametrize("T", [1, 30, 300, 2000])
+def test_tokens_do_not_depend_on_each_other_and_runs_repeat(T):
+    """A token of NaN and one of infinities leave the others as they were; a second run gives the same bits."""
+    import torch
+    d = make(T, 768, 520, act="silu", gated=True, seed=5)
+    a = torch.empty(T, 520, dtype=torch.bfloat16, device="cuda")
+    b = torch.empty_like(a)
+    M.moe_linear_forward(d["cfg"], d["wts"], d["x"], a)
+    M.moe_linear_forward(d["cfg"], d["wts"], d["x"], b)
+    assert torch.equal(a, b)
+    bad = sorted({0, T // 2})
+    x = d["x"].clone()
+    x[bad[0]] = float("nan")
+    x[bad[-1], 5] = float("inf")
+    M.moe_linear_forward(d["cfg"], d["wts"], x, b)
+    rest = [t for t in range(T) if t not in bad]
+    assert torch.equal(a[rest], b[rest])
+    assert not torch.isfinite(b[bad].float()).all()
+
+
+@pytest.mark.gpu
+def test_zero_tokens_writes_nothing():
+    import torch
+    cfg = M.linear_config(64, 32)
+    wts = M.linear_weights(cfg, torch.ones(32, 64, dtype=torch.bfloat16, device="cuda"))
+    M.moe_linear_forward(cfg, wts, torch.empty(0, 64, dtype=torch.bfloat16, device="cuda"),
+                         torch.empty(0, 32, dtype=torch.bfloat16, device="cuda"))
+    torch.cuda.synchronize()
+
+
+@pytest.mark.gpu
+@pytest.mark.parametrize("T", [1, 48, 700])
+def test_two_streams_and_replayed_graphs(T):
+    """Calls on two streams at once, and two captured graphs replayed at once, share nothing."""
+    import torch
+    ds = [make(T, 1024, 640, act="gelu_tanh", bias=True, seed=s) for s in (6, 7)]
+    want = []
+    for d in ds:
+        o = torch.empty(T, 640, dtype=torch.bfloat16, device="cuda")
+        M.moe_linear_forward(d["cfg"], d["wts"], d["x"], o)
+        want.append(o)
+    torch.cuda.synchronize()
+    streams = [torch.cuda.Stream() for _ in ds]
+    got = [torch.zeros_like(o) for o in want]
+    for _ in range(20):
+        for d, o, st in zip(ds, got, streams):
+            M.moe_linear_forward(d["cfg"], d["wts"], d["x"], o, stream=st)
+    torch.cuda.synchronize()
+    assert all(torch.equal(a, b) for a, b in zip(want, got))
+    graphs = []
+    for d, o, st in zip(ds, got, streams):
+        o.zero_()
+        g = torch.cuda.CUDAGraph()
+        torch.cuda.synchronize()
+        with torch.cuda.graph(g, stream=st):
+            M.moe_linear_forward(d["cfg"], d["wts"], d["x"], o)
+        graphs.append(g)
+    for _ in range(20):
+        for g, st in zip(graphs, streams):
+            with torch.cuda.stream(st):
+                g.replay()
+    torch.cuda.synchronize()
+    assert all(torch.equal(a, b) for a, b in zip(want, got))
+    assert M.moe_linear_device_error() == (M.MOE_OK, 0)
+
+
+@pytest.mark.gpu
+def test_binding_refuses_wrong_tensors():
+    import torch
+    bf = dict(dtype=torch.bfloat16, device="cuda")
+    cfg = M.linear_config(64, 32)
+    w, x, out = torch.ones(32, 64, **bf), torch.ones(4, 64, **bf), torch.zeros(4, 32, **bf)
+    wts = M.linear_weights(cfg, w)
+    M.moe_linear_forward(cfg, wts, x, out)
+    bad = [dict(x=x.float()), dict(x=x[:, :56]), dict(x=torch.ones(64, 4, **bf).T), dict(x=x.cpu()),
+           dict(out=out[:3]), dict(out=out.float()), dict(residual=torch.zeros(4, 31, **bf)),
+           dict(x=torch.ones(4, 65, **bf)[:, 1:]), dict(x=torch.ones(4, 68, **bf)[:, :64]),
+           dict(out=x[:, :32]), dict(residual=torch.zeros(1, 32, **bf).expand(4, 32)),
+           dict(out=torch.zeros(1, 32, **bf).expand(4, 32))]
+    for kw in bad:
+        args = dict(x=x, out=out, residual=None, **{})
+        args.update(kw)
+        with pytest.raises(M.MoeError) as e:
+            M.moe_linear_forward(cfg, wts, args["x"], args["out"], residual=args["residual"])
+        assert e.value.status == M.MOE_ERR_INVALID_ARG, kw
+    for kw in (dict(w_up=w), dict(bias=torch.zeros(31, device="cuda")), dict(bias_up=torch.zeros(32, device="cuda"))):
+        with pytest.raises(M.MoeError):
+            M.linear_weights(cfg, w, **kw)
+    with pytest.raises(M.MoeError):  # weights made for another config
+        M.moe_linear_forward(M.linear_config(64, 32, gated=True), wts, x, out)
+
+
+def test_refusals_on_the_host():
+    """Every bad argument is refused before any device work."""
+    lib = M.lib()
+
+    def call(cfg, w=16, w_up=None, bias=None, ldw=64, ldw_up=0, x=1024, ldx=64, res=None, ldr=0, T=4, out=4096, ldo=32,
+             bias_up=None):
+        wts = M.MoeLinearWeights(w, w_up, bias, bias_up, ldw, ldw_up)
+        return lib.moe_linear_forward(C.byref(cfg), C.byref(wts), x, ldx, res, ldr, T, out, ldo, None)
+
+    good = M.linear_config(64, 32)
+    assert call(good, T=0) == 0
+    for cfg, status in [(M.linear_config(0, 32), 1), (M.linear_config(64, -1), 1), (M.linear_config(64, 32, act=9), 1),
+                        (M.linear_config(64, 32, dtype=M.MOE_F32), 2),
+                        (M.linear_config(64, 32, out_dtype=M.MOE_F16), 2), (M.linear_config(64, 1 << 21), 2),
+                        (M.linear_config(64, 32, gated=True), 1)]:
+        assert call(cfg) == status, (cfg.in_features, cfg.out_features)
+    for kw in [dict(T=-1), dict(x=None), dict(w=None), dict(out=None), dict(x=1032), dict(w=8), dict(ldx=60),
+               dict(ldx=68), dict(ldw=63), dict(ldw=72 + 4), dict(ldo=31), dict(out=4097), dict(res=4096, ldr=31),
+               dict(res=4096, ldr=40), dict(res=4099, ldr=32), dict(bias=18), dict(out=1024)]:
+        assert call(good, **kw) == 1, kw
+        assert M.last_error()
+    assert call(good, ldx=1 << 40) == 2
+    gated = M.linear_config(64, 32, gated=True)
+    assert call(gated, w_up=24, ldw_up=64) == 1 and call(gated, w_up=32, ldw_up=60) == 1
+    assert lib.moe_linear_forward(None, None, None, 0, None, 0, 0, None, 0, None) == 1

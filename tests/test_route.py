@@ -1,0 +1,267 @@
+"""Expert choice (moe_route_from_logits, moe_route_topk) against the rules in
+64 bits, written as plain loops.
+
+The choice is exact: values are compared in fp64 on both sides, and the
+random inputs leave no two values within 1e-12 of each other unless the
+logits are equal (then the rule is the lower index).  A weight is an fp64
+value rounded to fp32 after one fp64 product: off by at most 2^-24 relative
+plus fp64 noise; the tests allow 2^-23.  Ties and near ties of the projected
+logits (moe_route_topk) are compared on the logits that the call returns."""
+import ctypes as C
+import math
+
+import numpy as np
+import pytest
+
+import quantized_expert_ffn_03_b200 as M
+
+SCORES = {"softmax": M.MOE_SCORE_SOFTMAX, "sigmoid": M.MOE_SCORE_SIGMOID}
+GROUPS = {"max": M.MOE_GROUP_MAX, "top2": M.MOE_GROUP_TOP2}
+RTOL = 2.0 ** -23
+
+
+def plain(logits, bias, K, score="softmax", groups=1, keep=1, group_score="max", renorm=True, scale=1.0):
+    """logits fp64 [T][E] (already the values of their type); bias fp32 [E] or None."""
+    T, E = logits.shape
+    per = E // groups
+    idx, w = np.zeros((T, K), np.int32), np.zeros((T, K))
+    for t in range(T):
+        l = np.where(np.isnan(logits[t]), -np.inf, np.minimum(logits[t], float(np.finfo(np.float32).max)))
+        with np.errstate(over="ignore"):
+            if score == "sigmoid":
+                s = 1.0 / (1.0 + np.exp(-l))
+            else:
+                p = np.exp(l - l.max()) if np.isfinite(l.max()) else np.zeros(E)
+                s = p / p.sum() if p.sum() > 0 else p
+        with np.errstate(invalid="ignore"):
+            v = s if bias is None else s + bias.astype(np.float64)
+        v = np.where(np.isnan(v), -np.inf, v)
+        order_by = l if bias is None else v
+        if groups > 1 and keep < groups:
+            val = []
+            for g in range(groups):
+                m = sorted(v[g * per:(g + 1) * per], reverse=True)
+                val.append(m[0] + m[1] if group_score == "top2" and per > 1 else m[0])
+            kept = sorted(range(groups), key=lambda g: (-val[g], g))[:keep]
+        else:
+            kept = range(groups)
+        cand = [e for g in kept for e in range(g * per, (g + 1) * per)]
+        chosen = sorted(cand, key=lambda e: (-order_by[e], e))[:K]
+        idx[t] = chosen
+        c = s[chosen]
+        if renorm:
+            c = c / c.sum() if c.sum() > 0 else np.zeros(K)
+        w[t] = c * float(np.float32(scale))
+    return idx, w
+
+
+def run(logits, K, bias=None, score="softmax", groups=1, keep=1, group_score="max", renorm=True, scale=1.0):
+    import torch
+    T, E = logits.shape
+    cfg = M.route_config(E, K, SCORES[score], groups, keep, GROUPS[group_score], renorm, scale)
+    idx = torch.full((T + 1, K), -7, dtype=torch.int32, device="cuda")
+    w = torch.full((T + 1, K), -7.0, device="cuda")
+    b = None if bias is None else torch.from_numpy(bias).cuda()
+    M.moe_route_from_logits(cfg, logits, idx[:T], w[:T], select_bias=b)
+    torch.cuda.synchronize()
+    assert (idx[T] == -7).all() and (w[T] == -7).all()
+    return idx[:T].cpu().numpy(), w[:T].cpu().numpy().astype(np.float64)
+
+
+def check(logits, K, bias=None, **kw):
+    gi, gw = run(logits, K, bias, **kw)
+    wi, ww = plain(logits.double().cpu().numpy(), bias, K, **kw)
+    assert np.array_equal(gi, wi)
+    assert np.isfinite(gw).all()
+    np.testing.assert_allclose(gw, ww, rtol=RTOL, atol=2.0 ** -149)
+
+
+def draw(T, E, seed, dtype="f32", pad=0, std=1.3):
+    import torch
+    g = torch.Generator(device="cuda").manual_seed(seed)
+    dt = {"f32": torch.float32, "bf16": torch.bfloat16, "f16": torch.float16}[dtype]
+    return (torch.randn(T, E + pad, generator=g, device="cuda") * std).to(dt)[:, :E]
+
+
+def bias_of(E, seed, off=0):
+    r = np.random.RandomState(seed)
+    b = (0.05 * r.standard_normal(E)).astype(np.float32)
+    b[r.permutation(E)[:off]] = -np.inf
+    return b
+
+
+CASES = [  # T, E, K, groups, keep
+    (1, 1, 1, 1, 1), (1, 8, 8, 1, 1), (1, 512, 4, 1, 1), (3, 33, 5, 1, 1), (5, 512, 10, 16, 4), (7, 60, 6, 4, 2),
+    (65, 256, 8, 8, 4), (9, 96, 8, 32, 5), (4, 31, 7, 31, 9), (130, 1000, 16, 1, 1), (17, 1024, 32, 16, 3),
+    (6, 2048, 32, 32, 7), (2, 1999, 3, 1, 1), (700, 128, 2, 4, 4)]
+
+
+@pytest.mark.gpu
+@pytest.mark.parametrize("T,E,K,groups,keep", CASES)
+@pytest.mark.parametrize("score", ["softmax", "sigmoid"])
+@pytest.mark.parametrize("dtype", ["f32", "bf16", "f16"])
+def test_matches_rules(T, E, K, groups, keep, score, dtype):
+    logits = draw(T, E, T + E + K, dtype, pad=3 if T > 4 else 0)
+    for group_score in ("max", "top2") if groups > 1 else ("max",):
+        for bias in (None, bias_of(E, E, off=E // 9)):
+            check(logits, K, bias, score=score, groups=groups, keep=keep, group_score=group_score)
+            check(logits, K, bias, score=score, groups=groups, keep=keep, group_score=group_score, renorm=False,
+                  scale=2.5)
+
+
+@pytest.mark.gpu
+@pytest.mark.parametrize("score", ["softmax", "sigmoid"])
+@pytest.mark.parametrize("groups,keep", [(1, 1), (8, 2)])
+def test_ties_go_to_the_lower_index(score, groups, keep):
+    """Equal logits, zeros of both signs, and two values one fp32 rounding apart (their fp32 sigmoids are equal)."""
+    import torch
+    l = torch.zeros(5, 64, device="cuda")
+    l[1, ::2] = -0.0
+    l[2] = draw(1, 64, 1).round()[0]
+    l[3, :] = 9.0
+    l[3, 63] = float(np.nextafter(np.float32(9.0), np.float32(10.0)))
+    l[4, 5:] = -3e38
+    for bias in (None, np.zeros(64, np.float32)):
+        for gs in ("max", "top2"):
+            check(l, 6, bias, score=score, groups=groups, keep=keep, group_score=gs)
+
+
+@pytest.mark.gpu
+@pytest.mark.parametrize("score", ["softmax", "sigmoid"])
+@pytest.mark.parametrize("renorm", [True, False])
+@pytest.mark.parametrize("groups,keep", [(1, 1), (6, 2)])
+def test_masked_and_non_finite_rows(score, renorm, groups, keep):
+    """A row with nothing left, with one expert left, of lowest values, with NaN, with infinities."""
+    import torch
+    inf = float("inf")
+    l = draw(8, 48, 9)
+    l[0] = -inf
+    l[1] = -inf
+    l[1, 40] = 0.5
+    l[2] = torch.finfo(torch.float32).min
+    l[3, ::3] = float("nan")
+    l[4] = float("nan")
+    l[5, 7] = inf
+    l[5, 30] = inf
+    l[6, 3:] = -inf
+    l[7, 0] = 1e30
+    off = np.zeros(48, np.float32)
+    off[10:44] = -np.inf
+    nan = np.zeros(48, np.float32)
+    nan[2] = np.nan
+    for bias in (None, bias_of(48, 3), off, nan, np.full(48, -np.inf, np.float32)):
+        for gs in ("max", "top2"):
+            check(l, 5, bias, score=score, renorm=renorm, groups=groups, keep=keep, group_score=gs, scale=1.5)
+
+
+@pytest.mark.gpu
+def test_graph_replay_and_other_stream():
+    import torch
+    l = draw(40, 256, 11)
+    cfg = M.route_config(256, 8, M.MOE_SCORE_SIGMOID, 8, 4, M.MOE_GROUP_TOP2)
+    want_i, want_w = torch.empty(40, 8, dtype=torch.int32, device="cuda"), torch.empty(40, 8, device="cuda")
+    M.moe_route_from_logits(cfg, l, want_i, want_w)
+    torch.cuda.synchronize()
+    i, w = torch.zeros_like(want_i), torch.zeros_like(want_w)
+    st = torch.cuda.Stream()
+    M.moe_route_from_logits(cfg, l, i, w, stream=st)
+    torch.cuda.synchronize()
+    assert torch.equal(i, want_i) and torch.equal(w, want_w)
+    g = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(g):
+        M.moe_route_from_logits(cfg, l, i, w)
+    i.zero_(), w.zero_()
+    g.replay()
+    torch.cuda.synchronize()
+    assert torch.equal(i, want_i) and torch.equal(w, want_w)
+
+
+@pytest.mark.gpu
+@pytest.mark.parametrize("T,H,E", [(1, 4096, 512), (5, 264, 60), (200, 1024, 256)])
+@pytest.mark.parametrize("into", ["logits_out", "workspace"])
+def test_projection_and_choice(T, H, E, into):
+    """moe_route_topk: logits within the fp32 summation bound, the choice exact on them."""
+    import torch
+    g = torch.Generator(device="cuda").manual_seed(T + H)
+    x = torch.randn(T, H, generator=g, device="cuda").bfloat16()
+    wr = (torch.randn(E, H, generator=g, device="cuda") * 0.02).bfloat16()
+    rb, sb = torch.randn(E, generator=g, device="cuda") * 0.1, torch.from_numpy(bias_of(E, 5)).cuda()
+    cfg = M.route_config(E, 4, M.MOE_SCORE_SIGMOID, 4, 2, M.MOE_GROUP_TOP2, True, 1.5)
+    idx, w = torch.empty(T, 4, dtype=torch.int32, device="cuda"), torch.empty(T, 4, device="cuda")
+    kw = {}
+    buf = torch.empty(M.moe_route_workspace_bytes(cfg, T), dtype=torch.uint8, device="cuda")
+    logits = buf[:4 * T * E].view(torch.float32).view(T, E) if into == "workspace" else \
+        torch.empty(T, E, device="cuda")
+    kw[into] = buf if into == "workspace" else logits
+    M.moe_route_topk(cfg, x, wr, idx, w, router_bias=rb, select_bias=sb, **kw)
+    torch.cuda.synchronize()
+    ref = x.double() @ wr.double().T + rb.double()
+    lim = 2 * (H + 1) * 2.0 ** -24 * (x.double().abs() @ wr.double().abs().T + rb.double().abs())
+    assert ((logits.double() - ref).abs() <= lim).all()
+    wi, ww = plain(logits.double().cpu().numpy(), sb.cpu().numpy(), 4, score="sigmoid", groups=4, keep=2,
+                   group_score="top2", scale=1.5)
+    assert np.array_equal(idx.cpu().numpy(), wi)
+    np.testing.assert_allclose(w.cpu().numpy(), ww, rtol=RTOL)
+
+
+@pytest.mark.gpu
+def test_softmax_choice_is_the_routers():
+    """Softmax, no groups, renormalised: the choice of moe_topk_from_logits, its weights to fp32 rounding."""
+    import torch
+    l = draw(33, 512, 21).contiguous()
+    idx, w = torch.empty(33, 4, dtype=torch.int32, device="cuda"), torch.empty(33, 4, device="cuda")
+    M.moe_topk_from_logits(M.config(4096, 1024, 512, 4), l, idx, w)
+    gi, gw = run(l, 4)
+    assert np.array_equal(gi, idx.cpu().numpy())
+    # the router's fp32 exp (2 ulp), sum of 4 and division: under 16 roundings of 2^-24
+    np.testing.assert_allclose(gw, w.cpu().numpy().astype(np.float64), rtol=16 * 2.0 ** -24)
+
+
+@pytest.mark.gpu
+def test_binding_refuses_wrong_tensors():
+    import torch
+    cfg = M.route_config(64, 4)
+    l, idx, w = torch.zeros(3, 64, device="cuda"), torch.zeros(3, 4, dtype=torch.int32, device="cuda"), \
+        torch.zeros(3, 4, device="cuda")
+    M.moe_route_from_logits(cfg, l, idx, w)
+    for a in [(l[:, :60], idx, w), (l.double(), idx, w), (l.cpu(), idx, w), (l, idx.long(), w), (l, idx[:2], w),
+              (l, idx, w.half()), (torch.zeros(64, 3, device="cuda").T, idx, w),
+              (torch.zeros(1, 64, device="cuda").expand(3, 64), idx, w)]:
+        with pytest.raises(M.MoeError) as e:
+            M.moe_route_from_logits(cfg, *a)
+        assert e.value.status == M.MOE_ERR_INVALID_ARG
+    with pytest.raises(M.MoeError):
+        M.moe_route_from_logits(cfg, l, idx, w, select_bias=torch.zeros(63, device="cuda"))
+
+
+def test_refusals_on_the_host():
+    lib = M.lib()
+
+    def call(cfg, logits=16, dtype=M.MOE_F32, ldl=64, bias=None, T=2, idx=32, w=48):
+        return lib.moe_route_from_logits(C.byref(cfg), logits, dtype, ldl, bias, T, idx, w, None)
+
+    good = M.route_config(64, 4, n_groups=8, topk_groups=2)
+    assert call(good, T=0) == 0
+    for cfg, status in [(M.route_config(0, 1), 1), (M.route_config(64, 0), 1), (M.route_config(64, 33), 2),
+                        (M.route_config(4096, 4), 2), (M.route_config(64, 4, n_groups=64, topk_groups=8), 2),
+                        (M.route_config(64, 4, n_groups=7, topk_groups=2), 1),
+                        (M.route_config(64, 4, n_groups=8, topk_groups=9), 1),
+                        (M.route_config(64, 17, n_groups=8, topk_groups=2), 1), (M.route_config(4, 5), 1),
+                        (M.route_config(64, 4, score=2), 1), (M.route_config(64, 4, group_score=5), 1),
+                        (M.route_config(64, 4, scale=math.inf), 1), (M.route_config(64, 4, scale=math.nan), 1)]:
+        assert call(cfg) == status, (cfg.n_experts, cfg.top_k, cfg.n_groups)
+        assert M.last_error()
+        if status == 1:
+            assert M.moe_route_workspace_bytes(cfg, 4) == 0
+    for kw in [dict(T=-1), dict(logits=None), dict(idx=None), dict(w=None), dict(ldl=63), dict(logits=18),
+               dict(bias=2), dict(idx=33), dict(w=50)]:
+        assert call(good, **kw) == 1, kw
+    assert call(good, dtype=7) == 2
+    assert M.moe_route_workspace_bytes(good, 3) == 768
+
+    def topk(cfg, hidden=64, x=1024, wr=2048, T=2, idx=32, w=48, lo=None, ws=4096, nb=1 << 20):
+        return lib.moe_route_topk(C.byref(cfg), hidden, x, wr, None, None, T, idx, w, lo, ws, nb, None)
+
+    assert topk(good, T=0) == 0
+    assert topk(good, hidden=60) == 2 and topk(good, x=None) == 1 and topk(good, x=1032) == 1
+    assert topk(good, ws=None) == M.MOE_ERR_WORKSPACE and topk(good, nb=100) == M.MOE_ERR_WORKSPACE
