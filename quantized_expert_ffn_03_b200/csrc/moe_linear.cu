@@ -1,15 +1,33 @@
 // moe_linear.cu -- dense product with its epilogue (moe_linear_forward):
 //   y[t][n] = act(x[t] . w[n] + bias[n]) [* (x[t] . w_up[n] + bias_up[n])] [+ res[t][n]]
 // fp32 accumulation and epilogue, one rounding to the output type.
+//
+// Three kernels, one per regime of T (choose_* below):
+//   rows   few tokens: the weights stream once through registers into
+//          m16n8k16 steps (HBM bound);
+//   split  up to a few hundred tokens: 128 features x all tokens per cluster,
+//          TMA -> tcgen05, K split over the cluster's CTAs and joined through
+//          distributed shared memory (HBM / L2 bound);
+//   pair   many tokens: persistent pairs of CTAs, 256-token tiles, tcgen05
+//          with both CTAs' operands, epilogue under the next tile's MMAs
+//          (tensor bound).
+#include <cuda.h>
 #include <cuda_bf16.h>
 #include <cuda_fp16.h>
 
 #include "../../include/moe.h"
+#include "moe_device.cuh"
 #include "moe_linear.h"
+#include "moe_tc.cuh"
 
 namespace moe {
 
+// The error word of the calls on a device: the first expired wait's code.
+__device__ uint32_t g_linear_err;
+
 namespace {
+
+constexpr unsigned kAll = 0xffffffffu;
 
 // ---- epilogue arithmetic ------------------------------------------------------------
 
@@ -154,28 +172,571 @@ __global__ void __launch_bounds__(32 * kRowsWarps) linear_rows_kernel(const Line
   }
 }
 
-}  // namespace
+// ---- bounded waits ------------------------------------------------------------------
 
-cudaError_t launch_linear(const LinearParams& p, bool f16, int sms, cudaStream_t st) {
-  (void)sms;
-  const int ntt = (p.T + kRowsTok - 1) / kRowsTok;
-  const dim3 grid((p.N + kRowsFeat - 1) / kRowsFeat, ntt < 65535 ? ntt : 65535);
-  if (p.w_up) {
-    if (f16)
-      linear_rows_kernel<true, true><<<grid, 32 * kRowsWarps, 0, st>>>(p);
-    else
-      linear_rows_kernel<false, true><<<grid, 32 * kRowsWarps, 0, st>>>(p);
-  } else {
-    if (f16)
-      linear_rows_kernel<true, false><<<grid, 32 * kRowsWarps, 0, st>>>(p);
-    else
-      linear_rows_kernel<false, false><<<grid, 32 * kRowsWarps, 0, st>>>(p);
+constexpr uint64_t kLinearTimeoutNs = 2000000000ull;  // 2 s per wait
+
+__device__ __forceinline__ bool bar_try(uint32_t bar, uint32_t parity) {
+  uint32_t ok;
+  asm volatile(
+      "{\n .reg .pred p;\n mbarrier.try_wait.parity.acquire.cluster.shared::cta.b64 p, [%1], %2;\n"
+      " selp.u32 %0, 1, 0, p;\n}"
+      : "=r"(ok)
+      : "r"(bar), "r"(parity)
+      : "memory");
+  return ok != 0;
+}
+__device__ __noinline__ bool bar_wait_slow(uint32_t bar, uint32_t parity) {
+  const uint64_t t0 = globaltimer_ns();
+  for (uint32_t it = 1;; ++it) {
+    if (bar_try(bar, parity)) return true;
+    if ((it & 63u) == 0u && globaltimer_ns() - t0 > kLinearTimeoutNs) {
+      atomicCAS(&g_linear_err, 0u, 1u);
+      return false;
+    }
   }
+}
+// Waits for phase `parity` of an mbarrier; false (and the error word set) on timeout.
+__device__ __forceinline__ bool bar_wait(uint32_t bar, uint32_t parity) {
+  return bar_try(bar, parity) || bar_wait_slow(bar, parity);
+}
+// After a wait has expired: time for copies and MMAs already issued to end
+// before the block leaves its shared memory and TMEM.
+__device__ __noinline__ void let_issued_work_end() {
+  const uint64_t t0 = globaltimer_ns();
+  for (int i = 0; i < 100000 && globaltimer_ns() - t0 < 5000000ull; ++i) __nanosleep(1000);
+}
+__device__ __forceinline__ void bar_init(uint32_t a, uint32_t n) {
+  asm volatile("mbarrier.init.shared::cta.b64 [%0], %1;" ::"r"(a), "r"(n) : "memory");
+}
+__device__ __forceinline__ void bar_expect(uint32_t a, uint32_t bytes) {
+  asm volatile("mbarrier.arrive.expect_tx.shared::cta.b64 _, [%0], %1;" ::"r"(a), "r"(bytes) : "memory");
+}
+__device__ __forceinline__ void sts_f4(uint32_t a, float x, float y, float z, float w) {
+  asm volatile("st.shared.v4.f32 [%0], {%1,%2,%3,%4};" ::"r"(a), "f"(x), "f"(y), "f"(z), "f"(w) : "memory");
+}
+__device__ __forceinline__ float4 lds_f4(uint32_t a) {
+  float4 v;
+  asm volatile("ld.shared.v4.f32 {%0,%1,%2,%3}, [%4];" : "=f"(v.x), "=f"(v.y), "=f"(v.z), "=f"(v.w) : "r"(a) : "memory");
+  return v;
+}
+
+constexpr int kKB = 64;                  // columns of K per stage: 128 bytes, one swizzle row
+constexpr uint32_t kTile = 128u * 128u;  // bytes of a 128-row operand tile of one stage
+
+// ---- some tokens: a cluster per 128 features, K split over its CTAs --------------------
+// The weights are the A operand (128 features), NT tokens the B operand: with
+// T < 128 no MMA row is wasted, and an output row of the accumulator is a
+// feature, so a warp's loads and stores of out and residual are contiguous.
+// Each CTA of the cluster takes a range of K; its accumulators go to its own
+// shared memory as fp32, and after a cluster barrier each CTA sums its share
+// of the outputs over the cluster in rank order and finishes them.  Nothing
+// is exchanged through global memory, so no workspace, and calls on several
+// streams share nothing.
+constexpr int kSplitThreads = 192;  // 4 warps read TMEM, one loads, one issues MMAs
+constexpr uint32_t kSplitSmem = 220u * 1024u;
+
+__host__ __device__ constexpr uint32_t split_stage(int nt, int na) { return na * kTile + (uint32_t)nt * 128u; }
+__host__ __device__ constexpr int split_stages(int nt, int na) {
+  return (int)(kSplitSmem / split_stage(nt, na)) < 12 ? (int)(kSplitSmem / split_stage(nt, na)) : 12;
+}
+__host__ __device__ constexpr uint32_t tmem_cols(int need) {
+  return need <= 32 ? 32 : need <= 64 ? 64 : need <= 128 ? 128 : need <= 256 ? 256 : 512;
+}
+
+template <bool F16, bool GATED, int NT>
+__global__ void __launch_bounds__(kSplitThreads, 1)
+    linear_split_kernel(const __grid_constant__ CUtensorMap map_w, const __grid_constant__ CUtensorMap map_u,
+                        const __grid_constant__ CUtensorMap map_x, const LinearParams p) {
+  constexpr int NA = GATED ? 2 : 1;
+  constexpr int ST = split_stages(NT, NA);
+  constexpr uint32_t kStage = split_stage(NT, NA);
+  static_assert((uint32_t)NA * NT * 512u <= ST * kStage, "the partial sums reuse the stages");
+  extern __shared__ uint8_t smem_raw[];
+  __shared__ __align__(8) uint64_t bars[2 * ST + 1];
+  __shared__ uint32_t tmem_slot;
+  const uint32_t s0 = (smem_u32(smem_raw) + 1023u) & ~1023u;
+  const uint32_t full = smem_u32(bars), empty = full + 8u * ST, accfull = empty + 8u * ST;
+  const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
+  const uint32_t rank = tc::cluster_rank(), S = gridDim.x;  // the cluster spans x
+  const int n0 = blockIdx.y * 128, t0 = blockIdx.z * NT;
+  const int KB = (p.K + kKB - 1) / kKB;
+  const int kb0 = (int)((int64_t)KB * rank / S), kb1 = (int)((int64_t)KB * (rank + 1) / S);
+
+  if (tid == 0) {
+    for (int s = 0; s < ST; ++s) bar_init(full + 8u * s, 1), bar_init(empty + 8u * s, 1);
+    bar_init(accfull, 1);
+    mbar_fence_init();
+  }
+  if (warp == 5) {
+    tc::tmem_alloc(smem_u32(&tmem_slot), tmem_cols(NA * NT));
+    tc::tmem_relinquish();
+  }
+  tc::fence_before_sync();
+  __syncthreads();
+  tc::fence_after_sync();
+  const uint32_t tmem = tmem_slot;
+
+  if (warp == 4) {
+    if (lane == 0) {
+      bool ok = true;
+#pragma unroll 1
+      for (int kb = kb0; kb < kb1 && ok; ++kb) {
+        const int i = kb - kb0, s = i % ST;
+        if (i >= ST) ok = bar_wait(empty + 8u * s, (uint32_t)(i / ST - 1) & 1u);
+        if (!ok) break;
+        const uint32_t st = s0 + (uint32_t)s * kStage;
+        bar_expect(full + 8u * s, kStage);
+        tc::tma_2d(st, &map_w, kb * kKB, n0, full + 8u * s);
+        if constexpr (GATED) tc::tma_2d(st + kTile, &map_u, kb * kKB, n0, full + 8u * s);
+        tc::tma_2d(st + NA * kTile, &map_x, kb * kKB, t0, full + 8u * s);
+      }
+      if (!ok) let_issued_work_end();
+    }
+  } else if (warp == 5) {
+    if (lane == 0) {
+      constexpr uint32_t idesc = tc::idesc_f16(128, NT, !F16);
+      bool ok = true;
+#pragma unroll 1
+      for (int kb = kb0; kb < kb1 && ok; ++kb) {
+        const int i = kb - kb0, s = i % ST;
+        ok = bar_wait(full + 8u * s, (uint32_t)(i / ST) & 1u);
+        if (!ok) break;
+        tc::fence_after_sync();
+        const uint32_t st = s0 + (uint32_t)s * kStage;
+#pragma unroll
+        for (int k = 0; k < 4; ++k) {
+          const uint64_t bd = tc::smem_desc_sw128(st + NA * kTile + 32u * k);
+#pragma unroll
+          for (int a = 0; a < NA; ++a)
+            tc::mma_f16_ss(tmem + (uint32_t)(a * NT), tc::smem_desc_sw128(st + a * kTile + 32u * k), bd, idesc,
+                           (i > 0 || k > 0) ? 1u : 0u);
+        }
+        tc::commit(empty + 8u * s);
+      }
+      if (ok)
+        tc::commit(accfull);
+      else
+        let_issued_work_end();
+    }
+  } else {
+    // partial sums: [matrix][token][feature] fp32 over the stages, which the
+    // completed MMAs no longer read
+    const bool ok = __all_sync(kAll, bar_wait(accfull, 0));
+    tc::fence_after_sync();
+    const uint32_t dst = s0 + 4u * (uint32_t)(32 * warp + lane);
+    if (ok) {
+#pragma unroll 1
+      for (int j = 0; j < NA * NT; j += 16) {
+        uint32_t v[16];
+        tc::ld_32x32b_x16(tmem + ((uint32_t)(32 * warp) << 16) + (uint32_t)j, v);
+        tc::wait_ld();
+#pragma unroll
+        for (int q = 0; q < 16; ++q)
+          asm volatile("st.shared.b32 [%0], %1;" ::"r"(dst + 512u * (uint32_t)(j + q)), "r"(v[q]) : "memory");
+      }
+    }
+    tc::fence_before_sync();
+  }
+  __syncwarp();
+  tc::cluster_arrive();
+  tc::cluster_wait();
+  tc::fence_after_sync();
+  if (warp == 5) tc::tmem_dealloc(tmem, tmem_cols(NA * NT));
+
+  // this CTA's share of the outputs: items of 4 adjacent features of a token
+  const int nt = min(NT, p.T - t0), items = nt * 32;
+  const int i0 = (int)((int64_t)items * rank / S), i1 = (int)((int64_t)items * (rank + 1) / S);
+#pragma unroll 1
+  for (int i = i0 + tid; i < i1; i += kSplitThreads) {
+    const int c = i >> 5, f = 4 * (i & 31);
+    float4 v[2] = {};
+#pragma unroll
+    for (int a = 0; a < NA; ++a) {
+      const uint32_t src = s0 + 512u * (uint32_t)(a * NT + c) + 4u * (uint32_t)f;
+#pragma unroll 1
+      for (uint32_t r = 0; r < S; ++r) {
+        const float4 q = tc::ld_cluster_f4(tc::map_rank(src, r));
+        v[a].x += q.x, v[a].y += q.y, v[a].z += q.z, v[a].w += q.w;
+      }
+    }
+    const int n = n0 + f, t = t0 + c;
+    if (n < p.N) finish_one<F16>(p, t, n, v[0].x, v[1].x);
+    if (n + 1 < p.N) finish_one<F16>(p, t, n + 1, v[0].y, v[1].y);
+    if (n + 2 < p.N) finish_one<F16>(p, t, n + 2, v[0].z, v[1].z);
+    if (n + 3 < p.N) finish_one<F16>(p, t, n + 3, v[0].w, v[1].w);
+  }
+  // no CTA leaves while another still reads its partial sums
+  __syncwarp();
+  tc::cluster_arrive();
+  tc::cluster_wait();
+}
+
+// ---- many tokens: persistent pairs of CTAs ---------------------------------------------
+// A pair owns a tile of 256 tokens x TN accumulator columns: each CTA loads
+// its 128 tokens (A) and its half of the weight rows (B), the even CTA issues
+// MMAs of M = 256 over both CTAs' operands, and each CTA's TMEM receives its
+// tokens' rows.  With a gate, the even CTA's half are rows of w and the odd
+// one's the same rows of w_up, so the first TN/2 columns are gates and the
+// others their ups: one main loop for both forms.  Two accumulators
+// alternate, so the epilogue of a tile runs under the next tile's MMAs.
+constexpr int kPairEpi = 8;                            // epilogue warps
+constexpr int kPairThreads = 32 * (kPairEpi + 2);      // + a loading and an MMA warp
+constexpr uint32_t kPairStage0 = kPairEpi * 32u * 32u * 4u;  // fp32 staging: 32 x 32 per epilogue warp
+
+template <int TN>
+struct PairPlan {
+  static constexpr uint32_t kBHalf = TN / 2 * 128u;
+  static constexpr uint32_t kStage = kTile + kBHalf;
+  static constexpr int kStages = TN == 256 ? 6 : 8;
+  static constexpr uint32_t kSmem = kPairStage0 + kStages * kStage + 1024u;
+};
+
+// Tile number -> (token tile, feature tile): columns of 8 token tiles, so that
+// the tiles in flight share their operands in L2.
+__device__ __forceinline__ void pair_tile(int tile, int MT, int FT, int& mt, int& ft) {
+  constexpr int kGroup = 8;
+  const int per = kGroup * FT, g = tile / per, in = tile - g * per;
+  const int rows = min(kGroup, MT - g * kGroup);
+  ft = in / rows;
+  mt = g * kGroup + in - ft * rows;
+}
+
+template <bool F16, bool GATED, int TN>
+__global__ void __launch_bounds__(kPairThreads, 1)
+    linear_pair_kernel(const __grid_constant__ CUtensorMap map_w, const __grid_constant__ CUtensorMap map_u,
+                       const __grid_constant__ CUtensorMap map_x, const LinearParams p) {
+  using P = PairPlan<TN>;
+  constexpr int ST = P::kStages;
+  constexpr int FN = GATED ? TN / 2 : TN;  // features per tile
+  extern __shared__ uint8_t smem_raw[];
+  __shared__ __align__(8) uint64_t bars[2 * ST + 4];
+  __shared__ uint32_t tmem_slot;
+  const uint32_t s0 = (smem_u32(smem_raw) + 1023u) & ~1023u;
+  const uint32_t op0 = s0 + kPairStage0;
+  const uint32_t full = smem_u32(bars), empty = full + 8u * ST, accfull = empty + 8u * ST, accfree = accfull + 16u;
+  const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
+  const uint32_t rank = tc::cluster_rank();
+  const int MT = (p.T + 255) / 256, FT = (p.N + FN - 1) / FN;
+  const int ntiles = MT * FT, npairs = gridDim.x / 2, pair = blockIdx.x / 2;
+  const int KB = (p.K + kKB - 1) / kKB;
+
+  if (tid == 0) {
+    for (int s = 0; s < ST; ++s) bar_init(full + 8u * s, 1), bar_init(empty + 8u * s, 1);
+    for (int b = 0; b < 2; ++b) bar_init(accfull + 8u * b, 1), bar_init(accfree + 8u * b, 2 * kPairEpi);
+    mbar_fence_init();
+  }
+  if (warp == kPairEpi + 1) {
+    tc::tmem_alloc2(smem_u32(&tmem_slot), 2 * TN);
+    tc::tmem_relinquish2();
+  }
+  tc::fence_before_sync();
+  __syncthreads();
+  tc::cluster_arrive();
+  tc::cluster_wait();
+  tc::fence_after_sync();
+  const uint32_t tmem = tmem_slot;
+
+  if (warp == kPairEpi) {
+    if (lane == 0) {
+      bool ok = true;
+      uint32_t i = 0;
+      const uint32_t full0 = tc::map_rank(full, 0);  // both CTAs' copies count on the even CTA's barriers
+      const void* mb = GATED && rank ? &map_u : &map_w;
+#pragma unroll 1
+      for (int tile = pair; tile < ntiles && ok; tile += npairs) {
+        int mt, ft;
+        pair_tile(tile, MT, FT, mt, ft);
+        const int y_a = mt * 256 + (int)rank * 128;
+        const int y_b = ft * FN + (GATED ? 0 : (int)rank * (TN / 2));
+#pragma unroll 1
+        for (int kb = 0; kb < KB; ++kb, ++i) {
+          const uint32_t s = i % ST;
+          if (i >= ST) ok = bar_wait(empty + 8u * s, (i / ST - 1u) & 1u);
+          if (!ok) break;
+          const uint32_t st = op0 + s * P::kStage;
+          if (rank == 0) bar_expect(full + 8u * s, 2 * P::kStage);
+          tc::tma2_2d(st, &map_x, kb * kKB, y_a, full0 + 8u * s);
+          tc::tma2_2d(st + kTile, mb, kb * kKB, y_b, full0 + 8u * s);
+        }
+      }
+      // the last stages' arrivals from the even CTA, before this block may leave
+      for (uint32_t j = i > ST ? i - ST : 0; j < i && ok; ++j) ok = bar_wait(empty + 8u * (j % ST), (j / ST) & 1u);
+      if (!ok) let_issued_work_end();
+    }
+  } else if (warp == kPairEpi + 1) {
+    if (rank == 0 && lane == 0) {
+      constexpr uint32_t idesc = tc::idesc_f16(256, TN, !F16);
+      bool ok = true;
+      uint32_t i = 0, it = 0;
+#pragma unroll 1
+      for (int tile = pair; tile < ntiles && ok; tile += npairs, ++it) {
+        const uint32_t b = it & 1u;
+        if (it >= 2) ok = bar_wait(accfree + 8u * b, (it / 2 - 1u) & 1u);
+        if (!ok) break;
+        tc::fence_after_sync();
+#pragma unroll 1
+        for (int kb = 0; kb < KB; ++kb, ++i) {
+          const uint32_t s = i % ST;
+          ok = bar_wait(full + 8u * s, (i / ST) & 1u);
+          if (!ok) break;
+          tc::fence_after_sync();
+          const uint32_t st = op0 + s * P::kStage;
+#pragma unroll
+          for (int k = 0; k < 4; ++k)
+            tc::mma2_f16_ss(tmem + b * TN, tc::smem_desc_sw128(st + 32u * k), tc::smem_desc_sw128(st + kTile + 32u * k),
+                            idesc, (kb > 0 || k > 0) ? 1u : 0u);
+          tc::commit2(empty + 8u * s);
+        }
+        if (ok) tc::commit2(accfull + 8u * b);
+      }
+      if (!ok) let_issued_work_end();
+    }
+  } else {
+    // Epilogue: warp w reads TMEM lanes 32 (w % 4) .. (its tokens) and half
+    // w / 4 of the columns, 32 features at a time: sums -> bias, activation,
+    // gate in "lane = token" order, through a private 32 x 32 fp32 square of
+    // shared memory (16-byte chunks XOR-swizzled by token) into "lanes along
+    // features" order, where residual and output are read and written in
+    // whole sectors.
+    const int quarter = warp & 3, half = warp >> 2;
+    const uint32_t sq = s0 + (uint32_t)warp * 4096u;
+    const uint32_t accfree0 = tc::map_rank(accfree, 0);
+    uint32_t it = 0;
+    bool ok = true;
+#pragma unroll 1
+    for (int tile = pair; tile < ntiles; tile += npairs, ++it) {
+      int mt, ft;
+      pair_tile(tile, MT, FT, mt, ft);
+      const uint32_t b = it & 1u;
+      ok = __all_sync(kAll, bar_wait(accfull + 8u * b, (it / 2) & 1u));
+      if (!ok) break;
+      tc::fence_after_sync();
+      const uint32_t acc = tmem + b * TN + ((uint32_t)(32 * quarter) << 16);
+      const int tok0 = mt * 256 + (int)rank * 128 + 32 * quarter;
+#pragma unroll 1
+      for (int c0 = half * (FN / 2); c0 < (half + 1) * (FN / 2); c0 += 32) {
+        const int n0 = ft * FN + c0;
+        uint32_t g[32], u[GATED ? 32 : 1];
+        tc::ld_32x32b_x32(acc + (uint32_t)c0, g);
+        if constexpr (GATED) tc::ld_32x32b_x32(acc + (uint32_t)(TN / 2 + c0), u);
+        const int nl = n0 + lane;
+        const float bg = p.bias && nl < p.N ? __ldg(p.bias + nl) : 0.f;
+        const float bu = GATED && p.bias_up && nl < p.N ? __ldg(p.bias_up + nl) : 0.f;
+        tc::wait_ld();
+        if (c0 + 32 >= (half + 1) * (FN / 2)) {
+          // the last read of this accumulator by this warp
+          tc::fence_before_sync();
+          __syncwarp();
+          if (lane == 0) tc::arrive_cluster(accfree0 + 8u * b);
+        }
+        if (n0 >= p.N || tok0 >= p.T) continue;
+#pragma unroll
+        for (int j = 0; j < 32; j += 4) {
+          float y[4];
+#pragma unroll
+          for (int q = 0; q < 4; ++q) {
+            float v = __uint_as_float(g[j + q]);
+            if (p.bias) v += __shfl_sync(kAll, bg, j + q);
+            v = activate(v, p.act);
+            if constexpr (GATED) {
+              float w = __uint_as_float(u[j + q]);
+              if (p.bias_up) w += __shfl_sync(kAll, bu, j + q);
+              v *= w;
+            }
+            y[q] = v;
+          }
+          sts_f4(sq + (uint32_t)lane * 128u + (((uint32_t)(j >> 2) ^ (lane & 7u)) << 4), y[0], y[1], y[2], y[3]);
+        }
+        __syncwarp();
+        if (p.vec && n0 + 32 <= p.N) {
+          if (p.out_f32) {
+#pragma unroll
+            for (int q = 0; q < 8; ++q) {  // 4 tokens x 8 chunks of 4 features
+              const int r = 4 * q + (lane >> 3), ch = lane & 7, t = tok0 + r;
+              if (t >= p.T) continue;
+              float4 v = lds_f4(sq + (uint32_t)r * 128u + ((uint32_t)(ch ^ (r & 7)) << 4));
+              if (p.res) {
+                const float4 e = *reinterpret_cast<const float4*>(static_cast<const float*>(p.res) + (size_t)t * p.ldr + n0 + 4 * ch);
+                v.x += e.x, v.y += e.y, v.z += e.z, v.w += e.w;
+              }
+              *reinterpret_cast<float4*>(static_cast<float*>(p.out) + (size_t)t * p.ldo + n0 + 4 * ch) = v;
+            }
+          } else {
+#pragma unroll
+            for (int q = 0; q < 4; ++q) {  // 8 tokens x 4 chunks of 8 features
+              const int r = 8 * q + (lane >> 2), ch = lane & 3, t = tok0 + r;
+              if (t >= p.T) continue;
+              const uint32_t row = sq + (uint32_t)r * 128u;
+              const float4 a = lds_f4(row + ((uint32_t)((2 * ch) ^ (r & 7)) << 4));
+              const float4 c = lds_f4(row + ((uint32_t)((2 * ch + 1) ^ (r & 7)) << 4));
+              float y[8] = {a.x, a.y, a.z, a.w, c.x, c.y, c.z, c.w};
+              if (p.res) {
+                const uint4 e = *reinterpret_cast<const uint4*>(static_cast<const uint16_t*>(p.res) + (size_t)t * p.ldr + n0 + 8 * ch);
+                const uint32_t w[4] = {e.x, e.y, e.z, e.w};
+#pragma unroll
+                for (int k = 0; k < 8; ++k) y[k] += from16<F16>((uint16_t)(w[k >> 1] >> (16 * (k & 1))));
+              }
+              uint32_t w[4];
+#pragma unroll
+              for (int k = 0; k < 4; ++k) w[k] = (uint32_t)to16<F16>(y[2 * k]) | (uint32_t)to16<F16>(y[2 * k + 1]) << 16;
+              *reinterpret_cast<uint4*>(static_cast<uint16_t*>(p.out) + (size_t)t * p.ldo + n0 + 8 * ch) = make_uint4(w[0], w[1], w[2], w[3]);
+            }
+          }
+        } else if (nl < p.N) {
+          // rows that start anywhere, or the last features: one element per lane
+#pragma unroll 4
+          for (int r = 0; r < 32; ++r) {
+            const int t = tok0 + r;
+            if (t >= p.T) break;
+            float v;
+            asm volatile("ld.shared.f32 %0, [%1];"
+                         : "=f"(v)
+                         : "r"(sq + (uint32_t)r * 128u + (((uint32_t)(lane >> 2) ^ (r & 7u)) << 4) + 4u * (lane & 3u))
+                         : "memory");
+            const size_t o = (size_t)t * p.ldo + nl;
+            if (p.out_f32) {
+              if (p.res) v += static_cast<const float*>(p.res)[(size_t)t * p.ldr + nl];
+              static_cast<float*>(p.out)[o] = v;
+            } else {
+              if (p.res) v += from16<F16>(static_cast<const uint16_t*>(p.res)[(size_t)t * p.ldr + nl]);
+              static_cast<uint16_t*>(p.out)[o] = to16<F16>(v);
+            }
+          }
+        }
+        __syncwarp();
+      }
+    }
+  }
+  __syncwarp();
+  tc::fence_before_sync();
+  tc::cluster_arrive();
+  tc::cluster_wait();
+  tc::fence_after_sync();
+  if (warp == kPairEpi + 1) tc::tmem_dealloc2(tmem, 2 * TN);
+}
+
+// ---- host side --------------------------------------------------------------------------
+
+using EncodeFn = decltype(&cuTensorMapEncodeTiled);
+
+// The driver's tensor-map encoder, looked up once.
+EncodeFn encoder() {
+  static EncodeFn fn = [] {
+    void* f = nullptr;
+    cudaDriverEntryPointQueryResult q;
+    if (cudaGetDriverEntryPointByVersion("cuTensorMapEncodeTiled", &f, 12000, cudaEnableDefault, &q) != cudaSuccess ||
+        q != cudaDriverEntryPointSuccess)
+      f = nullptr;
+    return reinterpret_cast<EncodeFn>(f);
+  }();
+  return fn;
+}
+
+// rows x K elements of 16 bits, ld apart, read in boxes of box_rows x 64
+// columns with the 128-byte swizzle; what lies outside reads as zero.
+bool make_map(CUtensorMap* m, bool f16, const void* base, int K, int rows, int64_t ld, int box_rows) {
+  const cuuint64_t dims[2] = {(cuuint64_t)K, (cuuint64_t)rows};
+  // one row: any stride will do, and the caller's may be none
+  const cuuint64_t strides[1] = {(cuuint64_t)(2 * ld)};
+  const cuuint32_t box[2] = {64, (cuuint32_t)box_rows}, step[2] = {1, 1};
+  return encoder()(m, f16 ? CU_TENSOR_MAP_DATA_TYPE_FLOAT16 : CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, 2,
+                   const_cast<void*>(base), dims, strides, box, step, CU_TENSOR_MAP_INTERLEAVE_NONE,
+                   CU_TENSOR_MAP_SWIZZLE_128B, CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
+                   CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
+}
+
+// A launch with clusters along x and room for `smem` bytes of dynamic shared
+// memory (the attribute is set once per kernel and device).
+template <auto Kernel>
+cudaError_t launch_cluster(dim3 grid, int threads, int cluster, uint32_t smem, const CUtensorMap& w,
+                           const CUtensorMap& u, const CUtensorMap& x, const LinearParams& p, cudaStream_t st) {
+  static bool set[64] = {};
+  int dev = 0;
+  cudaError_t e = cudaGetDevice(&dev);
+  if (e != cudaSuccess) return e;
+  if (dev < 0 || dev >= 64 || !set[dev]) {
+    e = cudaFuncSetAttribute(Kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)smem);
+    if (e != cudaSuccess) return e;
+    if (dev >= 0 && dev < 64) set[dev] = true;
+  }
+  cudaLaunchConfig_t c = {};
+  c.gridDim = grid;
+  c.blockDim = dim3(threads);
+  c.dynamicSmemBytes = smem;
+  c.stream = st;
+  cudaLaunchAttribute a[1];
+  a[0].id = cudaLaunchAttributeClusterDimension;
+  a[0].val.clusterDim.x = cluster;
+  a[0].val.clusterDim.y = 1;
+  a[0].val.clusterDim.z = 1;
+  c.attrs = a;
+  c.numAttrs = 1;
+  return cudaLaunchKernelEx(&c, Kernel, w, u, x, p);
+}
+
+template <bool F16, bool GATED, int NT>
+cudaError_t launch_split_t(const LinearParams& p, int S, cudaStream_t st) {
+  CUtensorMap w, u, x;
+  if (!make_map(&w, F16, p.w, p.K, p.N, p.ldw, 128) || !make_map(&x, F16, p.x, p.K, p.T, p.ldx, NT)) return cudaErrorInvalidValue;
+  u = w;
+  if (GATED && !make_map(&u, F16, p.w_up, p.K, p.N, p.ldw_up, 128)) return cudaErrorInvalidValue;
+  constexpr int NA = GATED ? 2 : 1;
+  constexpr uint32_t smem = split_stages(NT, NA) * split_stage(NT, NA) + 1024u;
+  const dim3 grid(S, (p.N + 127) / 128, (p.T + NT - 1) / NT);
+  return launch_cluster<linear_split_kernel<F16, GATED, NT>>(grid, kSplitThreads, S, smem, w, u, x, p, st);
+}
+
+template <bool F16, bool GATED>
+cudaError_t launch_split(const LinearParams& p, int S, cudaStream_t st) {
+  if (p.T <= 16) return launch_split_t<F16, GATED, 16>(p, S, st);
+  if (p.T <= 32) return launch_split_t<F16, GATED, 32>(p, S, st);
+  if (p.T <= 64) return launch_split_t<F16, GATED, 64>(p, S, st);
+  if (GATED || p.T <= 128) return launch_split_t<F16, GATED, 128>(p, S, st);
+  if constexpr (!GATED) return launch_split_t<F16, GATED, 256>(p, S, st);
+  return cudaErrorInvalidValue;
+}
+
+template <bool F16, bool GATED, int TN>
+cudaError_t launch_pair_t(const LinearParams& p, int sms, cudaStream_t st) {
+  CUtensorMap w, u, x;
+  constexpr int FN = GATED ? TN / 2 : TN;
+  if (!make_map(&w, F16, p.w, p.K, p.N, p.ldw, TN / 2) || !make_map(&x, F16, p.x, p.K, p.T, p.ldx, 128)) return cudaErrorInvalidValue;
+  u = w;
+  if (GATED && !make_map(&u, F16, p.w_up, p.K, p.N, p.ldw_up, TN / 2)) return cudaErrorInvalidValue;
+  const int64_t tiles = (int64_t)((p.T + 255) / 256) * ((p.N + FN - 1) / FN);
+  if (tiles > 0x3fffffff) return cudaErrorInvalidValue;
+  const int pairs = (int)(tiles < sms / 2 ? tiles : sms / 2);
+  return launch_cluster<linear_pair_kernel<F16, GATED, TN>>(dim3(2 * pairs), kPairThreads, 2, PairPlan<TN>::kSmem, w, u,
+                                                            x, p, st);
+}
+
+template <bool F16, bool GATED>
+cudaError_t launch_rows(const LinearParams& p, cudaStream_t st) {
+  const int ntt = (p.T + kRowsTok - 1) / kRowsTok;
+  linear_rows_kernel<F16, GATED><<<dim3((p.N + kRowsFeat - 1) / kRowsFeat, ntt), 32 * kRowsWarps, 0, st>>>(p);
   return cudaGetLastError();
 }
 
-// The error word of the calls on a device: the first expired wait's code.
-__device__ uint32_t g_linear_err;
+template <bool F16, bool GATED>
+cudaError_t launch_any(const LinearParams& p, int sms, cudaStream_t st) {
+  if (p.T <= 8) return launch_rows<F16, GATED>(p, st);
+  if (!encoder()) return cudaErrorNotSupported;
+  if (p.T <= 256) {
+    const int tiles = (p.N + 127) / 128 * (GATED && p.T > 128 ? 2 : 1), KB = (p.K + kKB - 1) / kKB;
+    int S = 1;
+    while (S < 8 && 2 * S * tiles <= sms && 2 * S <= KB) S *= 2;
+    return launch_split<F16, GATED>(p, S, st);
+  }
+  return launch_pair_t<F16, GATED, 256>(p, sms, st);
+}
+
+}  // namespace
+
+cudaError_t launch_linear(const LinearParams& p, bool f16, int sms, cudaStream_t st) {
+  if (p.w_up) return f16 ? launch_any<true, true>(p, sms, st) : launch_any<false, true>(p, sms, st);
+  return f16 ? launch_any<true, false>(p, sms, st) : launch_any<false, false>(p, sms, st);
+}
 
 cudaError_t read_linear_error(uint32_t* code, cudaStream_t st) {
   uint32_t zero = 0;
