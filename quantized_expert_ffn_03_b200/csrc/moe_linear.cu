@@ -31,21 +31,33 @@ constexpr unsigned kAll = 0xffffffffu;
 
 // ---- epilogue arithmetic ------------------------------------------------------------
 
-// The activation in fp32.  tanh-GELU is v * sigmoid(2u), the same value
-// without the cancellation of 1 + tanh(u) at negative u; GELU takes the
-// normal CDF for the same reason.  NaN passes through all of them.
-__device__ __forceinline__ float activate(float v, int act) {
+// The activation in fp32, one switch for N values (a switch for each value
+// fills the instruction cache once the loops around it are unrolled).
+// tanh-GELU is v * sigmoid(2u), the same value without the cancellation of
+// 1 + tanh(u) at negative u; GELU takes the normal CDF for the same reason.
+// NaN passes through all of them.
+template <int N>
+__device__ __forceinline__ void activate(float (&v)[N], int act) {
   switch (act) {
     case MOE_ACT_SILU:
-      return __fdividef(v, 1.f + __expf(-v));
+#pragma unroll
+      for (int i = 0; i < N; ++i) v[i] = __fdividef(v[i], 1.f + __expf(-v[i]));
+      break;
     case MOE_ACT_GELU:
-      return v * normcdff(v);
+#pragma unroll
+      for (int i = 0; i < N; ++i) v[i] *= normcdff(v[i]);
+      break;
     case MOE_ACT_GELU_TANH:
-      return __fdividef(v, 1.f + __expf(-1.5957691216057308f * fmaf(0.044715f * v * v, v, v)));
+#pragma unroll
+      for (int i = 0; i < N; ++i)
+        v[i] = __fdividef(v[i], 1.f + __expf(-1.5957691216057308f * fmaf(0.044715f * v[i] * v[i], v[i], v[i])));
+      break;
     case MOE_ACT_RELU:
-      return v < 0.f ? 0.f : v;
+#pragma unroll
+      for (int i = 0; i < N; ++i) v[i] = v[i] < 0.f ? 0.f : v[i];
+      break;
     default:
-      return v;
+      break;
   }
 }
 
@@ -69,7 +81,9 @@ __device__ __forceinline__ uint16_t to16(float v) {
 template <bool F16>
 __device__ __forceinline__ void finish_one(const LinearParams& p, int t, int n, float g, float u) {
   if (p.bias) g += __ldg(p.bias + n);
-  float y = activate(g, p.act);
+  float a[1] = {g};
+  activate(a, p.act);
+  float y = a[0];
   if (p.w_up) y *= p.bias_up ? u + __ldg(p.bias_up + n) : u;
   const size_t o = (size_t)t * p.ldo + n;
   if (p.out_f32) {
@@ -78,6 +92,67 @@ __device__ __forceinline__ void finish_one(const LinearParams& p, int t, int n, 
   } else {
     if (p.res) y += from16<F16>(static_cast<const uint16_t*>(p.res)[(size_t)t * p.ldr + n]);
     static_cast<uint16_t*>(p.out)[o] = to16<F16>(y);
+  }
+}
+
+// W (4 or 8) adjacent values of a row of out or residual, on a boundary of
+// their size.
+template <bool F16, int W>
+__device__ __forceinline__ void load_row(const LinearParams& p, const void* base, size_t at, float (&v)[W]) {
+  if (p.out_f32) {
+#pragma unroll
+    for (int i = 0; i < W; i += 4) {
+      const float4 e = *reinterpret_cast<const float4*>(static_cast<const float*>(base) + at + i);
+      v[i] = e.x, v[i + 1] = e.y, v[i + 2] = e.z, v[i + 3] = e.w;
+    }
+  } else {
+    uint32_t w[W / 2];
+    const uint16_t* src = static_cast<const uint16_t*>(base) + at;
+    if constexpr (W == 8) {
+      const uint4 e = *reinterpret_cast<const uint4*>(src);
+      w[0] = e.x, w[1] = e.y, w[2] = e.z, w[3] = e.w;
+    } else {
+      const uint2 e = *reinterpret_cast<const uint2*>(src);
+      w[0] = e.x, w[1] = e.y;
+    }
+#pragma unroll
+    for (int i = 0; i < W; ++i) v[i] = from16<F16>((uint16_t)(w[i >> 1] >> (16 * (i & 1))));
+  }
+}
+template <bool F16, int W>
+__device__ __forceinline__ void store_row(const LinearParams& p, size_t at, const float (&v)[W]) {
+  if (p.out_f32) {
+#pragma unroll
+    for (int i = 0; i < W; i += 4)
+      *reinterpret_cast<float4*>(static_cast<float*>(p.out) + at + i) = make_float4(v[i], v[i + 1], v[i + 2], v[i + 3]);
+  } else {
+    uint32_t w[W / 2];
+#pragma unroll
+    for (int i = 0; i < W / 2; ++i) w[i] = (uint32_t)to16<F16>(v[2 * i]) | (uint32_t)to16<F16>(v[2 * i + 1]) << 16;
+    uint16_t* dst = static_cast<uint16_t*>(p.out) + at;
+    if constexpr (W == 8)
+      *reinterpret_cast<uint4*>(dst) = make_uint4(w[0], w[1], w[2], w[3]);
+    else
+      *reinterpret_cast<uint2*>(dst) = make_uint2(w[0], w[1]);
+  }
+}
+// Bias, activation and gate of W adjacent features n .. (those below N).
+template <bool GATED, int W>
+__device__ __forceinline__ void bias_act_gate(const LinearParams& p, int n, float (&v)[W], const float (&u)[W]) {
+  if (p.bias) {
+#pragma unroll
+    for (int i = 0; i < W; ++i)
+      if (n + i < p.N) v[i] += __ldg(p.bias + n + i);
+  }
+  activate(v, p.act);
+  if constexpr (GATED) {
+    if (p.bias_up) {
+#pragma unroll
+      for (int i = 0; i < W; ++i) v[i] *= n + i < p.N ? u[i] + __ldg(p.bias_up + n + i) : 0.f;
+    } else {
+#pragma unroll
+      for (int i = 0; i < W; ++i) v[i] *= u[i];
+    }
   }
 }
 
@@ -179,7 +254,7 @@ constexpr uint64_t kLinearTimeoutNs = 2000000000ull;  // 2 s per wait
 __device__ __forceinline__ bool bar_try(uint32_t bar, uint32_t parity) {
   uint32_t ok;
   asm volatile(
-      "{\n .reg .pred p;\n mbarrier.try_wait.parity.acquire.cluster.shared::cta.b64 p, [%1], %2;\n"
+      "{\n .reg .pred p;\n mbarrier.try_wait.parity.shared::cta.b64 p, [%1], %2;\n"
       " selp.u32 %0, 1, 0, p;\n}"
       : "=r"(ok)
       : "r"(bar), "r"(parity)
@@ -221,6 +296,12 @@ __device__ __forceinline__ float4 lds_f4(uint32_t a) {
   return v;
 }
 
+// 8 floats from 16-byte chunks c, c + 1 of a swizzled 128-byte row.
+__device__ __forceinline__ void read8(uint32_t row, uint32_t c, uint32_t x, float (&v)[8]) {
+  const float4 a = lds_f4(row + ((c ^ x) << 4)), b = lds_f4(row + (((c + 1u) ^ x) << 4));
+  v[0] = a.x, v[1] = a.y, v[2] = a.z, v[3] = a.w, v[4] = b.x, v[5] = b.y, v[6] = b.z, v[7] = b.w;
+}
+
 constexpr int kKB = 64;                  // columns of K per stage: 128 bytes, one swizzle row
 constexpr uint32_t kTile = 128u * 128u;  // bytes of a 128-row operand tile of one stage
 
@@ -233,7 +314,9 @@ constexpr uint32_t kTile = 128u * 128u;  // bytes of a 128-row operand tile of o
 // of the outputs over the cluster in rank order and finishes them.  Nothing
 // is exchanged through global memory, so no workspace, and calls on several
 // streams share nothing.
-constexpr int kSplitThreads = 192;  // 4 warps read TMEM, one loads, one issues MMAs
+constexpr int kSplitEpi = 8;                         // warps that read TMEM
+constexpr int kSplitThreads = 32 * (kSplitEpi + 2);  // + a loading and an MMA warp
+constexpr int kMaxSplit = 8;                         // CTAs of a cluster (the portable size)
 constexpr uint32_t kSplitSmem = 220u * 1024u;
 
 __host__ __device__ constexpr uint32_t split_stage(int nt, int na) { return na * kTile + (uint32_t)nt * 128u; }
@@ -268,7 +351,7 @@ __global__ void __launch_bounds__(kSplitThreads, 1)
     bar_init(accfull, 1);
     mbar_fence_init();
   }
-  if (warp == 5) {
+  if (warp == kSplitEpi + 1) {
     tc::tmem_alloc(smem_u32(&tmem_slot), tmem_cols(NA * NT));
     tc::tmem_relinquish();
   }
@@ -277,7 +360,7 @@ __global__ void __launch_bounds__(kSplitThreads, 1)
   tc::fence_after_sync();
   const uint32_t tmem = tmem_slot;
 
-  if (warp == 4) {
+  if (warp == kSplitEpi) {
     if (lane == 0) {
       bool ok = true;
 #pragma unroll 1
@@ -293,7 +376,7 @@ __global__ void __launch_bounds__(kSplitThreads, 1)
       }
       if (!ok) let_issued_work_end();
     }
-  } else if (warp == 5) {
+  } else if (warp == kSplitEpi + 1) {
     if (lane == 0) {
       constexpr uint32_t idesc = tc::idesc_f16(128, NT, !F16);
       bool ok = true;
@@ -324,12 +407,13 @@ __global__ void __launch_bounds__(kSplitThreads, 1)
     // completed MMAs no longer read
     const bool ok = __all_sync(kAll, bar_wait(accfull, 0));
     tc::fence_after_sync();
-    const uint32_t dst = s0 + 4u * (uint32_t)(32 * warp + lane);
+    const int quarter = warp & 3, half = warp >> 2;  // TMEM lanes (features), half of the columns
+    const uint32_t dst = s0 + 4u * (uint32_t)(32 * quarter + lane);
     if (ok) {
 #pragma unroll 1
-      for (int j = 0; j < NA * NT; j += 16) {
+      for (int j = 16 * half; j < NA * NT; j += 32) {
         uint32_t v[16];
-        tc::ld_32x32b_x16(tmem + ((uint32_t)(32 * warp) << 16) + (uint32_t)j, v);
+        tc::ld_32x32b_x16(tmem + ((uint32_t)(32 * quarter) << 16) + (uint32_t)j, v);
         tc::wait_ld();
 #pragma unroll
         for (int q = 0; q < 16; ++q)
@@ -342,29 +426,44 @@ __global__ void __launch_bounds__(kSplitThreads, 1)
   tc::cluster_arrive();
   tc::cluster_wait();
   tc::fence_after_sync();
-  if (warp == 5) tc::tmem_dealloc(tmem, tmem_cols(NA * NT));
+  if (warp == kSplitEpi + 1) tc::tmem_dealloc(tmem, tmem_cols(NA * NT));
 
   // this CTA's share of the outputs: items of 4 adjacent features of a token
   const int nt = min(NT, p.T - t0), items = nt * 32;
   const int i0 = (int)((int64_t)items * rank / S), i1 = (int)((int64_t)items * (rank + 1) / S);
 #pragma unroll 1
   for (int i = i0 + tid; i < i1; i += kSplitThreads) {
-    const int c = i >> 5, f = 4 * (i & 31);
-    float4 v[2] = {};
+    const int c = i >> 5, f = 4 * (i & 31), n = n0 + f, t = t0 + c;
+    if (n >= p.N) continue;
+    const bool whole = p.vec && n + 4 <= p.N;
+    float e[4] = {0.f, 0.f, 0.f, 0.f}, v[NA][4] = {};
+    if (p.res && whole) load_row<F16>(p, p.res, (size_t)t * p.ldr + n, e);
+    float4 q[NA][kMaxSplit];
 #pragma unroll
-    for (int a = 0; a < NA; ++a) {
-      const uint32_t src = s0 + 512u * (uint32_t)(a * NT + c) + 4u * (uint32_t)f;
+    for (int a = 0; a < NA; ++a)
+#pragma unroll
+      for (uint32_t r = 0; r < kMaxSplit; ++r)
+        if (r < S) q[a][r] = tc::ld_cluster_f4(tc::map_rank(s0 + 512u * (uint32_t)(a * NT + c) + 4u * (uint32_t)f, r));
+#pragma unroll
+    for (int a = 0; a < NA; ++a)
+#pragma unroll
+      for (uint32_t r = 0; r < kMaxSplit; ++r)
+        if (r < S) v[a][0] += q[a][r].x, v[a][1] += q[a][r].y, v[a][2] += q[a][r].z, v[a][3] += q[a][r].w;
+    if (whole) {
+      bias_act_gate<GATED>(p, n, v[0], v[NA - 1]);
+      if (p.res) {
+#pragma unroll
+        for (int k = 0; k < 4; ++k) v[0][k] += e[k];
+      }
+      store_row<F16>(p, (size_t)t * p.ldo + n, v[0]);
+    } else {
 #pragma unroll 1
-      for (uint32_t r = 0; r < S; ++r) {
-        const float4 q = tc::ld_cluster_f4(tc::map_rank(src, r));
-        v[a].x += q.x, v[a].y += q.y, v[a].z += q.z, v[a].w += q.w;
+      for (int k = 0; k < 4; ++k) {
+        if (n + k < p.N) finish_one<F16>(p, t, n + k, v[0][0], v[NA - 1][0]);
+#pragma unroll
+        for (int a = 0; a < NA; ++a) v[a][0] = v[a][1], v[a][1] = v[a][2], v[a][2] = v[a][3];
       }
     }
-    const int n = n0 + f, t = t0 + c;
-    if (n < p.N) finish_one<F16>(p, t, n, v[0].x, v[1].x);
-    if (n + 1 < p.N) finish_one<F16>(p, t, n + 1, v[0].y, v[1].y);
-    if (n + 2 < p.N) finish_one<F16>(p, t, n + 2, v[0].z, v[1].z);
-    if (n + 3 < p.N) finish_one<F16>(p, t, n + 3, v[0].w, v[1].w);
   }
   // no CTA leaves while another still reads its partial sums
   __syncwarp();
@@ -409,6 +508,7 @@ __global__ void __launch_bounds__(kPairThreads, 1)
   using P = PairPlan<TN>;
   constexpr int ST = P::kStages;
   constexpr int FN = GATED ? TN / 2 : TN;  // features per tile
+  constexpr int FC = GATED ? 16 : 32;      // features of an epilogue step
   extern __shared__ uint8_t smem_raw[];
   __shared__ __align__(8) uint64_t bars[2 * ST + 4];
   __shared__ uint32_t tmem_slot;
@@ -494,11 +594,11 @@ __global__ void __launch_bounds__(kPairThreads, 1)
     }
   } else {
     // Epilogue: warp w reads TMEM lanes 32 (w % 4) .. (its tokens) and half
-    // w / 4 of the columns, 32 features at a time: sums -> bias, activation,
-    // gate in "lane = token" order, through a private 32 x 32 fp32 square of
-    // shared memory (16-byte chunks XOR-swizzled by token) into "lanes along
-    // features" order, where residual and output are read and written in
-    // whole sectors.
+    // w / 4 of the columns, 32 of them at a time (with a gate 16 and their 16
+    // ups), in "lane = token" order, and passes the raw sums through a private
+    // 32 x 32 fp32 square of shared memory (16-byte chunks XOR-swizzled by
+    // token) into "lanes along features" order: a lane then holds 8 adjacent
+    // features of a token, and residual and output move in whole sectors.
     const int quarter = warp & 3, half = warp >> 2;
     const uint32_t sq = s0 + (uint32_t)warp * 4096u;
     const uint32_t accfree0 = tc::map_rank(accfree, 0);
@@ -515,84 +615,67 @@ __global__ void __launch_bounds__(kPairThreads, 1)
       const uint32_t acc = tmem + b * TN + ((uint32_t)(32 * quarter) << 16);
       const int tok0 = mt * 256 + (int)rank * 128 + 32 * quarter;
 #pragma unroll 1
-      for (int c0 = half * (FN / 2); c0 < (half + 1) * (FN / 2); c0 += 32) {
+      for (int c0 = half * (FN / 2); c0 < (half + 1) * (FN / 2); c0 += FC) {
         const int n0 = ft * FN + c0;
-        uint32_t g[32], u[GATED ? 32 : 1];
-        tc::ld_32x32b_x32(acc + (uint32_t)c0, g);
-        if constexpr (GATED) tc::ld_32x32b_x32(acc + (uint32_t)(TN / 2 + c0), u);
-        const int nl = n0 + lane;
-        const float bg = p.bias && nl < p.N ? __ldg(p.bias + nl) : 0.f;
-        const float bu = GATED && p.bias_up && nl < p.N ? __ldg(p.bias_up + nl) : 0.f;
-        tc::wait_ld();
-        if (c0 + 32 >= (half + 1) * (FN / 2)) {
-          // the last read of this accumulator by this warp
-          tc::fence_before_sync();
-          __syncwarp();
-          if (lane == 0) tc::arrive_cluster(accfree0 + 8u * b);
-        }
-        if (n0 >= p.N || tok0 >= p.T) continue;
-#pragma unroll
-        for (int j = 0; j < 32; j += 4) {
-          float y[4];
-#pragma unroll
-          for (int q = 0; q < 4; ++q) {
-            float v = __uint_as_float(g[j + q]);
-            if (p.bias) v += __shfl_sync(kAll, bg, j + q);
-            v = activate(v, p.act);
-            if constexpr (GATED) {
-              float w = __uint_as_float(u[j + q]);
-              if (p.bias_up) w += __shfl_sync(kAll, bu, j + q);
-              v *= w;
-            }
-            y[q] = v;
+        {
+          uint32_t g[32];
+          if constexpr (GATED) {
+            uint32_t(&lo)[16] = *reinterpret_cast<uint32_t(*)[16]>(g);
+            uint32_t(&hi)[16] = *reinterpret_cast<uint32_t(*)[16]>(g + 16);
+            tc::ld_32x32b_x16(acc + (uint32_t)c0, lo);
+            tc::ld_32x32b_x16(acc + (uint32_t)(TN / 2 + c0), hi);
+          } else {
+            tc::ld_32x32b_x32(acc + (uint32_t)c0, g);
           }
-          sts_f4(sq + (uint32_t)lane * 128u + (((uint32_t)(j >> 2) ^ (lane & 7u)) << 4), y[0], y[1], y[2], y[3]);
+          tc::wait_ld();
+          if (c0 + FC >= (half + 1) * (FN / 2)) {
+            // the last read of this accumulator by this warp
+            tc::fence_before_sync();
+            __syncwarp();
+            if (lane == 0) tc::arrive_cluster(accfree0 + 8u * b);
+          }
+          if (n0 >= p.N || tok0 >= p.T) continue;
+#pragma unroll
+          for (int j = 0; j < 8; ++j)
+            sts_f4(sq + (uint32_t)lane * 128u + (((uint32_t)j ^ (lane & 7u)) << 4), __uint_as_float(g[4 * j]),
+                   __uint_as_float(g[4 * j + 1]), __uint_as_float(g[4 * j + 2]), __uint_as_float(g[4 * j + 3]));
         }
         __syncwarp();
-        if (p.vec && n0 + 32 <= p.N) {
-          if (p.out_f32) {
+        const bool whole = p.vec && n0 + FC <= p.N;
+        constexpr int LR = FC / 8, RP = 32 / LR;  // lanes of a row, rows of a pass
+        const int ch = lane % LR, n = n0 + 8 * ch;
+#pragma unroll 1
+        for (int r = lane / LR; r < 32; r += RP) {
+          const int t = tok0 + r;
+          const uint32_t row = sq + (uint32_t)r * 128u, x = (uint32_t)(r & 7);
+          float v[8], u[8], e[8];
+          if (whole && p.res && t < p.T) load_row<F16>(p, p.res, (size_t)t * p.ldr + n, e);
+          read8(row, 2u * ch, x, v);
+          if constexpr (GATED) read8(row, 2u * ch + 4u, x, u);
+          bias_act_gate<GATED>(p, n, v, u);
+          if (!whole) {
+            sts_f4(row + (((2u * ch) ^ x) << 4), v[0], v[1], v[2], v[3]);
+            sts_f4(row + (((2u * ch + 1u) ^ x) << 4), v[4], v[5], v[6], v[7]);
+          } else if (t < p.T) {
+            if (p.res) {
 #pragma unroll
-            for (int q = 0; q < 8; ++q) {  // 4 tokens x 8 chunks of 4 features
-              const int r = 4 * q + (lane >> 3), ch = lane & 7, t = tok0 + r;
-              if (t >= p.T) continue;
-              float4 v = lds_f4(sq + (uint32_t)r * 128u + ((uint32_t)(ch ^ (r & 7)) << 4));
-              if (p.res) {
-                const float4 e = *reinterpret_cast<const float4*>(static_cast<const float*>(p.res) + (size_t)t * p.ldr + n0 + 4 * ch);
-                v.x += e.x, v.y += e.y, v.z += e.z, v.w += e.w;
-              }
-              *reinterpret_cast<float4*>(static_cast<float*>(p.out) + (size_t)t * p.ldo + n0 + 4 * ch) = v;
+              for (int k = 0; k < 8; ++k) v[k] += e[k];
             }
-          } else {
-#pragma unroll
-            for (int q = 0; q < 4; ++q) {  // 8 tokens x 4 chunks of 8 features
-              const int r = 8 * q + (lane >> 2), ch = lane & 3, t = tok0 + r;
-              if (t >= p.T) continue;
-              const uint32_t row = sq + (uint32_t)r * 128u;
-              const float4 a = lds_f4(row + ((uint32_t)((2 * ch) ^ (r & 7)) << 4));
-              const float4 c = lds_f4(row + ((uint32_t)((2 * ch + 1) ^ (r & 7)) << 4));
-              float y[8] = {a.x, a.y, a.z, a.w, c.x, c.y, c.z, c.w};
-              if (p.res) {
-                const uint4 e = *reinterpret_cast<const uint4*>(static_cast<const uint16_t*>(p.res) + (size_t)t * p.ldr + n0 + 8 * ch);
-                const uint32_t w[4] = {e.x, e.y, e.z, e.w};
-#pragma unroll
-                for (int k = 0; k < 8; ++k) y[k] += from16<F16>((uint16_t)(w[k >> 1] >> (16 * (k & 1))));
-              }
-              uint32_t w[4];
-#pragma unroll
-              for (int k = 0; k < 4; ++k) w[k] = (uint32_t)to16<F16>(y[2 * k]) | (uint32_t)to16<F16>(y[2 * k + 1]) << 16;
-              *reinterpret_cast<uint4*>(static_cast<uint16_t*>(p.out) + (size_t)t * p.ldo + n0 + 8 * ch) = make_uint4(w[0], w[1], w[2], w[3]);
-            }
+            store_row<F16>(p, (size_t)t * p.ldo + n, v);
           }
-        } else if (nl < p.N) {
+        }
+        __syncwarp();
+        if (!whole) {
           // rows that start anywhere, or the last features: one element per lane
+          const int k = lane % FC, nl = n0 + k;
 #pragma unroll 4
-          for (int r = 0; r < 32; ++r) {
+          for (int r = lane / FC; r < 32; r += 32 / FC) {
             const int t = tok0 + r;
-            if (t >= p.T) break;
+            if (t >= p.T || nl >= p.N) continue;
             float v;
             asm volatile("ld.shared.f32 %0, [%1];"
                          : "=f"(v)
-                         : "r"(sq + (uint32_t)r * 128u + (((uint32_t)(lane >> 2) ^ (r & 7u)) << 4) + 4u * (lane & 3u))
+                         : "r"(sq + (uint32_t)r * 128u + ((uint32_t)((k >> 2) ^ (r & 7)) << 4) + 4u * (uint32_t)(k & 3))
                          : "memory");
             const size_t o = (size_t)t * p.ldo + nl;
             if (p.out_f32) {
@@ -603,8 +686,8 @@ __global__ void __launch_bounds__(kPairThreads, 1)
               static_cast<uint16_t*>(p.out)[o] = to16<F16>(v);
             }
           }
+          __syncwarp();
         }
-        __syncwarp();
       }
     }
   }
