@@ -28,6 +28,7 @@ __device__ uint32_t g_linear_err;
 namespace {
 
 constexpr unsigned kAll = 0xffffffffu;
+constexpr int kKB = 64;  // columns of K per step: 128 bytes, one swizzle row
 
 // ---- epilogue arithmetic ------------------------------------------------------------
 
@@ -74,6 +75,19 @@ __device__ __forceinline__ uint16_t to16(float v) {
     return __half_as_ushort(__float2half_rn(v));
   else
     return __bfloat16_as_ushort(__float2bfloat16_rn(v));
+}
+
+// Two values rounded to 16 bits, a in the low half (one instruction, where two
+// single conversions go to the slow conversion pipe).
+template <bool F16>
+__device__ __forceinline__ uint32_t pack16(float a, float b) {
+  if constexpr (F16) {
+    const __half2 h = __floats2half2_rn(a, b);
+    return *reinterpret_cast<const uint32_t*>(&h);
+  } else {
+    const __nv_bfloat162 h = __floats2bfloat162_rn(a, b);
+    return *reinterpret_cast<const uint32_t*>(&h);
+  }
 }
 
 // One output from its sums: bias, activation, gate, residual, store.  The
@@ -128,7 +142,7 @@ __device__ __forceinline__ void store_row(const LinearParams& p, size_t at, cons
   } else {
     uint32_t w[W / 2];
 #pragma unroll
-    for (int i = 0; i < W / 2; ++i) w[i] = (uint32_t)to16<F16>(v[2 * i]) | (uint32_t)to16<F16>(v[2 * i + 1]) << 16;
+    for (int i = 0; i < W / 2; ++i) w[i] = pack16<F16>(v[2 * i], v[2 * i + 1]);
     uint16_t* dst = static_cast<uint16_t*>(p.out) + at;
     if constexpr (W == 8)
       *reinterpret_cast<uint4*>(dst) = make_uint4(w[0], w[1], w[2], w[3]);
@@ -171,11 +185,29 @@ __device__ __forceinline__ void mma16816(float (&c)[4], uint32_t a0, uint32_t a1
                  : "r"(a0), "r"(a1), "r"(a2), "r"(a3), "r"(b0), "r"(b1));
 }
 
-// 8 elements of a row from column k (a multiple of 8); columns from K on read
-// as zero and are never touched in memory.
-__device__ __forceinline__ uint4 row8(const uint16_t* row, int k, int K, bool live) {
-  uint4 v = make_uint4(0u, 0u, 0u, 0u);
-  if (!live || k >= K) return v;
+// A block takes 8 features (the N of m16n8k16 steps) and up to 16 tokens (its
+// M; TM of them); its 8 warps take the 64-column units of K in turn.  Lane
+// (g, t) of a warp fetches 16 bytes of weight row g at columns 8t.. of each
+// 32-column half unit: the order of columns within a sum is free, so those 8
+// values serve as fragments of two k16 steps without a shuffle, and x is
+// read the same way.  Weights go through a ring of kRowsDepth units of shared
+// memory by cp.async, where each lane reads back what it copied itself: no
+// barrier, no registers held by loads in flight, and about 190 KB on their
+// way per SM (4 blocks of 48 KB).
+constexpr int kRowsFeat = 8, kRowsTok = 16, kRowsWarps = 8, kRowsDepth = 6;
+constexpr uint32_t kRowsUnit = 1024u;  // bytes of a warp's unit: 8 rows x 64 columns
+constexpr uint32_t rows_smem(int na) { return (uint32_t)(kRowsWarps * kRowsDepth * na) * kRowsUnit; }
+
+// 16 bytes of a row from column k; columns from K on read as zero and are
+// never touched in memory.
+__device__ __forceinline__ void row_copy16(uint32_t dst, const uint16_t* row, int k, int K, bool live) {
+  const int left = live ? 2 * (K - k) : 0;
+  const uint32_t n = left >= 16 ? 16u : left > 0 ? (uint32_t)left : 0u;
+  asm volatile("cp.async.cg.shared.global.L2::256B [%0], [%1], 16, %2;" ::"r"(dst), "l"(n ? row + k : row), "r"(n)
+               : "memory");
+}
+__device__ __forceinline__ uint4 row_load16(const uint16_t* row, int k, int K, bool live) {
+  if (!live || k >= K) return make_uint4(0u, 0u, 0u, 0u);
   if (k + 8 <= K) return __ldg(reinterpret_cast<const uint4*>(row + k));
   uint32_t h[4] = {0u, 0u, 0u, 0u};
 #pragma unroll
@@ -184,66 +216,85 @@ __device__ __forceinline__ uint4 row8(const uint16_t* row, int k, int K, bool li
   return make_uint4(h[0], h[1], h[2], h[3]);
 }
 
-// A block takes 16 features (the M of m16n8k16 steps) and 8 tokens; its 8
-// warps take the 64-column units of K in turn.  Lane (g, t) of a warp loads
-// 16 bytes of rows g and g + 8 at columns 8t.. of a 32-column half unit: the
-// order of columns within a sum is free, so those 8 values serve as the
-// fragments of two k16 steps without a shuffle, and x is loaded the same way.
-constexpr int kRowsFeat = 16, kRowsTok = 8, kRowsWarps = 8;
-template <bool F16, bool GATED>
-__global__ void __launch_bounds__(32 * kRowsWarps) linear_rows_kernel(const LinearParams p) {
-  constexpr int NA = GATED ? 2 : 1;
-  __shared__ float red[kRowsWarps][NA][kRowsTok][kRowsFeat + 1];
+template <bool F16, bool GATED, int TM>
+__global__ void __launch_bounds__(32 * kRowsWarps, 4) linear_rows_kernel(const LinearParams p) {
+  constexpr int NA = GATED ? 2 : 1, NX = TM / 8;
+  extern __shared__ __align__(128) uint8_t smem_raw[];
+  __shared__ float red[kRowsWarps][NA][TM][kRowsFeat];
   const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5, g = lane >> 2, t = lane & 3;
   const int n0 = blockIdx.x * kRowsFeat;
-  const int ntt = (p.T + kRowsTok - 1) / kRowsTok;
-#pragma unroll 1
-  for (int tt = blockIdx.y; tt < ntt; tt += gridDim.y) {
-    const int t0 = tt * kRowsTok;
-    float acc[NA][4] = {};
-    const bool xl = t0 + g < p.T;
-    const uint16_t* xr = p.x + (size_t)(xl ? t0 + g : 0) * p.ldx;
-    const bool l0 = n0 + g < p.N, l1 = n0 + g + 8 < p.N;
-    const uint16_t* w0[NA];
-    const uint16_t* w1[NA];
-    w0[0] = p.w + (size_t)(l0 ? n0 + g : 0) * p.ldw;
-    w1[0] = p.w + (size_t)(l1 ? n0 + g + 8 : 0) * p.ldw;
-    if constexpr (GATED) {
-      w0[1] = p.w_up + (size_t)(l0 ? n0 + g : 0) * p.ldw_up;
-      w1[1] = p.w_up + (size_t)(l1 ? n0 + g + 8 : 0) * p.ldw_up;
-    }
-#pragma unroll 2
-    for (int k = 64 * warp; k < p.K; k += 64 * kRowsWarps) {
+  const bool wl = n0 + g < p.N;
+  const uint16_t* wr[NA];
+  wr[0] = p.w + (size_t)(wl ? n0 + g : 0) * p.ldw;
+  if constexpr (GATED) wr[1] = p.w_up + (size_t)(wl ? n0 + g : 0) * p.ldw_up;
+  const uint32_t ring = smem_u32(smem_raw) + (uint32_t)(warp * kRowsDepth * NA) * kRowsUnit + 16u * (uint32_t)lane;
+  const int units = (p.K + kKB - 1) / kKB, mine = (units - warp + kRowsWarps - 1) / kRowsWarps;
+  auto fetch = [&](int i) {  // this warp's unit i, or an empty group behind the last
+    if (i < mine) {
+      const int k = kKB * (warp + kRowsWarps * i) + 8 * t;
+      const uint32_t dst = ring + (uint32_t)(i % kRowsDepth * NA) * kRowsUnit;
 #pragma unroll
-      for (int h = 0; h < 2; ++h) {
-        const int kk = k + 32 * h + 8 * t;
-        const uint4 xv = row8(xr, kk, p.K, xl);
-#pragma unroll
-        for (int a = 0; a < NA; ++a) {
-          const uint4 v0 = row8(w0[a], kk, p.K, l0), v1 = row8(w1[a], kk, p.K, l1);
-          mma16816<F16>(acc[a], v0.x, v1.x, v0.y, v1.y, xv.x, xv.y);
-          mma16816<F16>(acc[a], v0.z, v1.z, v0.w, v1.w, xv.z, xv.w);
-        }
+      for (int a = 0; a < NA; ++a) {
+        row_copy16(dst + (uint32_t)a * kRowsUnit, wr[a], k, p.K, wl);
+        row_copy16(dst + (uint32_t)a * kRowsUnit + 512u, wr[a], k + 32, p.K, wl);
       }
     }
+    asm volatile("cp.async.commit_group;" ::: "memory");
+  };
 #pragma unroll
-    for (int a = 0; a < NA; ++a) {
-      red[warp][a][2 * t][g] = acc[a][0];
-      red[warp][a][2 * t + 1][g] = acc[a][1];
-      red[warp][a][2 * t][g + 8] = acc[a][2];
-      red[warp][a][2 * t + 1][g + 8] = acc[a][3];
+  for (int i = 0; i < kRowsDepth - 1; ++i) fetch(i);
+
+  bool xl[NX];
+  const uint16_t* xr[NX];
+#pragma unroll
+  for (int j = 0; j < NX; ++j) {
+    xl[j] = g + 8 * j < p.T;
+    xr[j] = p.x + (size_t)(xl[j] ? g + 8 * j : 0) * p.ldx;
+  }
+  float acc[NA][4] = {};
+#pragma unroll 1
+  for (int i = 0; i < mine; ++i) {
+    const int k = kKB * (warp + kRowsWarps * i) + 8 * t;
+    uint4 xv[NX][2];
+#pragma unroll
+    for (int j = 0; j < NX; ++j) {
+      xv[j][0] = row_load16(xr[j], k, p.K, xl[j]);
+      xv[j][1] = row_load16(xr[j], k + 32, p.K, xl[j]);
     }
-    __syncthreads();
-    if (threadIdx.x < kRowsFeat * kRowsTok) {
-      const int f = threadIdx.x % kRowsFeat, c = threadIdx.x / kRowsFeat;
-      float s[2] = {0.f, 0.f};
+    asm volatile("cp.async.wait_group %0;" ::"n"(kRowsDepth - 2) : "memory");
+    const uint32_t src = ring + (uint32_t)(i % kRowsDepth * NA) * kRowsUnit;
+    uint4 wv[NA][2];
 #pragma unroll
-      for (int a = 0; a < NA; ++a)
+    for (int a = 0; a < NA; ++a)
 #pragma unroll
-        for (int w = 0; w < kRowsWarps; ++w) s[a] += red[w][a][c][f];
-      if (n0 + f < p.N && t0 + c < p.T) finish_one<F16>(p, t0 + c, n0 + f, s[0], s[1]);
-    }
-    __syncthreads();
+      for (int h = 0; h < 2; ++h)
+        asm volatile("ld.shared.v4.u32 {%0,%1,%2,%3}, [%4];"
+                     : "=r"(wv[a][h].x), "=r"(wv[a][h].y), "=r"(wv[a][h].z), "=r"(wv[a][h].w)
+                     : "r"(src + (uint32_t)a * kRowsUnit + 512u * (uint32_t)h)
+                     : "memory");
+    fetch(i + kRowsDepth - 1);  // into the slot that the last turn read
+#pragma unroll
+    for (int a = 0; a < NA; ++a)
+#pragma unroll
+      for (int h = 0; h < 2; ++h) {
+        const uint4 lo = xv[0][h], hi = NX > 1 ? xv[NX - 1][h] : make_uint4(0u, 0u, 0u, 0u);
+        mma16816<F16>(acc[a], lo.x, hi.x, lo.y, hi.y, wv[a][h].x, wv[a][h].y);
+        mma16816<F16>(acc[a], lo.z, hi.z, lo.w, hi.w, wv[a][h].z, wv[a][h].w);
+      }
+  }
+#pragma unroll
+  for (int a = 0; a < NA; ++a)
+#pragma unroll
+    for (int q = 0; q < 2 * NX; ++q) red[warp][a][g + 8 * (q >> 1)][2 * t + (q & 1)] = acc[a][q];
+  __syncthreads();
+  const int f = threadIdx.x % kRowsFeat, c = threadIdx.x / kRowsFeat;
+  if (c < TM && c < p.T && n0 + f < p.N) {
+    float s[2] = {0.f, 0.f};
+#pragma unroll
+    for (int a = 0; a < NA; ++a)
+#pragma unroll
+      for (int w = 0; w < kRowsWarps; ++w) s[a] += red[w][a][c][f];
+    finish_one<F16>(p, c, n0 + f, s[0], s[1]);
   }
 }
 
@@ -302,7 +353,6 @@ __device__ __forceinline__ void read8(uint32_t row, uint32_t c, uint32_t x, floa
   v[0] = a.x, v[1] = a.y, v[2] = a.z, v[3] = a.w, v[4] = b.x, v[5] = b.y, v[6] = b.z, v[7] = b.w;
 }
 
-constexpr int kKB = 64;                  // columns of K per stage: 128 bytes, one swizzle row
 constexpr uint32_t kTile = 128u * 128u;  // bytes of a 128-row operand tile of one stage
 
 // ---- some tokens: a cluster per 128 features, K split over its CTAs --------------------
@@ -346,6 +396,10 @@ __global__ void __launch_bounds__(kSplitThreads, 1)
   const int KB = (p.K + kKB - 1) / kKB;
   const int kb0 = (int)((int64_t)KB * rank / S), kb1 = (int)((int64_t)KB * (rank + 1) / S);
 
+  if (warp == kSplitEpi && lane == 0) {
+    tc::prefetch_map(&map_w);
+    tc::prefetch_map(&map_x);
+  }
   if (tid == 0) {
     for (int s = 0; s < ST; ++s) bar_init(full + 8u * s, 1), bar_init(empty + 8u * s, 1);
     bar_init(accfull, 1);
@@ -429,39 +483,58 @@ __global__ void __launch_bounds__(kSplitThreads, 1)
   if (warp == kSplitEpi + 1) tc::tmem_dealloc(tmem, tmem_cols(NA * NT));
 
   // this CTA's share of the outputs: items of 4 adjacent features of a token
+  // (item j = floats 4j .. of [token][feature]), a few per turn so that their
+  // loads overlap
+  constexpr int kTurn = GATED ? 2 : 4;
   const int nt = min(NT, p.T - t0), items = nt * 32;
   const int i0 = (int)((int64_t)items * rank / S), i1 = (int)((int64_t)items * (rank + 1) / S);
 #pragma unroll 1
-  for (int i = i0 + tid; i < i1; i += kSplitThreads) {
-    const int c = i >> 5, f = 4 * (i & 31), n = n0 + f, t = t0 + c;
-    if (n >= p.N) continue;
-    const bool whole = p.vec && n + 4 <= p.N;
-    float e[4] = {0.f, 0.f, 0.f, 0.f}, v[NA][4] = {};
-    if (p.res && whole) load_row<F16>(p, p.res, (size_t)t * p.ldr + n, e);
-    float4 q[NA][kMaxSplit];
+  for (int i = i0 + tid; i < i1; i += kTurn * kSplitThreads) {
+    float e[kTurn][4] = {}, v[kTurn][NA][4] = {};
 #pragma unroll
-    for (int a = 0; a < NA; ++a)
+    for (int m = 0; m < kTurn; ++m) {
+      const int j = i + m * kSplitThreads, c = j >> 5, n = n0 + 4 * (j & 31);
+      if (j < i1 && p.res && p.vec && n + 4 <= p.N) load_row<F16>(p, p.res, (size_t)(t0 + c) * p.ldr + n, e[m]);
+    }
 #pragma unroll
-      for (uint32_t r = 0; r < kMaxSplit; ++r)
-        if (r < S) q[a][r] = tc::ld_cluster_f4(tc::map_rank(s0 + 512u * (uint32_t)(a * NT + c) + 4u * (uint32_t)f, r));
+    for (int m = 0; m < kTurn; ++m) {
+      const int j = i + m * kSplitThreads;
+      if (j >= i1) continue;
+      float4 q[NA][kMaxSplit];
 #pragma unroll
-    for (int a = 0; a < NA; ++a)
+      for (int a = 0; a < NA; ++a)
 #pragma unroll
-      for (uint32_t r = 0; r < kMaxSplit; ++r)
-        if (r < S) v[a][0] += q[a][r].x, v[a][1] += q[a][r].y, v[a][2] += q[a][r].z, v[a][3] += q[a][r].w;
-    if (whole) {
-      bias_act_gate<GATED>(p, n, v[0], v[NA - 1]);
-      if (p.res) {
+        for (uint32_t r = 0; r < kMaxSplit; ++r)
+          if (r < S) q[a][r] = tc::ld_cluster_f4(tc::map_rank(s0 + 512u * (uint32_t)(a * NT) + 16u * (uint32_t)j, r));
 #pragma unroll
-        for (int k = 0; k < 4; ++k) v[0][k] += e[k];
-      }
-      store_row<F16>(p, (size_t)t * p.ldo + n, v[0]);
-    } else {
+      for (int a = 0; a < NA; ++a)
+#pragma unroll
+        for (uint32_t r = 0; r < kMaxSplit; ++r)
+          if (r < S) {
+            v[m][a][0] += q[a][r].x, v[m][a][1] += q[a][r].y;
+            v[m][a][2] += q[a][r].z, v[m][a][3] += q[a][r].w;
+          }
+    }
+#pragma unroll
+    for (int m = 0; m < kTurn; ++m) {
+      const int j = i + m * kSplitThreads, t = t0 + (j >> 5), n = n0 + 4 * (j & 31);
+      if (j >= i1 || n >= p.N) continue;
+      float(&y)[4] = v[m][0];
+      if (p.vec && n + 4 <= p.N) {
+        bias_act_gate<GATED>(p, n, y, v[m][NA - 1]);
+        if (p.res) {
+#pragma unroll
+          for (int k = 0; k < 4; ++k) y[k] += e[m][k];
+        }
+        store_row<F16>(p, (size_t)t * p.ldo + n, y);
+      } else {
+        float(&u)[4] = v[m][NA - 1];
 #pragma unroll 1
-      for (int k = 0; k < 4; ++k) {
-        if (n + k < p.N) finish_one<F16>(p, t, n + k, v[0][0], v[NA - 1][0]);
-#pragma unroll
-        for (int a = 0; a < NA; ++a) v[a][0] = v[a][1], v[a][1] = v[a][2], v[a][2] = v[a][3];
+        for (int k = 0; k < 4 && n + k < p.N; ++k) {
+          finish_one<F16>(p, t, n + k, y[0], u[0]);
+          y[0] = y[1], y[1] = y[2], y[2] = y[3];
+          if constexpr (GATED) u[0] = u[1], u[1] = u[2], u[2] = u[3];
+        }
       }
     }
   }
@@ -489,6 +562,49 @@ struct PairPlan {
   static constexpr uint32_t kStage = kTile + kBHalf;
   static constexpr int kStages = TN == 256 ? 6 : 8;
   static constexpr uint32_t kSmem = kPairStage0 + kStages * kStage + 1024u;
+};
+
+template <int V>
+struct Const {
+  __device__ constexpr int operator()() const { return V; }
+};
+
+__device__ __forceinline__ void load_bias(const float* bias, int n, int N, float (&v)[8]) {
+#pragma unroll
+  for (int i = 0; i < 8; ++i) v[i] = n + i < N ? __ldg(bias + n + i) : 0.f;
+}
+
+// A lane's residual values of one epilogue step, as they lie in memory: 8
+// adjacent features of PASS rows.  Only where whole rows move in 16 bytes
+// (the other rows read their residual as they are written).
+template <bool F16, int FC, int PASS>
+struct Residual {
+  uint4 raw[PASS][2];
+  __device__ __forceinline__ void fetch(const LinearParams& p, int t, int step, int n, int n0) {
+    if (!p.vec || n0 + FC > p.N) return;
+#pragma unroll
+    for (int q = 0; q < PASS; ++q) {
+      if (t + q * step >= p.T) continue;
+      const size_t at = (size_t)(t + q * step) * p.ldr + n;
+      if (p.out_f32) {
+        raw[q][0] = *reinterpret_cast<const uint4*>(static_cast<const float*>(p.res) + at);
+        raw[q][1] = *reinterpret_cast<const uint4*>(static_cast<const float*>(p.res) + at + 4);
+      } else {
+        raw[q][0] = *reinterpret_cast<const uint4*>(static_cast<const uint16_t*>(p.res) + at);
+      }
+    }
+  }
+  __device__ __forceinline__ void add(const LinearParams& p, int q, float (&v)[8]) const {
+    const uint32_t w[8] = {raw[q][0].x, raw[q][0].y, raw[q][0].z, raw[q][0].w,
+                           raw[q][1].x, raw[q][1].y, raw[q][1].z, raw[q][1].w};
+    if (p.out_f32) {
+#pragma unroll
+      for (int k = 0; k < 8; ++k) v[k] += __uint_as_float(w[k]);
+    } else {
+#pragma unroll
+      for (int k = 0; k < 8; ++k) v[k] += from16<F16>((uint16_t)(w[k >> 1] >> (16 * (k & 1))));
+    }
+  }
 };
 
 // Tile number -> (token tile, feature tile): columns of 8 token tiles, so that
@@ -521,6 +637,10 @@ __global__ void __launch_bounds__(kPairThreads, 1)
   const int ntiles = MT * FT, npairs = gridDim.x / 2, pair = blockIdx.x / 2;
   const int KB = (p.K + kKB - 1) / kKB;
 
+  if (warp == kPairEpi && lane == 0) {
+    tc::prefetch_map(&map_w);
+    tc::prefetch_map(&map_x);
+  }
   if (tid == 0) {
     for (int s = 0; s < ST; ++s) bar_init(full + 8u * s, 1), bar_init(empty + 8u * s, 1);
     for (int b = 0; b < 2; ++b) bar_init(accfull + 8u * b, 1), bar_init(accfree + 8u * b, 2 * kPairEpi);
@@ -602,6 +722,9 @@ __global__ void __launch_bounds__(kPairThreads, 1)
     const int quarter = warp & 3, half = warp >> 2;
     const uint32_t sq = s0 + (uint32_t)warp * 4096u;
     const uint32_t accfree0 = tc::map_rank(accfree, 0);
+    constexpr int LR = FC / 8, RP = 32 / LR, PASS = LR;  // lanes of a row, rows of a pass, passes
+    const int ch = lane % LR;
+    Residual<F16, FC, PASS> res;
     uint32_t it = 0;
     bool ok = true;
 #pragma unroll 1
@@ -609,14 +732,22 @@ __global__ void __launch_bounds__(kPairThreads, 1)
       int mt, ft;
       pair_tile(tile, MT, FT, mt, ft);
       const uint32_t b = it & 1u;
+      const int tok0 = mt * 256 + (int)rank * 128 + 32 * quarter;
+      // residual rows are fetched a step ahead, those of the first step while
+      // the tile's MMAs still run
+      if (p.res) res.fetch(p, tok0 + lane / LR, RP, ft * FN + half * (FN / 2) + 8 * ch, ft * FN + half * (FN / 2));
       ok = __all_sync(kAll, bar_wait(accfull + 8u * b, (it / 2) & 1u));
       if (!ok) break;
       tc::fence_after_sync();
       const uint32_t acc = tmem + b * TN + ((uint32_t)(32 * quarter) << 16);
-      const int tok0 = mt * 256 + (int)rank * 128 + 32 * quarter;
 #pragma unroll 1
       for (int c0 = half * (FN / 2); c0 < (half + 1) * (FN / 2); c0 += FC) {
         const int n0 = ft * FN + c0;
+        const bool whole = p.vec && n0 + FC <= p.N;
+        const int n = n0 + 8 * ch;
+        float bg[8], bu[8];
+        if (p.bias) load_bias(p.bias, n, p.N, bg);
+        if (GATED && p.bias_up) load_bias(p.bias_up, n, p.N, bu);
         {
           uint32_t g[32];
           if constexpr (GATED) {
@@ -641,29 +772,46 @@ __global__ void __launch_bounds__(kPairThreads, 1)
                    __uint_as_float(g[4 * j + 1]), __uint_as_float(g[4 * j + 2]), __uint_as_float(g[4 * j + 3]));
         }
         __syncwarp();
-        const bool whole = p.vec && n0 + FC <= p.N;
-        constexpr int LR = FC / 8, RP = 32 / LR;  // lanes of a row, rows of a pass
-        const int ch = lane % LR, n = n0 + 8 * ch;
-#pragma unroll 1
-        for (int r = lane / LR; r < 32; r += RP) {
-          const int t = tok0 + r;
-          const uint32_t row = sq + (uint32_t)r * 128u, x = (uint32_t)(r & 7);
-          float v[8], u[8], e[8];
-          if (whole && p.res && t < p.T) load_row<F16>(p, p.res, (size_t)t * p.ldr + n, e);
-          read8(row, 2u * ch, x, v);
-          if constexpr (GATED) read8(row, 2u * ch + 4u, x, u);
-          bias_act_gate<GATED>(p, n, v, u);
-          if (!whole) {
-            sts_f4(row + (((2u * ch) ^ x) << 4), v[0], v[1], v[2], v[3]);
-            sts_f4(row + (((2u * ch + 1u) ^ x) << 4), v[4], v[5], v[6], v[7]);
-          } else if (t < p.T) {
-            if (p.res) {
+        // one switch per step: each activation has its own straight-line passes
+        auto passes = [&](auto act) {
 #pragma unroll
-              for (int k = 0; k < 8; ++k) v[k] += e[k];
+          for (int q = 0; q < PASS; ++q) {
+            const int r = lane / LR + q * RP, t = tok0 + r;
+            const uint32_t row = sq + (uint32_t)r * 128u, x = (uint32_t)(r & 7);
+            float v[8];
+            [[maybe_unused]] float u[8];
+            read8(row, 2u * ch, x, v);
+            if constexpr (GATED) read8(row, 2u * ch + 4u, x, u);
+            if (p.bias) {
+#pragma unroll
+              for (int k = 0; k < 8; ++k) v[k] += bg[k];
             }
-            store_row<F16>(p, (size_t)t * p.ldo + n, v);
+            activate(v, act());
+            if constexpr (GATED) {
+              if (p.bias_up) {
+#pragma unroll
+                for (int k = 0; k < 8; ++k) u[k] += bu[k];
+              }
+#pragma unroll
+              for (int k = 0; k < 8; ++k) v[k] *= u[k];
+            }
+            if (!whole) {
+              sts_f4(row + (((2u * ch) ^ x) << 4), v[0], v[1], v[2], v[3]);
+              sts_f4(row + (((2u * ch + 1u) ^ x) << 4), v[4], v[5], v[6], v[7]);
+            } else if (t < p.T) {
+              if (p.res) res.add(p, q, v);
+              store_row<F16>(p, (size_t)t * p.ldo + n, v);
+            }
           }
+        };
+        switch (p.act) {
+          case MOE_ACT_SILU: passes(Const<MOE_ACT_SILU>()); break;
+          case MOE_ACT_GELU: passes(Const<MOE_ACT_GELU>()); break;
+          case MOE_ACT_GELU_TANH: passes(Const<MOE_ACT_GELU_TANH>()); break;
+          case MOE_ACT_RELU: passes(Const<MOE_ACT_RELU>()); break;
+          default: passes(Const<MOE_ACT_NONE>()); break;
         }
+        if (p.res && c0 + FC < (half + 1) * (FN / 2)) res.fetch(p, tok0 + lane / LR, RP, n + FC, n0 + FC);
         __syncwarp();
         if (!whole) {
           // rows that start anywhere, or the last features: one element per lane
@@ -729,20 +877,24 @@ bool make_map(CUtensorMap* m, bool f16, const void* base, int K, int rows, int64
                    CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
 }
 
-// A launch with clusters along x and room for `smem` bytes of dynamic shared
-// memory (the attribute is set once per kernel and device).
+// Allows a kernel `smem` bytes of dynamic shared memory, once per device.
 template <auto Kernel>
-cudaError_t launch_cluster(dim3 grid, int threads, int cluster, uint32_t smem, const CUtensorMap& w,
-                           const CUtensorMap& u, const CUtensorMap& x, const LinearParams& p, cudaStream_t st) {
+cudaError_t allow_smem(uint32_t smem) {
   static bool set[64] = {};
   int dev = 0;
   cudaError_t e = cudaGetDevice(&dev);
+  if (e != cudaSuccess || (dev >= 0 && dev < 64 && set[dev])) return e;
+  e = cudaFuncSetAttribute(Kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)smem);
+  if (e == cudaSuccess && dev >= 0 && dev < 64) set[dev] = true;
+  return e;
+}
+
+// A launch with clusters along x.
+template <auto Kernel>
+cudaError_t launch_cluster(dim3 grid, int threads, int cluster, uint32_t smem, const CUtensorMap& w,
+                           const CUtensorMap& u, const CUtensorMap& x, const LinearParams& p, cudaStream_t st) {
+  const cudaError_t e = allow_smem<Kernel>(smem);
   if (e != cudaSuccess) return e;
-  if (dev < 0 || dev >= 64 || !set[dev]) {
-    e = cudaFuncSetAttribute(Kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)smem);
-    if (e != cudaSuccess) return e;
-    if (dev >= 0 && dev < 64) set[dev] = true;
-  }
   cudaLaunchConfig_t c = {};
   c.gridDim = grid;
   c.blockDim = dim3(threads);
@@ -794,16 +946,19 @@ cudaError_t launch_pair_t(const LinearParams& p, int sms, cudaStream_t st) {
                                                             x, p, st);
 }
 
-template <bool F16, bool GATED>
+template <bool F16, bool GATED, int TM>
 cudaError_t launch_rows(const LinearParams& p, cudaStream_t st) {
-  const int ntt = (p.T + kRowsTok - 1) / kRowsTok;
-  linear_rows_kernel<F16, GATED><<<dim3((p.N + kRowsFeat - 1) / kRowsFeat, ntt), 32 * kRowsWarps, 0, st>>>(p);
+  constexpr uint32_t smem = rows_smem(GATED ? 2 : 1);
+  const cudaError_t e = allow_smem<linear_rows_kernel<F16, GATED, TM>>(smem);
+  if (e != cudaSuccess) return e;
+  linear_rows_kernel<F16, GATED, TM><<<(p.N + kRowsFeat - 1) / kRowsFeat, 32 * kRowsWarps, smem, st>>>(p);
   return cudaGetLastError();
 }
 
 template <bool F16, bool GATED>
 cudaError_t launch_any(const LinearParams& p, int sms, cudaStream_t st) {
-  if (p.T <= 8) return launch_rows<F16, GATED>(p, st);
+  if (p.T <= 8) return launch_rows<F16, GATED, 8>(p, st);
+  if (p.T <= kRowsTok) return launch_rows<F16, GATED, 16>(p, st);
   if (!encoder()) return cudaErrorNotSupported;
   if (p.T <= 256) {
     const int tiles = (p.N + 127) / 128 * (GATED && p.T > 128 ? 2 : 1), KB = (p.K + kKB - 1) / kKB;
