@@ -162,9 +162,10 @@ moe_status moe_topk_from_logits(const moe_config* cfg, const float* logits, int 
  *              index
  *   w          scale * s_idx, or scale * s_idx / sum of the K chosen s with
  *              renormalise (0 when that sum is 0, as for a row of -inf)
- * Values are compared in fp64 (without a bias and within a group the order is
- * that of the logits), so the choice does not hang on how an fp32 sigmoid
- * rounds; weights are rounded to fp32 once.
+ * The choice is that of values compared in fp64 (without a bias experts, and
+ * groups of MOE_GROUP_MAX, are ordered by their logits), so it does not hang
+ * on how an fp32 sigmoid rounds.  Weights are fp32: within 2^-18 of the
+ * formula (typically 2^-23), or within 2^-126.
  * Limits: E <= 2048, K <= 32, n_groups <= 32, K <= topk_groups * E / n_groups. */
 enum { MOE_SCORE_SOFTMAX = 0, MOE_SCORE_SIGMOID = 1 };
 enum { MOE_GROUP_MAX = 0, MOE_GROUP_TOP2 = 1 };

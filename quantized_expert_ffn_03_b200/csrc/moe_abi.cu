@@ -1013,8 +1013,7 @@ moe_status moe_route_from_logits(const moe_route_config* cfg, const void* logits
   if (ldl < cfg->n_experts) return fail(MOE_ERR_INVALID_ARG, "row stride of the logits must be >= n_experts");
   if (!aligned(logits, dtype == MOE_F32 ? 4 : 2) || !aligned(select_bias, 4) || !aligned(idx, 4) || !aligned(w, 4))
     return fail(MOE_ERR_INVALID_ARG, "arrays must be aligned to their elements");
-  DeviceInfo di;
-  if ((s = device_info(&di)) != MOE_OK) return s;
+  const int size = dtype == MOE_F32 ? 4 : 2;
   RouteParams p = {};
   p.T = T;
   p.E = cfg->n_experts;
@@ -1023,6 +1022,10 @@ moe_status moe_route_from_logits(const moe_route_config* cfg, const void* logits
   p.n_groups = cfg->topk_groups == cfg->n_groups ? 1 : cfg->n_groups;  // all kept: no groups
   p.topk_groups = p.n_groups == 1 ? 1 : cfg->topk_groups;
   p.top2 = cfg->group_score == MOE_GROUP_TOP2;
+  p.per = p.E / p.n_groups;
+  p.per_inv = p.per > 1 ? (uint32_t)(((1ull << 32) + p.per - 1) / p.per) : 0;
+  p.vec = aligned(logits, 16) && p.E * size % 16 == 0 && (T == 1 || ldl * size % 16 == 0);
+  for (p.lane_shift = 5; (p.n_groups << p.lane_shift) > 32;) --p.lane_shift;
   p.renorm = cfg->renormalise;
   p.scale = cfg->scale;
   p.logits = logits;
@@ -1030,7 +1033,7 @@ moe_status moe_route_from_logits(const moe_route_config* cfg, const void* logits
   p.bias = select_bias;
   p.idx = idx;
   p.w = w;
-  CUDA_TRY(launch_route(p, dtype, di.sms, stream));
+  CUDA_TRY(launch_route(p, dtype, stream));
   return ok();
 }
 

@@ -32,6 +32,10 @@ struct RouteParams {
   int T, E, K;
   int sigmoid;
   int n_groups, topk_groups, top2;
+  int per;           // experts of a group
+  uint32_t per_inv;  // ceil(2^32 / per): q / per as a high product, for per > 1
+  int lane_shift;    // log2 of the lanes that share a group
+  int vec;           // every row of logits is whole 16-byte pieces on 16-byte boundaries
   int renorm;
   float scale;
   const void* logits;
@@ -43,6 +47,6 @@ struct RouteParams {
 constexpr int kRouteMaxExperts = 2048;
 constexpr int kRouteMaxGroups = 32;
 // dtype: MOE_BF16, MOE_F16 or MOE_F32.
-cudaError_t launch_route(const RouteParams& p, int dtype, int sms, cudaStream_t st);
+cudaError_t launch_route(const RouteParams& p, int dtype, cudaStream_t st);
 
 }  // namespace moe

@@ -5,6 +5,7 @@
 #include <float.h>
 
 #include "../../include/moe.h"
+#include "moe_device.cuh"
 #include "moe_linear.h"
 
 namespace moe {
@@ -39,99 +40,394 @@ __device__ __forceinline__ void warp_best(uint64_t& key, int& at) {
 __device__ __forceinline__ double sigmoid64(double l) { return 1.0 / (1.0 + exp(-l)); }
 
 template <typename T>
-__global__ void __launch_bounds__(32 * kRouteWarps) route_kernel(const RouteParams p) {
-  extern __shared__ uint64_t keys_all[];
-  const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
-  uint64_t* key = keys_all + (size_t)warp * p.E;
-  const int per = p.E / p.n_groups;
-#pragma unroll 1
-  for (int64_t t = (int64_t)blockIdx.x * kRouteWarps + warp; t < p.T; t += (int64_t)gridDim.x * kRouteWarps) {
-    const T* row = static_cast<const T*>(p.logits) + (size_t)t * p.ldl;
-    auto logit = [&](int e) {
-      const float l = load_logit(row + e);
-      return l != l ? -INFINITY : fminf(l, FLT_MAX);
-    };
-    float top = -INFINITY;
-    double sum = 0.0;
-    if (!p.sigmoid) {
-      for (int e = lane; e < p.E; e += 32) top = fmaxf(top, logit(e));
+__device__ __forceinline__ float logit_of(const T* row, int e) {
+  const float l = load_logit(row + e);
+  return l != l ? -INFINITY : fminf(l, FLT_MAX);
+}
+
+__device__ __forceinline__ float warp_maxf(float v) {
 #pragma unroll
-      for (int o = 16; o; o >>= 1) top = fmaxf(top, __shfl_xor_sync(kAll, top, o));
-      if (top == -INFINITY) top = 0.f;  // a row of -inf: every score is 0
-      for (int e = lane; e < p.E; e += 32) sum += exp((double)logit(e) - (double)top);
+  for (int o = 16; o; o >>= 1) v = fmaxf(v, __shfl_xor_sync(kAll, v, o));
+  return v;
+}
+
+// ---- the rules as they stand, in fp64: K rounds over all E values ------------------------
+// Taken for the few tokens whose choice the fp32 values below leave open.
+// key: E words of shared memory of this warp.
+template <typename T>
+__device__ __noinline__ void route_exact(const RouteParams& p, int64_t t, uint64_t* key) {
+  const int lane = threadIdx.x & 31, per = p.E / p.n_groups;
+  const T* row = static_cast<const T*>(p.logits) + (size_t)t * p.ldl;
+  float top = -INFINITY;
+  double sum = 0.0;
+  if (!p.sigmoid) {
+    for (int e = lane; e < p.E; e += 32) top = fmaxf(top, logit_of(row, e));
+    top = warp_maxf(top);
+    if (top == -INFINITY) top = 0.f;  // a row of -inf: every score is 0
+    for (int e = lane; e < p.E; e += 32) sum += exp((double)logit_of(row, e) - (double)top);
 #pragma unroll
-      for (int o = 16; o; o >>= 1) sum += __shfl_xor_sync(kAll, sum, o);
-      if (sum == 0.0) sum = 1.0;
-    }
-    auto score = [&](float l) { return p.sigmoid ? sigmoid64((double)l) : exp((double)l - (double)top) / sum; };
-    const bool by_value = p.bias != nullptr;
-    auto value = [&](int e) { return rank64(score(logit(e)) + (by_value ? (double)__ldg(p.bias + e) : 0.0)); };
-    // the order of experts: by value, or by logit where the score alone decides
-    for (int e = lane; e < p.E; e += 32) key[e] = order64(by_value ? value(e) : (double)logit(e));
-    __syncwarp();
-    uint32_t kept = kAll;
-    if (p.n_groups > 1) {
-      uint64_t gk = 0;
-      if (lane < p.n_groups) {
-        double a = -INFINITY, b = -INFINITY;
-        for (int j = 0; j < per; ++j) {
-          const double v = value(lane * per + j);
-          if (v > a)
-            b = a, a = v;
-          else if (v > b)
-            b = v;
-        }
-        gk = order64(p.top2 && per > 1 ? rank64(a + b) : a);
+    for (int o = 16; o; o >>= 1) sum += __shfl_xor_sync(kAll, sum, o);
+    if (sum == 0.0) sum = 1.0;
+  }
+  auto score = [&](float l) { return p.sigmoid ? sigmoid64((double)l) : exp((double)l - (double)top) / sum; };
+  const bool by_value = p.bias != nullptr;
+  auto value = [&](int e) { return rank64(score(logit_of(row, e)) + (by_value ? (double)__ldg(p.bias + e) : 0.0)); };
+  // what a group is ranked by: values, or without a bias the largest logit
+  auto in_group = [&](int e) { return by_value || p.top2 ? value(e) : (double)logit_of(row, e); };
+  __syncwarp();
+  // the order of experts: by value, or by logit where the score alone decides
+  for (int e = lane; e < p.E; e += 32) key[e] = order64(by_value ? value(e) : (double)logit_of(row, e));
+  __syncwarp();
+  uint32_t kept = kAll;
+  if (p.n_groups > 1) {
+    uint64_t gk = 0;
+    if (lane < p.n_groups) {
+      double a = -INFINITY, b = -INFINITY;
+      for (int j = 0; j < per; ++j) {
+        const double v = in_group(lane * per + j);
+        if (v > a)
+          b = a, a = v;
+        else if (v > b)
+          b = v;
       }
-      kept = 0;
-      for (int i = 0; i < p.topk_groups; ++i) {
-        uint64_t k = kept >> lane & 1u ? 0ull : gk;
-        int at = lane;
-        warp_best(k, at);
-        kept |= 1u << at;
-      }
+      gk = order64(p.top2 && per > 1 ? rank64(a + b) : a);
     }
-    double mine = 0.0, total = 0.0;  // lane k: the score of choice k
-    int chosen = 0;
-    for (int k = 0; k < p.K; ++k) {
-      uint64_t best = 0;
-      int at = p.E;
-      for (int e = lane; e < p.E; e += 32)
-        if (key[e] > best && (p.n_groups == 1 || (kept >> (e / per) & 1u))) best = key[e], at = e;
-      warp_best(best, at);
-      if (lane == (at & 31)) key[at] = 0;
-      const double s = score(logit(at));
-      total += s;
-      if (lane == k) mine = s, chosen = at;
-      __syncwarp();
+    kept = 0;
+    for (int i = 0; i < p.topk_groups; ++i) {
+      uint64_t k = kept >> lane & 1u ? 0ull : gk;
+      int at = lane;
+      warp_best(k, at);
+      kept |= 1u << at;
     }
-    if (lane < p.K) {
-      const double w = p.renorm ? (total > 0.0 ? mine / total : 0.0) : mine;
-      p.idx[(size_t)t * p.K + lane] = chosen;
-      p.w[(size_t)t * p.K + lane] = (float)(w * (double)p.scale);
-    }
+  }
+  double mine = 0.0, total = 0.0;  // lane k: the score of choice k
+  int chosen = 0;
+  for (int k = 0; k < p.K; ++k) {
+    uint64_t best = 0;
+    int at = p.E;
+    for (int e = lane; e < p.E; e += 32)
+      if (key[e] > best && (p.n_groups == 1 || (kept >> (e / per) & 1u))) best = key[e], at = e;
+    warp_best(best, at);
+    if (lane == (at & 31)) key[at] = 0;
+    const double s = score(logit_of(row, at));
+    total += s;
+    if (lane == k) mine = s, chosen = at;
     __syncwarp();
+  }
+  if (lane < p.K) {
+    const double w = p.renorm ? (total > 0.0 ? mine / total : 0.0) : mine;
+    p.idx[(size_t)t * p.K + lane] = chosen;
+    p.w[(size_t)t * p.K + lane] = (float)(w * (double)p.scale);
   }
 }
 
+// ---- one warp per token ------------------------------------------------------------------
+// Values are fp32 here.  With s' the fp32 score of s (__expf is off by at most
+// 2 + 1.16 |x| ulp of e^x, a fast division by 2):
+//   sigmoid   |s' - s| <= 2^-23 ((1 - s) (2 + 1.16 |l|) s + 1/2 + 2 s) < 2^-21
+//   softmax   e^(l - max) is off by at most 2^-22; the row's sum by 20 + ulp,
+//             so |s' - s| <= 2^-18 / sum (no score is larger than 1 / sum)
+// and v' = s' + bias adds 2^-24 |v'|.  A choice that holds by more than these
+// bounds is the fp64 choice.  Where two candidates are closer, theirs (at most
+// 32, one per lane) are computed in fp64; a row with more candidates, or with
+// groups that close, goes to route_exact.  Without a bias experts are ordered
+// by their logits, which needs no bound.
+//
+// Top-K in one go instead of K rounds over E: each lane's largest value; the
+// K-th largest of those 32 is a bound that at least K values reach; the values
+// that reach it (a few more than K of E) are gathered one per lane, and each
+// lane counts how many beat its own.
+__device__ __forceinline__ uint32_t order32(float v) {
+  const uint32_t u = __float_as_uint(v + 0.f);
+  return u >> 31 ? ~u : u | 0x80000000u;
+}
+__device__ __forceinline__ float from_order32(uint32_t k) {
+  return __uint_as_float(k >> 31 ? k & 0x7fffffffu : ~k);
+}
+__device__ __forceinline__ float rank32(float v) { return v != v ? -INFINITY : v; }
+
+// The k-th largest (k from 0) of the lanes' values: a bitonic sort, descending.
+__device__ __forceinline__ float warp_kth(float v, int k) {
+  const int lane = threadIdx.x & 31;
+#pragma unroll
+  for (int size = 2; size <= 32; size <<= 1)
+#pragma unroll
+    for (int o = size >> 1; o; o >>= 1) {
+      const float other = __shfl_xor_sync(kAll, v, o);
+      const bool keep_max = ((lane & o) == 0) == ((lane & size) == 0);
+      v = keep_max ? fmaxf(v, other) : fminf(v, other);
+    }
+  return __shfl_sync(kAll, v, k);
+}
+
+template <bool LONG>
+struct MaskOf {
+  using type = uint32_t;
+};
+template <>
+struct MaskOf<true> {
+  using type = uint64_t;
+};
+__device__ __forceinline__ int count_bits(uint32_t m) { return __popc(m); }
+__device__ __forceinline__ int count_bits(uint64_t m) { return __popcll(m); }
+
+// 16 bytes of logits: W of them.
 template <typename T>
-cudaError_t launch_route_t(const RouteParams& p, int sms, cudaStream_t st) {
+struct Wide {
+  static constexpr int W = 16 / sizeof(T);
+  static __device__ __forceinline__ void load(const T* p, float (&v)[W]) {
+    const uint4 u = __ldg(reinterpret_cast<const uint4*>(p));
+    const T* h = reinterpret_cast<const T*>(&u);
+#pragma unroll
+    for (int i = 0; i < W; ++i) v[i] = to_float(h[i]);
+  }
+  static __device__ __forceinline__ float to_float(float x) { return x; }
+  static __device__ __forceinline__ float to_float(__nv_bfloat16 x) { return __bfloat162float(x); }
+  static __device__ __forceinline__ float to_float(__half x) { return __half2float(x); }
+};
+
+// NV: values per lane, a multiple of Wide<T>::W with 32 NV >= E.
+template <typename T, int NV>
+__global__ void __launch_bounds__(32 * kRouteWarps) route_kernel(const RouteParams p) {
+  constexpr int W = Wide<T>::W;
+  extern __shared__ uint64_t keys_all[];
+  __shared__ int cand_all[kRouteWarps][32];
+  __shared__ float cval_all[kRouteWarps][32];
+  const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
+  const int64_t t = (int64_t)blockIdx.x * kRouteWarps + warp;
+  if (t >= p.T) return;
+  uint64_t* key = keys_all + (size_t)warp * p.E;
+  float* val = reinterpret_cast<float*>(key);  // groups: the values by expert
+  int* cand = cand_all[warp];
+  float* cval = cval_all[warp];
+  const T* row = static_cast<const T*>(p.logits) + (size_t)t * p.ldl;
+  const bool by_value = p.bias != nullptr;
+  // value i of this lane is expert place(i): W adjacent ones per 16-byte load
+  auto place = [&](int i) { return W * (lane + 32 * (i / W)) + i % W; };
+
+  // ---- logits -> v: what experts are ordered by (values, or logits without a bias) ----
+  float v[NV];
+  float top = -INFINITY, inv = 1.f;
+#pragma unroll
+  for (int i = 0; i < NV; i += W) {
+    float l[W];
+    if (p.vec) {
+      if (place(i) < p.E)
+        Wide<T>::load(row + place(i), l);
+      else
+#pragma unroll
+        for (int j = 0; j < W; ++j) l[j] = -INFINITY;
+    } else {
+#pragma unroll
+      for (int j = 0; j < W; ++j) l[j] = place(i + j) < p.E ? load_logit(row + place(i + j)) : -INFINITY;
+    }
+#pragma unroll
+    for (int j = 0; j < W; ++j) v[i + j] = fminf(rank32(l[j]), FLT_MAX);
+  }
+  if (!p.sigmoid) {
+#pragma unroll
+    for (int i = 0; i < NV; ++i) top = fmaxf(top, v[i]);
+    top = warp_maxf(top);
+    if (top == -INFINITY) top = 0.f;  // a row of -inf: every score is 0
+    if (by_value || !p.renorm) {
+      float sum = 0.f;
+#pragma unroll
+      for (int i = 0; i < NV; ++i) sum += __expf(v[i] - top);
+      sum = warp_sum(sum);
+      inv = sum > 0.f ? __fdividef(1.f, sum) : 1.f;
+    }
+  }
+  const float eps = p.sigmoid || !by_value ? 0x1p-21f : 0x1p-18f * inv;  // bound of a score's error
+  auto score = [&](float l) { return p.sigmoid ? __fdividef(1.f, 1.f + __expf(-l)) : __expf(l - top) * inv; };
+  if (by_value) {
+#pragma unroll
+    for (int i = 0; i < NV; ++i)
+      v[i] = place(i) < p.E ? rank32(score(v[i]) + __ldg(p.bias + place(i))) : -INFINITY;
+  }
+
+  // ---- groups: v becomes the values of the kept groups' experts, entry q of
+  // them (value i of a lane: q = lane + 32 i) being expert `expert(q)` ----
+  int entries = p.E;
+  bool open = false;  // the choice is not certain
+  int my_group = 0;
+  const bool grouped = p.n_groups > 1;
+  if (grouped) {
+#pragma unroll
+    for (int i = 0; i < NV; ++i)
+      if (place(i) < p.E) val[place(i)] = v[i];
+    __syncwarp();
+    // `lanes` lanes per group, each the two largest values of its share, walked
+    // from a place of the group's own so that lanes meet different banks
+    const int lanes = 1 << p.lane_shift, grp = lane >> p.lane_shift, sub = lane & (lanes - 1);
+    float a = -INFINITY, b = -INFINITY;
+    const bool plain = by_value || !p.top2;  // no score needed: values, or logits by their largest
+    if (grp < p.n_groups) {
+      int q = sub + grp * lanes;  // (i + grp * lanes) modulo per
+      while (q >= p.per) q -= p.per;
+      const float* mine = val + grp * p.per;
+#pragma unroll 4
+      for (int i = sub; i < p.per; i += lanes) {
+        float x = mine[q];
+        if (!plain) x = score(x);
+        b = fmaxf(b, fminf(a, x));
+        a = fmaxf(a, x);
+        q += lanes;
+        if (q >= p.per) q -= p.per;
+      }
+    }
+    for (int o = 1; o < lanes; o <<= 1) {
+      const float a2 = __shfl_xor_sync(kAll, a, o), b2 = __shfl_xor_sync(kAll, b, o);
+      b = fmaxf(fmaxf(b, b2), fminf(a, a2));
+      a = fmaxf(a, a2);
+    }
+    const float x = p.top2 && p.per > 1 ? rank32(a + b) : a;
+    int rank = 0;  // of this lane's group among all
+    for (int g = 0; g < p.n_groups; ++g) {
+      const float o = __shfl_sync(kAll, x, g << p.lane_shift);
+      rank += o > x || (o == x && g < grp);
+    }
+    const bool first = sub == 0 && grp < p.n_groups, in = first && rank < p.topk_groups;
+    if (in) cand[rank] = grp;
+    if (by_value || p.top2) {
+      // the last kept group has to lead the first one left out by more than
+      // twice the error of a sum of two values
+      const float lo = from_order32(__reduce_min_sync(kAll, in ? order32(x) : ~0u));
+      const float hi = from_order32(__reduce_max_sync(kAll, first && !in ? order32(x) : 0u));
+      open = !(lo - hi > 4.f * eps + 0x1p-21f * fmaxf(fabsf(lo), fabsf(hi)));
+    }
+    entries = p.topk_groups * p.per;
+    __syncwarp();
+    my_group = lane < p.topk_groups ? cand[lane] : 0;
+    __syncwarp();
+  }
+  auto expert = [&](int q) {  // by the whole warp
+    const int g = p.per == 1 ? q : (int)__umulhi((uint32_t)q, p.per_inv);  // q / per
+    return __shfl_sync(kAll, my_group, g & 31) * p.per + q - g * p.per;
+  };
+  if (grouped) {
+#pragma unroll
+    for (int i = 0; i < NV; ++i) {
+      if (32 * i >= entries) {
+        v[i] = -INFINITY;
+      } else {
+        const int q = lane + 32 * i, e = expert(q);
+        v[i] = q < entries ? val[e] : -INFINITY;
+      }
+    }
+  }
+
+  // ---- candidates ----
+  float best = -INFINITY;
+#pragma unroll
+  for (int i = 0; i < NV; ++i) best = fmaxf(best, v[i]);
+  float bound = warp_kth(best, p.K - 1);
+  if (by_value) bound -= 2.f * eps + 0x1p-22f * fabsf(bound);
+  using Mask = typename MaskOf<(NV > 32)>::type;
+  Mask mask = 0;
+#pragma unroll
+  for (int i = 0; i < NV; ++i)
+    if (v[i] >= bound && (grouped ? lane + 32 * i < entries : place(i) < entries)) mask |= (Mask)1 << i;
+  const int mine = count_bits(mask);
+  int at = mine;
+#pragma unroll
+  for (int o = 1; o < 32; o <<= 1) {
+    const int x = __shfl_up_sync(kAll, at, o);
+    if (lane >= o) at += x;
+  }
+  const int count = __shfl_sync(kAll, at, 31);
+  if (count > 32) open = true;
+  if (!open) {
+    at -= mine;
+#pragma unroll
+    for (int i = 0; i < NV; ++i)
+      if (mask >> i & 1) {
+        cand[at] = grouped ? lane + 32 * i : place(i);
+        cval[at++] = v[i];
+      }
+  }
+  __syncwarp();
+
+  // ---- one candidate per lane: its rank, whether the order is certain ----
+  if (!open) {
+    const bool live = lane < count;
+    int e = live ? cand[lane] : 0;
+    if (grouped) e = expert(e);
+    const float x = live ? cval[lane] : -INFINITY;
+    const float l = live ? logit_of(row, e) : -INFINITY;
+    const float tol = fmaf(0x1p-23f, fabsf(x), 2.f * eps);
+    int rank = 0;
+    bool close = false;
+#pragma unroll 4
+    for (int j = 0; j < count; ++j) {
+      const float o = __shfl_sync(kAll, x, j);
+      const int oe = __shfl_sync(kAll, e, j);
+      rank += o > x || (o == x && oe < e);
+      close = close || (j != lane && !(fabsf(o - x) > tol));
+    }
+    if (by_value && __any_sync(kAll, live && rank < p.K && close)) {
+      // candidates' values in fp64
+      double sum = 1.0;
+      if (!p.sigmoid) {
+        sum = 0.0;
+        for (int i = lane; i < p.E; i += 32) sum += exp((double)logit_of(row, i) - (double)top);
+#pragma unroll
+        for (int o = 16; o; o >>= 1) sum += __shfl_xor_sync(kAll, sum, o);
+        if (sum == 0.0) sum = 1.0;
+      }
+      const double d = rank64((p.sigmoid ? sigmoid64((double)l) : exp((double)l - (double)top) / sum) +
+                              (double)__ldg(p.bias + e));
+      rank = 0;
+      for (int j = 0; j < count; ++j) {
+        const double o = __shfl_sync(kAll, d, j);
+        const int oe = __shfl_sync(kAll, e, j);
+        rank += o > d || (o == d && oe < e);
+      }
+    }
+    const bool in = live && rank < p.K;
+    // weights from the accurate exponential
+    float w = p.sigmoid ? __fdiv_rn(1.f, 1.f + expf(-l)) : expf(l - top) * inv;
+    if (p.renorm) {
+      const float total = warp_sum(in ? w : 0.f);
+      w = __fdiv_rn(w, total);
+      open = !(total >= 0x1p-100f);  // scores near or below fp32's range (or none): fp64
+    }
+    if (!open) {
+      if (in) {
+        p.idx[(size_t)t * p.K + rank] = e;
+        p.w[(size_t)t * p.K + rank] = w * p.scale;
+      }
+      return;
+    }
+  }
+  route_exact<T>(p, t, key);
+}
+
+template <typename T, int NV>
+cudaError_t launch_route_nv(const RouteParams& p, cudaStream_t st) {
   const size_t smem = sizeof(uint64_t) * kRouteWarps * (size_t)p.E;
-  cudaError_t e = cudaFuncSetAttribute(route_kernel<T>, cudaFuncAttributeMaxDynamicSharedMemorySize,
-                                       (int)(sizeof(uint64_t) * kRouteWarps * kRouteMaxExperts));
-  if (e != cudaSuccess) return e;
-  const int64_t blocks = ((int64_t)p.T + kRouteWarps - 1) / kRouteWarps;
-  const int grid = (int)(blocks < 32 * sms ? blocks : 32 * sms);
-  route_kernel<T><<<grid, 32 * kRouteWarps, smem, st>>>(p);
+  if (smem > 48 * 1024) {  // the largest E only
+    const cudaError_t e = cudaFuncSetAttribute(route_kernel<T, NV>, cudaFuncAttributeMaxDynamicSharedMemorySize,
+                                               (int)(sizeof(uint64_t) * kRouteWarps * kRouteMaxExperts));
+    if (e != cudaSuccess) return e;
+  }
+  route_kernel<T, NV><<<(p.T + kRouteWarps - 1) / kRouteWarps, 32 * kRouteWarps, smem, st>>>(p);
   return cudaGetLastError();
+}
+
+template <typename T>
+cudaError_t launch_route_t(const RouteParams& p, cudaStream_t st) {
+  if (p.E <= 256) return launch_route_nv<T, 8>(p, st);
+  if (p.E <= 512) return launch_route_nv<T, 16>(p, st);
+  if (p.E <= 1024) return launch_route_nv<T, 32>(p, st);
+  return launch_route_nv<T, 64>(p, st);
 }
 
 }  // namespace
 
-cudaError_t launch_route(const RouteParams& p, int dtype, int sms, cudaStream_t st) {
-  if (dtype == MOE_F32) return launch_route_t<float>(p, sms, st);
-  if (dtype == MOE_BF16) return launch_route_t<__nv_bfloat16>(p, sms, st);
-  return launch_route_t<__half>(p, sms, st);
+cudaError_t launch_route(const RouteParams& p, int dtype, cudaStream_t st) {
+  if (dtype == MOE_F32) return launch_route_t<float>(p, st);
+  if (dtype == MOE_BF16) return launch_route_t<__nv_bfloat16>(p, st);
+  return launch_route_t<__half>(p, st);
 }
 
 }  // namespace moe
