@@ -51,87 +51,211 @@ __device__ __forceinline__ float warp_maxf(float v) {
   return v;
 }
 
-// ---- the rules as they stand, in fp64: K rounds over all E values ------------------------
-// Taken for the few tokens whose choice the fp32 values below leave open.
-// key: E words of shared memory of this warp.
+// ---- the choice in fp64, for what the fp32 values below leave open ------------------------
+
+// A row's scores in fp64; top: its largest logit (0 for a row of -inf).
+struct Scorer64 {
+  bool sigmoid;
+  double top, sum;
+  __device__ __forceinline__ double operator()(float l) const {
+    return sigmoid ? sigmoid64((double)l) : exp((double)l - top) / sum;
+  }
+};
 template <typename T>
-__device__ __noinline__ void route_exact(const RouteParams& p, int64_t t, uint64_t* key) {
-  const int lane = threadIdx.x & 31, per = p.E / p.n_groups;
-  const T* row = static_cast<const T*>(p.logits) + (size_t)t * p.ldl;
-  float top = -INFINITY;
-  double sum = 0.0;
+__device__ __forceinline__ Scorer64 scorer64(const RouteParams& p, const T* row, float top) {
+  Scorer64 s = {p.sigmoid != 0, (double)top, 1.0};
   if (!p.sigmoid) {
+    double sum = 0.0;
+#pragma unroll 4
+    for (int e = threadIdx.x & 31; e < p.E; e += 32) sum += exp((double)logit_of(row, e) - s.top);
+#pragma unroll
+    for (int o = 16; o; o >>= 1) sum += __shfl_xor_sync(kAll, sum, o);
+    if (sum > 0.0) s.sum = sum;
+  }
+  return s;
+}
+template <typename T>
+__device__ __forceinline__ double value64(const RouteParams& p, const Scorer64& score, const T* row, int e) {
+  return rank64(score(logit_of(row, e)) + (p.bias ? (double)__ldg(p.bias + e) : 0.0));
+}
+
+// The rank of this lane's candidate, expert e (the first `count` lanes have one).
+template <typename T>
+__device__ __noinline__ int rank_candidates64(const RouteParams& p, const T* row, float top, int e, int count) {
+  const double d = value64(p, scorer64(p, row, top), row, e);
+  int rank = 0;
+  for (int j = 0; j < count; ++j) {
+    const double o = __shfl_sync(kAll, d, j);
+    const int oe = __shfl_sync(kAll, e, j);
+    rank += o > d || (o == d && oe < e);
+  }
+  return rank;
+}
+
+// Whether this lane's group is kept, where lo (the least value kept) and hi (the
+// largest left out) are within tol: fp64 values for the groups that close, in
+// the rank order of the others.  x: the lane's group's fp32 value; first: the
+// lane stands for its group.
+template <typename T>
+__device__ __noinline__ bool keep_group64(const RouteParams& p, const T* row, float top, float x, bool first, float lo,
+                                          float hi, float tol) {
+  const int lane = threadIdx.x & 31, grp = lane >> p.lane_shift;
+  const Scorer64 score = scorer64(p, row, top);
+  const bool sure = first && x > hi + tol, near = first && !sure && !(x < lo - tol);
+  const int left = p.topk_groups - __popc(__ballot_sync(kAll, sure));
+  const uint32_t nears = __ballot_sync(kAll, near);
+  double mine = 0.0;
+  for (uint32_t m = nears; m; m &= m - 1) {
+    const int at = __ffs(m) - 1, g = at >> p.lane_shift;
+    double a = -INFINITY, b = -INFINITY;
+    for (int j = lane; j < p.per; j += 32) {
+      const double v = value64(p, score, row, g * p.per + j);
+      b = fmax(b, fmin(a, v));
+      a = fmax(a, v);
+    }
+#pragma unroll 1
+    for (int o = 16; o; o >>= 1) {
+      const double a2 = __shfl_xor_sync(kAll, a, o), b2 = __shfl_xor_sync(kAll, b, o);
+      b = fmax(fmax(b, b2), fmin(a, a2));
+      a = fmax(a, a2);
+    }
+    if (lane == at) mine = p.top2 && p.per > 1 ? rank64(a + b) : a;
+  }
+  int rank = 0;
+  for (uint32_t m = nears; m; m &= m - 1) {
+    const int at = __ffs(m) - 1;
+    const double o = __shfl_sync(kAll, mine, at);
+    rank += o > mine || (o == mine && (at >> p.lane_shift) < grp);
+  }
+  return sure || (near && rank < left);
+}
+
+// A whole token.  key: E words of shared memory of this warp; cand: 32 more.
+template <typename T>
+__device__ __noinline__ void route_exact(const RouteParams& p, int64_t t, uint64_t* key, int* cand) {
+  const int lane = threadIdx.x & 31;
+  const T* row = static_cast<const T*>(p.logits) + (size_t)t * p.ldl;
+  const bool by_value = p.bias != nullptr;
+  float top = 0.f;
+  if (!p.sigmoid) {
+    top = -INFINITY;
     for (int e = lane; e < p.E; e += 32) top = fmaxf(top, logit_of(row, e));
     top = warp_maxf(top);
     if (top == -INFINITY) top = 0.f;  // a row of -inf: every score is 0
-    for (int e = lane; e < p.E; e += 32) sum += exp((double)logit_of(row, e) - (double)top);
-#pragma unroll
-    for (int o = 16; o; o >>= 1) sum += __shfl_xor_sync(kAll, sum, o);
-    if (sum == 0.0) sum = 1.0;
   }
-  auto score = [&](float l) { return p.sigmoid ? sigmoid64((double)l) : exp((double)l - (double)top) / sum; };
-  const bool by_value = p.bias != nullptr;
-  auto value = [&](int e) { return rank64(score(logit_of(row, e)) + (by_value ? (double)__ldg(p.bias + e) : 0.0)); };
-  // what a group is ranked by: values, or without a bias the largest logit
-  auto in_group = [&](int e) { return by_value || p.top2 ? value(e) : (double)logit_of(row, e); };
+  const Scorer64 score = scorer64(p, row, top);
   __syncwarp();
-  // the order of experts: by value, or by logit where the score alone decides
-  for (int e = lane; e < p.E; e += 32) key[e] = order64(by_value ? value(e) : (double)logit_of(row, e));
-  __syncwarp();
+
+  // kept groups, a bit each: by their values, or without a bias by their largest logit
   uint32_t kept = kAll;
   if (p.n_groups > 1) {
-    uint64_t gk = 0;
-    if (lane < p.n_groups) {
-      double a = -INFINITY, b = -INFINITY;
-      for (int j = 0; j < per; ++j) {
-        const double v = in_group(lane * per + j);
-        if (v > a)
-          b = a, a = v;
-        else if (v > b)
-          b = v;
-      }
-      gk = order64(p.top2 && per > 1 ? rank64(a + b) : a);
-    }
-    kept = 0;
-    for (int i = 0; i < p.topk_groups; ++i) {
-      uint64_t k = kept >> lane & 1u ? 0ull : gk;
-      int at = lane;
-      warp_best(k, at);
-      kept |= 1u << at;
-    }
-  }
-  double mine = 0.0, total = 0.0;  // lane k: the score of choice k
-  int chosen = 0;
-  for (int k = 0; k < p.K; ++k) {
-    uint64_t best = 0;
-    int at = p.E;
+    double* dv = reinterpret_cast<double*>(key);
+#pragma unroll 4
     for (int e = lane; e < p.E; e += 32)
-      if (key[e] > best && (p.n_groups == 1 || (kept >> (e / per) & 1u))) best = key[e], at = e;
-    warp_best(best, at);
-    if (lane == (at & 31)) key[at] = 0;
-    const double s = score(logit_of(row, at));
-    total += s;
-    if (lane == k) mine = s, chosen = at;
+      dv[e] = by_value || p.top2 ? value64(p, score, row, e) : (double)logit_of(row, e);
+    __syncwarp();
+    const int lanes = 1 << p.lane_shift, grp = lane >> p.lane_shift, sub = lane & (lanes - 1);
+    double a = -INFINITY, b = -INFINITY;
+    if (grp < p.n_groups)
+      for (int j = sub; j < p.per; j += lanes) {
+        const double x = dv[grp * p.per + j];
+        b = fmax(b, fmin(a, x));
+        a = fmax(a, x);
+      }
+    for (int o = 1; o < lanes; o <<= 1) {
+      const double a2 = __shfl_xor_sync(kAll, a, o), b2 = __shfl_xor_sync(kAll, b, o);
+      b = fmax(fmax(b, b2), fmin(a, a2));
+      a = fmax(a, a2);
+    }
+    const double x = p.top2 && p.per > 1 ? rank64(a + b) : a;
+    int rank = 0;
+    for (int g = 0; g < p.n_groups; ++g) {
+      const double o = __shfl_sync(kAll, x, g << p.lane_shift);
+      rank += o > x || (o == x && g < grp);
+    }
+    kept = __reduce_or_sync(kAll, sub == 0 && grp < p.n_groups && rank < p.topk_groups ? 1u << grp : 0u);
     __syncwarp();
   }
-  if (lane < p.K) {
-    const double w = p.renorm ? (total > 0.0 ? mine / total : 0.0) : mine;
-    p.idx[(size_t)t * p.K + lane] = chosen;
-    p.w[(size_t)t * p.K + lane] = (float)(w * (double)p.scale);
+
+  // experts by value, or by logit where the score alone decides; 0: left out
+  uint64_t best = 0;
+#pragma unroll 4
+  for (int e = lane; e < p.E; e += 32) {
+    const bool in = p.n_groups == 1 || (kept >> (e / p.per) & 1u);
+    const uint64_t k = in ? order64(by_value ? value64(p, score, row, e) : (double)logit_of(row, e)) : 0ull;
+    key[e] = k;
+    best = k > best ? k : best;
+  }
+  // candidates: those that reach the K-th of the lanes' largest, if they are
+  // few enough; all of them count where fewer than K lanes have any
+#pragma unroll 1
+  for (int size = 2; size <= 32; size <<= 1)
+#pragma unroll 1
+    for (int o = size >> 1; o; o >>= 1) {
+      const uint64_t other = __shfl_xor_sync(kAll, best, o);
+      const bool keep_max = ((lane & o) == 0) == ((lane & size) == 0);
+      best = (other > best) == keep_max ? other : best;
+    }
+  const uint64_t kth = __shfl_sync(kAll, best, p.K - 1), bound = kth ? kth : 1ull;
+  int count = 0;
+  for (int e0 = 0; e0 < p.E; e0 += 32) {
+    const int e = e0 + lane;
+    const bool in = e < p.E && key[e] >= bound;
+    const uint32_t m = __ballot_sync(kAll, in);
+    const int at = count + __popc(m & ((1u << lane) - 1u));
+    if (in && at < 32) cand[at] = e;
+    count += __popc(m);
+  }
+  __syncwarp();
+  int chosen = 0, rank = 32;
+  if (count <= 32) {
+    chosen = lane < count ? cand[lane] : 0;
+    const uint64_t mine = lane < count ? key[chosen] : 0ull;
+    if (lane < count) {
+      rank = 0;
+      for (int j = 0; j < count; ++j) {
+        const int e = cand[j];
+        const uint64_t k = key[e];
+        rank += k > mine || (k == mine && e < chosen);
+      }
+    }
+  } else {
+    // many equal values: K rounds, lane k keeps the choice of round k
+    for (int k = 0; k < p.K; ++k) {
+      uint64_t most = 0;
+      int at = p.E;
+      for (int e = lane; e < p.E; e += 32)
+        if (key[e] > most) most = key[e], at = e;
+      warp_best(most, at);
+      if (lane == (at & 31)) key[at] = 0;
+      if (lane == k) chosen = at, rank = k;
+      __syncwarp();
+    }
+  }
+  double w = rank < p.K ? score(logit_of(row, chosen)) : 0.0;
+  if (p.renorm) {
+    double total = w;
+#pragma unroll
+    for (int o = 16; o; o >>= 1) total += __shfl_xor_sync(kAll, total, o);
+    w = total > 0.0 ? w / total : 0.0;
+  }
+  if (rank < p.K) {
+    p.idx[(size_t)t * p.K + rank] = chosen;
+    p.w[(size_t)t * p.K + rank] = (float)(w * (double)p.scale);
   }
 }
 
 // ---- one warp per token ------------------------------------------------------------------
-// Values are fp32 here.  With s' the fp32 score of s (__expf is off by at most
-// 2 + 1.16 |x| ulp of e^x, a fast division by 2):
+// Values are fp32 here.  With s' the fp32 score of s (fast_exp is off by at most
+// 2 + 1.16 |x| ulp, a fast division by 2):
 //   sigmoid   |s' - s| <= 2^-23 ((1 - s) (2 + 1.16 |l|) s + 1/2 + 2 s) < 2^-21
 //   softmax   e^(l - max) is off by at most 2^-22; the row's sum by 20 + ulp,
 //             so |s' - s| <= 2^-18 / sum (no score is larger than 1 / sum)
 // and v' = s' + bias adds 2^-24 |v'|.  A choice that holds by more than these
-// bounds is the fp64 choice.  Where two candidates are closer, theirs (at most
-// 32, one per lane) are computed in fp64; a row with more candidates, or with
-// groups that close, goes to route_exact.  Without a bias experts are ordered
-// by their logits, which needs no bound.
+// bounds is the fp64 choice; where candidates or groups are closer (a token in
+// some hundreds), theirs alone are computed in fp64.  A row with more candidates
+// than lanes goes to route_exact.  Without a bias experts are ordered by their
+// logits, which needs no bound.
 //
 // Top-K in one go instead of K rounds over E: each lane's largest value; the
 // K-th largest of those 32 is a bound that at least K values reach; the values
@@ -144,7 +268,13 @@ __device__ __forceinline__ uint32_t order32(float v) {
 __device__ __forceinline__ float from_order32(uint32_t k) {
   return __uint_as_float(k >> 31 ? k & 0x7fffffffu : ~k);
 }
-__device__ __forceinline__ float rank32(float v) { return v != v ? -INFINITY : v; }
+__device__ __forceinline__ float rank32(float v) { return fmaxf(v, -INFINITY); }  // NaN ranks as -inf
+// e^x to within 2 + 1.16 |x| ulp; 0 below fp32's normal range.
+__device__ __forceinline__ float fast_exp(float x) {
+  float y;
+  asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x * 1.4426950408889634f));
+  return y;
+}
 
 // The k-th largest (k from 0) of the lanes' values: a bitonic sort, descending.
 __device__ __forceinline__ float warp_kth(float v, int k) {
@@ -170,6 +300,8 @@ struct MaskOf<true> {
 };
 __device__ __forceinline__ int count_bits(uint32_t m) { return __popc(m); }
 __device__ __forceinline__ int count_bits(uint64_t m) { return __popcll(m); }
+__device__ __forceinline__ int lowest_bit(uint32_t m) { return __ffs(m) - 1; }
+__device__ __forceinline__ int lowest_bit(uint64_t m) { return __ffsll(m) - 1; }
 
 // 16 bytes of logits: W of them.
 template <typename T>
@@ -188,10 +320,11 @@ struct Wide {
 
 // NV: values per lane, a multiple of Wide<T>::W with 32 NV >= E.
 template <typename T, int NV>
-__global__ void __launch_bounds__(32 * kRouteWarps) route_kernel(const RouteParams p) {
+__global__ void __launch_bounds__(32 * kRouteWarps, NV <= 16 ? 7 : NV == 32 ? 5 : 3) route_kernel(const RouteParams p) {
   constexpr int W = Wide<T>::W;
   extern __shared__ uint64_t keys_all[];
   __shared__ int cand_all[kRouteWarps][32];
+  __shared__ uint64_t ckey_all[kRouteWarps][32];
   __shared__ float cval_all[kRouteWarps][32];
   const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
   const int64_t t = (int64_t)blockIdx.x * kRouteWarps + warp;
@@ -199,6 +332,7 @@ __global__ void __launch_bounds__(32 * kRouteWarps) route_kernel(const RoutePara
   uint64_t* key = keys_all + (size_t)warp * p.E;
   float* val = reinterpret_cast<float*>(key);  // groups: the values by expert
   int* cand = cand_all[warp];
+  uint64_t* ckey = ckey_all[warp];
   float* cval = cval_all[warp];
   const T* row = static_cast<const T*>(p.logits) + (size_t)t * p.ldl;
   const bool by_value = p.bias != nullptr;
@@ -222,7 +356,7 @@ __global__ void __launch_bounds__(32 * kRouteWarps) route_kernel(const RoutePara
       for (int j = 0; j < W; ++j) l[j] = place(i + j) < p.E ? load_logit(row + place(i + j)) : -INFINITY;
     }
 #pragma unroll
-    for (int j = 0; j < W; ++j) v[i + j] = fminf(rank32(l[j]), FLT_MAX);
+    for (int j = 0; j < W; ++j) v[i + j] = fminf(rank32(l[j]), FLT_MAX);  // (-inf behind the last expert)
   }
   if (!p.sigmoid) {
 #pragma unroll
@@ -232,13 +366,13 @@ __global__ void __launch_bounds__(32 * kRouteWarps) route_kernel(const RoutePara
     if (by_value || !p.renorm) {
       float sum = 0.f;
 #pragma unroll
-      for (int i = 0; i < NV; ++i) sum += __expf(v[i] - top);
+      for (int i = 0; i < NV; ++i) sum += fast_exp(v[i] - top);
       sum = warp_sum(sum);
       inv = sum > 0.f ? __fdividef(1.f, sum) : 1.f;
     }
   }
   const float eps = p.sigmoid || !by_value ? 0x1p-21f : 0x1p-18f * inv;  // bound of a score's error
-  auto score = [&](float l) { return p.sigmoid ? __fdividef(1.f, 1.f + __expf(-l)) : __expf(l - top) * inv; };
+  auto score = [&](float l) { return p.sigmoid ? __fdividef(1.f, 1.f + fast_exp(-l)) : fast_exp(l - top) * inv; };
   if (by_value) {
 #pragma unroll
     for (int i = 0; i < NV; ++i)
@@ -248,7 +382,7 @@ __global__ void __launch_bounds__(32 * kRouteWarps) route_kernel(const RoutePara
   // ---- groups: v becomes the values of the kept groups' experts, entry q of
   // them (value i of a lane: q = lane + 32 i) being expert `expert(q)` ----
   int entries = p.E;
-  bool open = false;  // the choice is not certain
+  bool open = false;  // not to be decided here
   int my_group = 0;
   const bool grouped = p.n_groups > 1;
   if (grouped) {
@@ -286,15 +420,18 @@ __global__ void __launch_bounds__(32 * kRouteWarps) route_kernel(const RoutePara
       const float o = __shfl_sync(kAll, x, g << p.lane_shift);
       rank += o > x || (o == x && g < grp);
     }
-    const bool first = sub == 0 && grp < p.n_groups, in = first && rank < p.topk_groups;
-    if (in) cand[rank] = grp;
+    const bool first = sub == 0 && grp < p.n_groups;
+    bool in = first && rank < p.topk_groups;
     if (by_value || p.top2) {
       // the last kept group has to lead the first one left out by more than
       // twice the error of a sum of two values
       const float lo = from_order32(__reduce_min_sync(kAll, in ? order32(x) : ~0u));
       const float hi = from_order32(__reduce_max_sync(kAll, first && !in ? order32(x) : 0u));
-      open = !(lo - hi > 4.f * eps + 0x1p-21f * fmaxf(fabsf(lo), fabsf(hi)));
+      const float tol = 4.f * eps + 0x1p-21f * fmaxf(fabsf(lo), fabsf(hi));
+      if (!(lo - hi > tol)) in = keep_group64(p, row, top, x, first, lo, hi, tol);
     }
+    const uint32_t kept = __ballot_sync(kAll, in);
+    if (in) cand[__popc(kept & ((1u << lane) - 1u))] = grp;
     entries = p.topk_groups * p.per;
     __syncwarp();
     my_group = lane < p.topk_groups ? cand[lane] : 0;
@@ -326,7 +463,12 @@ __global__ void __launch_bounds__(32 * kRouteWarps) route_kernel(const RoutePara
   Mask mask = 0;
 #pragma unroll
   for (int i = 0; i < NV; ++i)
-    if (v[i] >= bound && (grouped ? lane + 32 * i < entries : place(i) < entries)) mask |= (Mask)1 << i;
+    if (v[i] >= bound) mask |= (Mask)1 << i;
+  if (bound == -INFINITY) {  // the places behind the last expert hold -inf too
+#pragma unroll
+    for (int i = 0; i < NV; ++i)
+      if ((grouped ? lane + 32 * i : place(i)) >= entries) mask &= ~((Mask)1 << i);
+  }
   const int mine = count_bits(mask);
   int at = mine;
 #pragma unroll
@@ -337,13 +479,10 @@ __global__ void __launch_bounds__(32 * kRouteWarps) route_kernel(const RoutePara
   const int count = __shfl_sync(kAll, at, 31);
   if (count > 32) open = true;
   if (!open) {
-    at -= mine;
-#pragma unroll
-    for (int i = 0; i < NV; ++i)
-      if (mask >> i & 1) {
-        cand[at] = grouped ? lane + 32 * i : place(i);
-        cval[at++] = v[i];
-      }
+    for (at -= mine; mask; mask &= mask - 1) {
+      const int i = lowest_bit(mask);
+      cand[at++] = grouped ? lane + 32 * i : place(i);
+    }
   }
   __syncwarp();
 
@@ -352,36 +491,23 @@ __global__ void __launch_bounds__(32 * kRouteWarps) route_kernel(const RoutePara
     const bool live = lane < count;
     int e = live ? cand[lane] : 0;
     if (grouped) e = expert(e);
-    const float x = live ? cval[lane] : -INFINITY;
-    const float l = live ? logit_of(row, e) : -INFINITY;
-    const float tol = fmaf(0x1p-23f, fabsf(x), 2.f * eps);
+    // its value again, by the same operations
+    const float l = fminf(rank32(load_logit(row + e)), FLT_MAX);
+    const float x = by_value ? rank32(score(l) + __ldg(p.bias + e)) : l;
+    const uint64_t mine64 = live ? (uint64_t)order32(x) << 32 | (uint32_t)~e : 0ull;
+    ckey[lane] = mine64;
+    __syncwarp();
     int rank = 0;
-    bool close = false;
 #pragma unroll 4
-    for (int j = 0; j < count; ++j) {
-      const float o = __shfl_sync(kAll, x, j);
-      const int oe = __shfl_sync(kAll, e, j);
-      rank += o > x || (o == x && oe < e);
-      close = close || (j != lane && !(fabsf(o - x) > tol));
-    }
-    if (by_value && __any_sync(kAll, live && rank < p.K && close)) {
-      // candidates' values in fp64
-      double sum = 1.0;
-      if (!p.sigmoid) {
-        sum = 0.0;
-        for (int i = lane; i < p.E; i += 32) sum += exp((double)logit_of(row, i) - (double)top);
-#pragma unroll
-        for (int o = 16; o; o >>= 1) sum += __shfl_xor_sync(kAll, sum, o);
-        if (sum == 0.0) sum = 1.0;
-      }
-      const double d = rank64((p.sigmoid ? sigmoid64((double)l) : exp((double)l - (double)top) / sum) +
-                              (double)__ldg(p.bias + e));
-      rank = 0;
-      for (int j = 0; j < count; ++j) {
-        const double o = __shfl_sync(kAll, d, j);
-        const int oe = __shfl_sync(kAll, e, j);
-        rank += o > d || (o == d && oe < e);
-      }
+    for (int j = 0; j < count; ++j) rank += ckey[j] > mine64;
+    if (by_value) {
+      // values in descending order, each against the next: the first K must
+      // lead by more than the two errors
+      if (live) cval[rank] = x;
+      __syncwarp();
+      const float hi = cval[lane], lo = cval[(lane + 1) & 31];
+      const bool close = lane < p.K && lane + 1 < count && !(hi - lo > fmaf(0x1p-23f, fabsf(hi) + fabsf(lo), 2.f * eps));
+      if (__any_sync(kAll, close)) rank = rank_candidates64(p, row, top, e, count);
     }
     const bool in = live && rank < p.K;
     // weights from the accurate exponential
@@ -389,7 +515,7 @@ __global__ void __launch_bounds__(32 * kRouteWarps) route_kernel(const RoutePara
     if (p.renorm) {
       const float total = warp_sum(in ? w : 0.f);
       w = __fdiv_rn(w, total);
-      open = !(total >= 0x1p-100f);  // scores near or below fp32's range (or none): fp64
+      open = open || !(total >= 0x1p-100f);  // scores near or below fp32's range (or none): fp64
     }
     if (!open) {
       if (in) {
@@ -399,7 +525,7 @@ __global__ void __launch_bounds__(32 * kRouteWarps) route_kernel(const RoutePara
       return;
     }
   }
-  route_exact<T>(p, t, key);
+  route_exact<T>(p, t, key, cand);
 }
 
 template <typename T, int NV>

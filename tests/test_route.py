@@ -133,6 +133,22 @@ def test_ties_go_to_the_lower_index(score, groups, keep):
 
 @pytest.mark.gpu
 @pytest.mark.parametrize("score", ["softmax", "sigmoid"])
+@pytest.mark.parametrize("E,groups,keep", [(30, 1, 1), (64, 16, 5), (512, 16, 4)])
+@pytest.mark.parametrize("spread", [2e-6, 1e-4, 1e-2])
+def test_near_ties_follow_fp64(score, E, groups, keep, spread):
+    """Logits a few fp32 steps apart and biases that nearly make up for them: fp32 scores cannot order these values."""
+    import torch
+    r = np.random.RandomState(E)
+    l = np.float32(2.0) + (spread * r.standard_normal((300, E))).astype(np.float32)
+    l = torch.from_numpy(l.astype(np.float32)).cuda()
+    for bias in (np.zeros(E, np.float32), (0.1 * spread * r.standard_normal(E)).astype(np.float32)):
+        for gs in ("max", "top2"):
+            for renorm in (True, False):
+                check(l, 6, bias, score=score, groups=groups, keep=keep, group_score=gs, renorm=renorm)
+
+
+@pytest.mark.gpu
+@pytest.mark.parametrize("score", ["softmax", "sigmoid"])
 @pytest.mark.parametrize("renorm", [True, False])
 @pytest.mark.parametrize("groups,keep", [(1, 1), (6, 2)])
 def test_masked_and_non_finite_rows(score, renorm, groups, keep):
