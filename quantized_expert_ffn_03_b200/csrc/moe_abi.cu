@@ -959,8 +959,11 @@ moe_status moe_linear_forward(const moe_linear_config* cfg, const moe_linear_wei
   p.N = N;
   p.act = cfg->act;
   p.out_f32 = cfg->out_dtype == MOE_F32;
-  p.vec = aligned(out, 16) && (T == 1 || ldo * osz % 16 == 0) &&
-          (!residual || (aligned(residual, 16) && (T == 1 || ldr * osz % 16 == 0)));
+  auto starts_on = [&](size_t bytes) {
+    return aligned(out, bytes) && (T == 1 || ldo * osz % bytes == 0) &&
+           (!residual || (aligned(residual, bytes) && (T == 1 || ldr * osz % bytes == 0)));
+  };
+  p.vec = starts_on(16) ? 2 : starts_on(2 * osz) ? 1 : 0;
   p.x = static_cast<const uint16_t*>(x);
   p.w = static_cast<const uint16_t*>(wts->w);
   p.w_up = cfg->gated ? static_cast<const uint16_t*>(wts->w_up) : nullptr;

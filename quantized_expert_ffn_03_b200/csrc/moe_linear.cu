@@ -150,26 +150,6 @@ __device__ __forceinline__ void store_row(const LinearParams& p, size_t at, cons
       *reinterpret_cast<uint2*>(dst) = make_uint2(w[0], w[1]);
   }
 }
-// Bias, activation and gate of W adjacent features n .. (those below N).
-template <bool GATED, int W>
-__device__ __forceinline__ void bias_act_gate(const LinearParams& p, int n, float (&v)[W], const float (&u)[W]) {
-  if (p.bias) {
-#pragma unroll
-    for (int i = 0; i < W; ++i)
-      if (n + i < p.N) v[i] += __ldg(p.bias + n + i);
-  }
-  activate(v, p.act);
-  if constexpr (GATED) {
-    if (p.bias_up) {
-#pragma unroll
-      for (int i = 0; i < W; ++i) v[i] *= n + i < p.N ? u[i] + __ldg(p.bias_up + n + i) : 0.f;
-    } else {
-#pragma unroll
-      for (int i = 0; i < W; ++i) v[i] *= u[i];
-    }
-  }
-}
-
 // ---- few tokens: weights streamed once through registers ------------------------------
 
 template <bool F16>
@@ -338,210 +318,419 @@ __device__ __forceinline__ void bar_init(uint32_t a, uint32_t n) {
 __device__ __forceinline__ void bar_expect(uint32_t a, uint32_t bytes) {
   asm volatile("mbarrier.arrive.expect_tx.shared::cta.b64 _, [%0], %1;" ::"r"(a), "r"(bytes) : "memory");
 }
-__device__ __forceinline__ void sts_f4(uint32_t a, float x, float y, float z, float w) {
-  asm volatile("st.shared.v4.f32 [%0], {%1,%2,%3,%4};" ::"r"(a), "f"(x), "f"(y), "f"(z), "f"(w) : "memory");
-}
 __device__ __forceinline__ float4 lds_f4(uint32_t a) {
   float4 v;
   asm volatile("ld.shared.v4.f32 {%0,%1,%2,%3}, [%4];" : "=f"(v.x), "=f"(v.y), "=f"(v.z), "=f"(v.w) : "r"(a) : "memory");
   return v;
 }
 
-// 8 floats from 16-byte chunks c, c + 1 of a swizzled 128-byte row.
-__device__ __forceinline__ void read8(uint32_t row, uint32_t c, uint32_t x, float (&v)[8]) {
-  const float4 a = lds_f4(row + ((c ^ x) << 4)), b = lds_f4(row + (((c + 1u) ^ x) << 4));
-  v[0] = a.x, v[1] = a.y, v[2] = a.z, v[3] = a.w, v[4] = b.x, v[5] = b.y, v[6] = b.z, v[7] = b.w;
-}
-
 constexpr uint32_t kTile = 128u * 128u;  // bytes of a 128-row operand tile of one stage
 
-// ---- some tokens: a cluster per 128 features, K split over its CTAs --------------------
-// The weights are the A operand (128 features), NT tokens the B operand: with
-// T < 128 no MMA row is wasted, and an output row of the accumulator is a
-// feature, so a warp's loads and stores of out and residual are contiguous.
-// Each CTA of the cluster takes a range of K; its accumulators go to its own
-// shared memory as fp32, and after a cluster barrier each CTA sums its share
-// of the outputs over the cluster in rank order and finishes them.  Nothing
-// is exchanged through global memory, so no workspace, and calls on several
-// streams share nothing.
-constexpr int kSplitEpi = 8;                         // warps that read TMEM
-constexpr int kSplitThreads = 32 * (kSplitEpi + 2);  // + a loading and an MMA warp
-constexpr int kMaxSplit = 8;                         // CTAs of a cluster (the portable size)
-constexpr uint32_t kSplitSmem = 220u * 1024u;
+// ---- epilogue from accumulator fragments ------------------------------------------------
+// Both tcgen05 kernels have tokens as rows of the accumulator and features as
+// its columns, and read it in units of 16 tokens x 32 features as fragments:
+// lane (g, t) holds tokens g, g + 8 and of each 8 features i = 0..3 features 2t,
+// 2t + 1.  Rounded to pairs, the four words of a token are transposed among
+// the four lanes that share it (4 shuffles), so that a lane holds 8 adjacent
+// features and four lanes write a token's 64 bytes in 16-byte pieces; the
+// residual comes the same way back.  (Through shared memory instead: 3 times
+// the shared-memory traffic, which the MMAs need.)  Rows that do not start on
+// 16-byte boundaries are written in pairs of features, or through a 16 x 32
+// square of shared memory as whole rows of single ones.
 
-__host__ __device__ constexpr uint32_t split_stage(int nt, int na) { return na * kTile + (uint32_t)nt * 128u; }
-__host__ __device__ constexpr int split_stages(int nt, int na) {
-  return (int)(kSplitSmem / split_stage(nt, na)) < 12 ? (int)(kSplitSmem / split_stage(nt, na)) : 12;
-}
-__host__ __device__ constexpr uint32_t tmem_cols(int need) {
-  return need <= 32 ? 32 : need <= 64 ? 64 : need <= 128 ? 128 : need <= 256 ? 256 : 512;
+// Word k of lane t becomes word t of lane k, among 4 neighbouring lanes.
+__device__ __forceinline__ void transpose4(uint32_t (&w)[4], int t) {
+  const bool odd = t & 1, up = t & 2;
+  uint32_t a = odd ? w[0] : w[1], b = odd ? w[2] : w[3];
+  a = __shfl_xor_sync(kAll, a, 1), b = __shfl_xor_sync(kAll, b, 1);
+  if (odd)
+    w[0] = a, w[2] = b;
+  else
+    w[1] = a, w[3] = b;
+  a = up ? w[0] : w[2], b = up ? w[1] : w[3];
+  a = __shfl_xor_sync(kAll, a, 2), b = __shfl_xor_sync(kAll, b, 2);
+  if (up)
+    w[0] = a, w[1] = b;
+  else
+    w[2] = a, w[3] = b;
 }
 
-template <bool F16, bool GATED, int NT>
-__global__ void __launch_bounds__(kSplitThreads, 1)
-    linear_split_kernel(const __grid_constant__ CUtensorMap map_w, const __grid_constant__ CUtensorMap map_u,
-                        const __grid_constant__ CUtensorMap map_x, const LinearParams p) {
-  constexpr int NA = GATED ? 2 : 1;
-  constexpr int ST = split_stages(NT, NA);
-  constexpr uint32_t kStage = split_stage(NT, NA);
-  static_assert((uint32_t)NA * NT * 512u <= ST * kStage, "the partial sums reuse the stages");
+template <bool F16, bool GATED>
+struct Epilogue {
+  const LinearParams& p;
+  const int lane, g, t;      // t = lane % 4, g = lane / 4
+  const uint32_t square;     // 2 KB of shared memory of this warp
+  float b[8], bu[8];         // biases of the unit's features
+  uint32_t raw[2][8];        // residual of tokens g, g + 8 as read: 8 adjacent features
+
+  __device__ __forceinline__ Epilogue(const LinearParams& p_, int lane_, uint32_t square_)
+      : p(p_), lane(lane_), g(lane_ >> 2), t(lane_ & 3), square(square_) {}
+  // value k of this lane is feature 8 (k / 2) + 2t + k % 2 of the unit
+  __device__ __forceinline__ int feature(int k) const { return 8 * (k >> 1) + 2 * t + (k & 1); }
+  __device__ __forceinline__ bool whole(int n0) const { return p.vec == 2 && n0 + 32 <= p.N; }
+  __device__ __forceinline__ void load_bias(int n0) {
+    if (p.bias) {
+#pragma unroll
+      for (int k = 0; k < 8; ++k) b[k] = n0 + feature(k) < p.N ? __ldg(p.bias + n0 + feature(k)) : 0.f;
+    }
+    if (GATED && p.bias_up) {
+#pragma unroll
+      for (int k = 0; k < 8; ++k) bu[k] = n0 + feature(k) < p.N ? __ldg(p.bias_up + n0 + feature(k)) : 0.f;
+    }
+  }
+  // residual of the unit at token t0, feature n0, ahead of its use
+  __device__ __forceinline__ void fetch(int t0, int n0) {
+    if (!p.res || !whole(n0)) return;
+#pragma unroll
+    for (int h = 0; h < 2; ++h) {
+      const int tok = t0 + g + 8 * h;
+      if (tok >= p.T) continue;
+      const size_t at = (size_t)tok * p.ldr + n0 + 8 * t;
+      uint4 a, c = make_uint4(0u, 0u, 0u, 0u);
+      if (p.out_f32) {
+        a = *reinterpret_cast<const uint4*>(static_cast<const float*>(p.res) + at);
+        c = *reinterpret_cast<const uint4*>(static_cast<const float*>(p.res) + at + 4);
+      } else {
+        a = *reinterpret_cast<const uint4*>(static_cast<const uint16_t*>(p.res) + at);
+      }
+      raw[h][0] = a.x, raw[h][1] = a.y, raw[h][2] = a.z, raw[h][3] = a.w;
+      raw[h][4] = c.x, raw[h][5] = c.y, raw[h][6] = c.z, raw[h][7] = c.w;
+    }
+  }
+  // bias, activation and gate of a token's 8 values (h: token g + 8 h)
+  template <int ACT>
+  __device__ __forceinline__ void values(int h, const float (&v)[16], const float (&u)[GATED ? 16 : 1], float (&y)[8]) {
+#pragma unroll
+    for (int k = 0; k < 8; ++k) y[k] = v[4 * (k >> 1) + 2 * h + (k & 1)];
+    if (p.bias) {
+#pragma unroll
+      for (int k = 0; k < 8; ++k) y[k] += b[k];
+    }
+    activate(y, ACT);
+    if constexpr (GATED) {
+#pragma unroll
+      for (int k = 0; k < 8; ++k) {
+        const float w = u[4 * (k >> 1) + 2 * h + (k & 1)];
+        y[k] *= p.bias_up ? w + bu[k] : w;
+      }
+    }
+  }
+  template <int ACT>
+  __device__ __forceinline__ void rows(int t0, int n0, const float (&v)[16], const float (&u)[GATED ? 16 : 1],
+                                       uint32_t (&r)[2][8]) {
+    const bool full = whole(n0);
+#pragma unroll
+    for (int h = 0; h < 2; ++h) {
+      const int tok = t0 + g + 8 * h;
+      float y[8];
+      values<ACT>(h, v, u, y);
+      const size_t o = (size_t)tok * p.ldo + n0;
+      if (full && !p.out_f32) {
+        uint32_t w[4];
+        if (p.res) {
+          uint32_t e[4] = {r[h][0], r[h][1], r[h][2], r[h][3]};
+          transpose4(e, t);
+#pragma unroll
+          for (int k = 0; k < 8; ++k) y[k] += from16<F16>((uint16_t)(e[k >> 1] >> (16 * (k & 1))));
+        }
+#pragma unroll
+        for (int i = 0; i < 4; ++i) w[i] = pack16<F16>(y[2 * i], y[2 * i + 1]);
+        transpose4(w, t);
+        if (tok < p.T)
+          *reinterpret_cast<uint4*>(static_cast<uint16_t*>(p.out) + o + 8 * t) = make_uint4(w[0], w[1], w[2], w[3]);
+      } else if (full) {
+        uint32_t lo[4], hi[4];  // the even and the odd features
+#pragma unroll
+        for (int i = 0; i < 4; ++i) lo[i] = __float_as_uint(y[2 * i]), hi[i] = __float_as_uint(y[2 * i + 1]);
+        transpose4(lo, t), transpose4(hi, t);
+        if (tok < p.T) {
+          float z[8];
+#pragma unroll
+          for (int i = 0; i < 4; ++i) z[2 * i] = __uint_as_float(lo[i]), z[2 * i + 1] = __uint_as_float(hi[i]);
+          if (p.res) {
+#pragma unroll
+            for (int k = 0; k < 8; ++k) z[k] += __uint_as_float(r[h][k]);
+          }
+          store_row<F16>(p, o + 8 * t, z);
+        }
+      } else if (p.vec) {
+        const size_t ro = (size_t)tok * p.ldr + n0;
+#pragma unroll
+        for (int i = 0; i < 4; ++i) {
+          const int f = 8 * i + 2 * t;
+          if (tok >= p.T || n0 + f >= p.N) continue;
+          if (n0 + f + 1 < p.N) {
+            if (p.out_f32) {
+              float2 q = make_float2(y[2 * i], y[2 * i + 1]);
+              if (p.res) {
+                const float2 e = *reinterpret_cast<const float2*>(static_cast<const float*>(p.res) + ro + f);
+                q.x += e.x, q.y += e.y;
+              }
+              *reinterpret_cast<float2*>(static_cast<float*>(p.out) + o + f) = q;
+            } else {
+              if (p.res) {
+                const uint32_t e = *reinterpret_cast<const uint32_t*>(static_cast<const uint16_t*>(p.res) + ro + f);
+                y[2 * i] += from16<F16>((uint16_t)e), y[2 * i + 1] += from16<F16>((uint16_t)(e >> 16));
+              }
+              *reinterpret_cast<uint32_t*>(static_cast<uint16_t*>(p.out) + o + f) = pack16<F16>(y[2 * i], y[2 * i + 1]);
+            }
+          } else {
+            put(y[2 * i], ro + f, o + f);
+          }
+        }
+      } else {
+#pragma unroll
+        for (int i = 0; i < 4; ++i)
+          asm volatile("st.shared.v2.f32 [%0], {%1, %2};" ::"r"(square + cell(g + 8 * h, 8 * i + 2 * t)), "f"(y[2 * i]),
+                       "f"(y[2 * i + 1])
+                       : "memory");
+      }
+    }
+  }
+  // Byte of feature f of token r in the square: rows of 128 bytes, 16-byte
+  // pieces XOR-ed by the row so that the writes above meet different banks.
+  __device__ __forceinline__ static uint32_t cell(int r, int f) {
+    return (uint32_t)(128 * r + 16 * ((f >> 2) ^ (r & 7)) + 4 * (f & 3));
+  }
+  __device__ __forceinline__ void put(float y, size_t ro, size_t o) {
+    if (p.out_f32) {
+      if (p.res) y += static_cast<const float*>(p.res)[ro];
+      static_cast<float*>(p.out)[o] = y;
+    } else {
+      if (p.res) y += from16<F16>(static_cast<const uint16_t*>(p.res)[ro]);
+      static_cast<uint16_t*>(p.out)[o] = to16<F16>(y);
+    }
+  }
+  // finishes a unit; r: its residual as fetched.  One switch per unit: each
+  // activation has its own straight-line code.
+  __device__ __forceinline__ void unit(int t0, int n0, const float (&v)[16], const float (&u)[GATED ? 16 : 1],
+                                       uint32_t (&r)[2][8]) {
+    switch (p.act) {
+      case MOE_ACT_SILU: rows<MOE_ACT_SILU>(t0, n0, v, u, r); break;
+      case MOE_ACT_GELU: rows<MOE_ACT_GELU>(t0, n0, v, u, r); break;
+      case MOE_ACT_GELU_TANH: rows<MOE_ACT_GELU_TANH>(t0, n0, v, u, r); break;
+      case MOE_ACT_RELU: rows<MOE_ACT_RELU>(t0, n0, v, u, r); break;
+      default: rows<MOE_ACT_NONE>(t0, n0, v, u, r); break;
+    }
+    if (p.vec == 0) {
+      __syncwarp();
+      if (n0 + lane < p.N) {
+#pragma unroll 4
+        for (int r0 = 0; r0 < 16; ++r0) {
+          if (t0 + r0 >= p.T) break;
+          float y;
+          asm volatile("ld.shared.f32 %0, [%1];" : "=f"(y) : "r"(square + cell(r0, lane)) : "memory");
+          put(y, (size_t)(t0 + r0) * p.ldr + n0 + lane, (size_t)(t0 + r0) * p.ldo + n0 + lane);
+        }
+      }
+      __syncwarp();
+    }
+  }
+};
+
+// The fragments of a unit.
+__device__ __forceinline__ void load_unit(uint32_t taddr, float (&v)[16]) {
+  tc::ld_16x256b_x4(taddr, reinterpret_cast<uint32_t(&)[16]>(v));
+}
+
+// ---- some tokens: a cluster per tile, K split over its CTAs ------------------------------
+// Tiles of BT <= 128 tokens x FN features.  Each CTA of the cluster takes a
+// range of K and accumulates it in its TMEM.  Then unit u of the tile belongs
+// to CTA u % S: the others write their partial sums of it into that CTA's
+// shared memory, and after one cluster barrier the owner adds them in rank
+// order and finishes the unit.  Nothing is exchanged through global memory, so
+// no workspace, and calls on several streams share nothing.
+// With T < 128 only BT rows of x are loaded; the MMA reads whatever lies behind
+// them as its other rows, whose results nobody reads.
+constexpr int kTileEpi = 8;                         // warps that read TMEM
+constexpr int kTileThreads = 32 * (kTileEpi + 2);   // + a loading and an MMA warp
+constexpr int kTileStages = 12;                     // at most
+constexpr int kMaxSplit = 8;                        // CTAs of a cluster (the portable size)
+constexpr uint32_t kMaxSmem = 227u * 1024u - 512u;  // dynamic shared memory next to the static
+
+// Shared-memory plan of a tile: stages, their bytes, and the slots for other
+// CTAs' partial sums behind them.
+struct TilePlan {
+  int BT, S, stages;
+  uint32_t stage, slots, total;
+};
+__host__ __device__ inline TilePlan tile_plan(int BT, int rows, int na, int fn, int S) {
+  TilePlan q;
+  q.BT = BT, q.S = S;
+  q.stage = (uint32_t)(BT + rows) * 128u;
+  const int units = (BT / 16) * (fn / 32);
+  const uint32_t exchange = (uint32_t)((units + S - 1) / S * (S - 1) * na) * 2048u;
+  const uint32_t tail = kTile - (uint32_t)BT * 128u > exchange ? kTile - (uint32_t)BT * 128u : exchange;
+  const int fit = (int)((kMaxSmem - 1024u - tail) / q.stage);
+  q.stages = fit < kTileStages ? fit : kTileStages;
+  q.slots = (uint32_t)q.stages * q.stage;
+  q.total = 1024u + q.slots + tail;
+  return q;
+}
+
+template <bool F16, bool GATED, int FN>
+__global__ void __launch_bounds__(kTileThreads, 1)
+    linear_tile_kernel(const __grid_constant__ CUtensorMap map_w, const __grid_constant__ CUtensorMap map_u,
+                       const __grid_constant__ CUtensorMap map_x, const LinearParams p, const TilePlan plan) {
+  constexpr int NA = GATED ? 2 : 1, CN = NA * FN, G = FN / 32;
+  constexpr uint32_t kCols = CN < 32 ? 32 : CN;  // TMEM columns (a power of two)
   extern __shared__ uint8_t smem_raw[];
-  __shared__ __align__(8) uint64_t bars[2 * ST + 1];
+  __shared__ __align__(8) uint64_t bars[2 * kTileStages + 1];
   __shared__ uint32_t tmem_slot;
   const uint32_t s0 = (smem_u32(smem_raw) + 1023u) & ~1023u;
-  const uint32_t full = smem_u32(bars), empty = full + 8u * ST, accfull = empty + 8u * ST;
-  const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
-  const uint32_t rank = tc::cluster_rank(), S = gridDim.x;  // the cluster spans x
-  const int n0 = blockIdx.y * 128, t0 = blockIdx.z * NT;
+  const uint32_t full = smem_u32(bars), empty = full + 8u * kTileStages, accfull = empty + 8u * kTileStages;
+  const int tid = threadIdx.x, warp = __shfl_sync(kAll, tid >> 5, 0), lane = tid & 31;
+  const uint32_t rank = tc::cluster_rank(), S = (uint32_t)plan.S;  // the cluster spans x
+  const int n0 = blockIdx.y * FN, t0 = blockIdx.z * plan.BT;
   const int KB = (p.K + kKB - 1) / kKB;
   const int kb0 = (int)((int64_t)KB * rank / S), kb1 = (int)((int64_t)KB * (rank + 1) / S);
 
-  if (warp == kSplitEpi && lane == 0) {
+  if (warp == kTileEpi && lane == 0) {
     tc::prefetch_map(&map_w);
     tc::prefetch_map(&map_x);
+    if (GATED) tc::prefetch_map(&map_u);
   }
   if (tid == 0) {
-    for (int s = 0; s < ST; ++s) bar_init(full + 8u * s, 1), bar_init(empty + 8u * s, 1);
+    for (int s = 0; s < plan.stages; ++s) bar_init(full + 8u * s, 1), bar_init(empty + 8u * s, 1);
     bar_init(accfull, 1);
     mbar_fence_init();
   }
-  if (warp == kSplitEpi + 1) {
-    tc::tmem_alloc(smem_u32(&tmem_slot), tmem_cols(NA * NT));
+  if (warp == kTileEpi + 1) {
+    tc::tmem_alloc(smem_u32(&tmem_slot), kCols);
     tc::tmem_relinquish();
   }
   tc::fence_before_sync();
   __syncthreads();
   tc::fence_after_sync();
+  tc::cluster_arrive();  // (1) this CTA runs: its shared memory may be written
   const uint32_t tmem = tmem_slot;
 
-  if (warp == kSplitEpi) {
-    if (lane == 0) {
-      bool ok = true;
+  // units of this warp: token blocks 2 q, 2 q + 1 of its TMEM quarter, every
+  // other group of features
+  const int quarter = warp & 3, half = warp >> 2;
+  const int nt = min(plan.BT, p.T - t0);
+  auto each_unit = [&](auto&& f) {
 #pragma unroll 1
-      for (int kb = kb0; kb < kb1 && ok; ++kb) {
-        const int i = kb - kb0, s = i % ST;
-        if (i >= ST) ok = bar_wait(empty + 8u * s, (uint32_t)(i / ST - 1) & 1u);
-        if (!ok) break;
-        const uint32_t st = s0 + (uint32_t)s * kStage;
-        bar_expect(full + 8u * s, kStage);
-        tc::tma_2d(st, &map_w, kb * kKB, n0, full + 8u * s);
-        if constexpr (GATED) tc::tma_2d(st + kTile, &map_u, kb * kKB, n0, full + 8u * s);
-        tc::tma_2d(st + NA * kTile, &map_x, kb * kKB, t0, full + 8u * s);
-      }
-      if (!ok) let_issued_work_end();
+    for (int j = 0; j < (G + 1) / 2 * 2; ++j) {
+      const int rb = 2 * quarter + (j & 1), grp = half + 2 * (j >> 1);
+      if (grp < G && 16 * rb < nt && n0 + 32 * grp < p.N) f(rb, grp, rb * G + grp);
     }
-  } else if (warp == kSplitEpi + 1) {
-    if (lane == 0) {
-      constexpr uint32_t idesc = tc::idesc_f16(128, NT, !F16);
-      bool ok = true;
+  };
+  const uint32_t acc = tmem + ((uint32_t)(32 * quarter) << 16);
+  auto load = [&](int rb, int grp, float (&v)[16], float (&u)[GATED ? 16 : 1]) {
+    const uint32_t at = acc + ((uint32_t)(16 * (rb & 1)) << 16) + (uint32_t)grp * 32u;
+    load_unit(at, v);
+    if constexpr (GATED) load_unit(at + FN, u);
+    tc::wait_ld();
+  };
+
+  // The loading and the MMA warp run their loops as whole warps, so that
+  // addresses and descriptors stay in uniform registers, and one lane issues:
+  // with the loops inside a one-lane branch a step took 350 ns whatever its size.
+  if (warp == kTileEpi) {
+    const bool lead = tc::elect_one();
+    bool ok = true;
+    uint32_t s = 0, phase = 1;  // (an empty stage's barrier counts as a phase ago)
 #pragma unroll 1
-      for (int kb = kb0; kb < kb1 && ok; ++kb) {
-        const int i = kb - kb0, s = i % ST;
-        ok = bar_wait(full + 8u * s, (uint32_t)(i / ST) & 1u);
-        if (!ok) break;
-        tc::fence_after_sync();
-        const uint32_t st = s0 + (uint32_t)s * kStage;
+    for (int kb = kb0; kb < kb1; ++kb) {
+      if (kb - kb0 >= plan.stages) ok = __all_sync(kAll, bar_wait(empty + 8u * s, phase));
+      if (!ok) break;
+      const uint32_t st = s0 + s * plan.stage, w = st + (uint32_t)plan.BT * 128u, bar = full + 8u * s;
+      if (lead) {
+        bar_expect(bar, plan.stage);
+        tc::tma_2d(w, &map_w, kb * kKB, n0, bar);
+        if constexpr (GATED) tc::tma_2d(w + FN * 128u, &map_u, kb * kKB, n0, bar);
+        tc::tma_2d(st, &map_x, kb * kKB, t0, bar);
+      }
+      __syncwarp();
+      if (++s == (uint32_t)plan.stages) s = 0, phase ^= 1u;
+    }
+    if (!ok) let_issued_work_end();
+    __syncwarp();
+    tc::cluster_wait();  // (1)
+  } else if (warp == kTileEpi + 1) {
+    constexpr uint32_t idesc = tc::idesc_f16(128, CN, !F16);
+    const bool lead = tc::elect_one();
+    bool ok = true;
+    uint32_t s = 0, phase = 0;
+#pragma unroll 1
+    for (int kb = kb0; kb < kb1; ++kb) {
+      ok = __all_sync(kAll, bar_wait(full + 8u * s, phase));
+      if (!ok) break;
+      tc::fence_after_sync();
+      const uint32_t st = s0 + s * plan.stage;
+      const uint32_t a = tc::desc_lo(st), w = tc::desc_lo(st + (uint32_t)plan.BT * 128u);
+      if (lead) {
 #pragma unroll
-        for (int k = 0; k < 4; ++k) {
-          const uint64_t bd = tc::smem_desc_sw128(st + NA * kTile + 32u * k);
-#pragma unroll
-          for (int a = 0; a < NA; ++a)
-            tc::mma_f16_ss(tmem + (uint32_t)(a * NT), tc::smem_desc_sw128(st + a * kTile + 32u * k), bd, idesc,
-                           (i > 0 || k > 0) ? 1u : 0u);
-        }
+        for (int k = 0; k < 4; ++k) tc::mma_f16_lo(tmem, a + 2u * k, w + 2u * k, idesc, (kb > kb0 || k > 0) ? 1u : 0u);
         tc::commit(empty + 8u * s);
       }
-      if (ok)
-        tc::commit(accfull);
-      else
-        let_issued_work_end();
+      __syncwarp();
+      if (++s == (uint32_t)plan.stages) s = 0, phase ^= 1u;
     }
+    if (!ok)
+      let_issued_work_end();
+    else if (lead)
+      tc::commit(accfull);
+    __syncwarp();
+    tc::cluster_wait();  // (1)
   } else {
-    // partial sums: [matrix][token][feature] fp32 over the stages, which the
-    // completed MMAs no longer read
+    tc::cluster_wait();  // (1)
     const bool ok = __all_sync(kAll, bar_wait(accfull, 0));
     tc::fence_after_sync();
-    const int quarter = warp & 3, half = warp >> 2;  // TMEM lanes (features), half of the columns
-    const uint32_t dst = s0 + 4u * (uint32_t)(32 * quarter + lane);
-    if (ok) {
-#pragma unroll 1
-      for (int j = 16 * half; j < NA * NT; j += 32) {
-        uint32_t v[16];
-        tc::ld_32x32b_x16(tmem + ((uint32_t)(32 * quarter) << 16) + (uint32_t)j, v);
-        tc::wait_ld();
+    if (ok && S > 1)
+      each_unit([&](int rb, int grp, int unit) {
+        const uint32_t owner = (uint32_t)unit % S;
+        if (owner == rank) return;
+        float v[16], u[GATED ? 16 : 1];
+        load(rb, grp, v, u);
+        const uint32_t slot = (uint32_t)unit / S * (S - 1) + (rank < owner ? rank : rank - 1);
+        const uint32_t dst = tc::map_rank(s0 + plan.slots + slot * (NA * 2048u) + 16u * (uint32_t)lane, owner);
+        const uint32_t* w = reinterpret_cast<const uint32_t*>(v);
 #pragma unroll
-        for (int q = 0; q < 16; ++q)
-          asm volatile("st.shared.b32 [%0], %1;" ::"r"(dst + 512u * (uint32_t)(j + q)), "r"(v[q]) : "memory");
-      }
-    }
-    tc::fence_before_sync();
+        for (int i = 0; i < 4; ++i) tc::st_cluster_v4(dst + 512u * i, w[4 * i], w[4 * i + 1], w[4 * i + 2], w[4 * i + 3]);
+        if constexpr (GATED) {
+          const uint32_t* z = reinterpret_cast<const uint32_t*>(u);
+#pragma unroll
+          for (int i = 0; i < 4; ++i)
+            tc::st_cluster_v4(dst + 2048u + 512u * i, z[4 * i], z[4 * i + 1], z[4 * i + 2], z[4 * i + 3]);
+        }
+      });
   }
   __syncwarp();
-  tc::cluster_arrive();
+  tc::cluster_arrive();  // (2) partial sums are where they belong
   tc::cluster_wait();
-  tc::fence_after_sync();
-  if (warp == kSplitEpi + 1) tc::tmem_dealloc(tmem, tmem_cols(NA * NT));
-
-  // this CTA's share of the outputs: items of 4 adjacent features of a token
-  // (item j = floats 4j .. of [token][feature]), a few per turn so that their
-  // loads overlap
-  constexpr int kTurn = GATED ? 2 : 4;
-  const int nt = min(NT, p.T - t0), items = nt * 32;
-  const int i0 = (int)((int64_t)items * rank / S), i1 = (int)((int64_t)items * (rank + 1) / S);
+  if (warp < kTileEpi) {
+    Epilogue<F16, GATED> epi(p, lane, s0 + (uint32_t)warp * 2048u);  // (the stages are done with)
+    each_unit([&](int rb, int grp, int unit) {
+      if ((uint32_t)unit % S != rank) return;
+      epi.fetch(t0 + 16 * rb, n0 + 32 * grp);
+      epi.load_bias(n0 + 32 * grp);
+      float own[16], own_u[GATED ? 16 : 1], v[16] = {}, u[GATED ? 16 : 1] = {};
+      load(rb, grp, own, own_u);
+      const uint32_t src = s0 + plan.slots + (uint32_t)unit / S * (S - 1) * (NA * 2048u) + 16u * (uint32_t)lane;
 #pragma unroll 1
-  for (int i = i0 + tid; i < i1; i += kTurn * kSplitThreads) {
-    float e[kTurn][4] = {}, v[kTurn][NA][4] = {};
+      for (uint32_t r = 0; r < S; ++r) {  // in rank order, whoever adds
+        const uint32_t at = src + (r < rank ? r : r - 1) * (NA * 2048u);
 #pragma unroll
-    for (int m = 0; m < kTurn; ++m) {
-      const int j = i + m * kSplitThreads, c = j >> 5, n = n0 + 4 * (j & 31);
-      if (j < i1 && p.res && p.vec && n + 4 <= p.N) load_row<F16>(p, p.res, (size_t)(t0 + c) * p.ldr + n, e[m]);
-    }
-#pragma unroll
-    for (int m = 0; m < kTurn; ++m) {
-      const int j = i + m * kSplitThreads;
-      if (j >= i1) continue;
-      float4 q[NA][kMaxSplit];
-#pragma unroll
-      for (int a = 0; a < NA; ++a)
-#pragma unroll
-        for (uint32_t r = 0; r < kMaxSplit; ++r)
-          if (r < S) q[a][r] = tc::ld_cluster_f4(tc::map_rank(s0 + 512u * (uint32_t)(a * NT) + 16u * (uint32_t)j, r));
-#pragma unroll
-      for (int a = 0; a < NA; ++a)
-#pragma unroll
-        for (uint32_t r = 0; r < kMaxSplit; ++r)
-          if (r < S) {
-            v[m][a][0] += q[a][r].x, v[m][a][1] += q[a][r].y;
-            v[m][a][2] += q[a][r].z, v[m][a][3] += q[a][r].w;
+        for (int i = 0; i < 4; ++i) {
+          const float4 q = r == rank ? make_float4(own[4 * i], own[4 * i + 1], own[4 * i + 2], own[4 * i + 3])
+                                     : lds_f4(at + 512u * i);
+          v[4 * i] += q.x, v[4 * i + 1] += q.y, v[4 * i + 2] += q.z, v[4 * i + 3] += q.w;
+          if constexpr (GATED) {
+            const float4 z = r == rank ? make_float4(own_u[4 * i], own_u[4 * i + 1], own_u[4 * i + 2], own_u[4 * i + 3])
+                                       : lds_f4(at + 2048u + 512u * i);
+            u[4 * i] += z.x, u[4 * i + 1] += z.y, u[4 * i + 2] += z.z, u[4 * i + 3] += z.w;
           }
-    }
-#pragma unroll
-    for (int m = 0; m < kTurn; ++m) {
-      const int j = i + m * kSplitThreads, t = t0 + (j >> 5), n = n0 + 4 * (j & 31);
-      if (j >= i1 || n >= p.N) continue;
-      float(&y)[4] = v[m][0];
-      if (p.vec && n + 4 <= p.N) {
-        bias_act_gate<GATED>(p, n, y, v[m][NA - 1]);
-        if (p.res) {
-#pragma unroll
-          for (int k = 0; k < 4; ++k) y[k] += e[m][k];
-        }
-        store_row<F16>(p, (size_t)t * p.ldo + n, y);
-      } else {
-        float(&u)[4] = v[m][NA - 1];
-#pragma unroll 1
-        for (int k = 0; k < 4 && n + k < p.N; ++k) {
-          finish_one<F16>(p, t, n + k, y[0], u[0]);
-          y[0] = y[1], y[1] = y[2], y[2] = y[3];
-          if constexpr (GATED) u[0] = u[1], u[1] = u[2], u[2] = u[3];
         }
       }
-    }
+      epi.unit(t0 + 16 * rb, n0 + 32 * grp, v, u, epi.raw);
+    });
   }
-  // no CTA leaves while another still reads its partial sums
-  __syncwarp();
-  tc::cluster_arrive();
-  tc::cluster_wait();
+  tc::fence_before_sync();
+  __syncthreads();
+  tc::fence_after_sync();
+  if (warp == kTileEpi + 1) tc::tmem_dealloc(tmem, kCols);
 }
 
 // ---- many tokens: persistent pairs of CTAs ---------------------------------------------
@@ -552,59 +741,15 @@ __global__ void __launch_bounds__(kSplitThreads, 1)
 // one's the same rows of w_up, so the first TN/2 columns are gates and the
 // others their ups: one main loop for both forms.  Two accumulators
 // alternate, so the epilogue of a tile runs under the next tile's MMAs.
-constexpr int kPairEpi = 8;                            // epilogue warps
-constexpr int kPairThreads = 32 * (kPairEpi + 2);      // + a loading and an MMA warp
-constexpr uint32_t kPairStage0 = kPairEpi * 32u * 32u * 4u;  // fp32 staging: 32 x 32 per epilogue warp
+constexpr int kPairEpi = 8;                        // epilogue warps
+constexpr int kPairThreads = 32 * (kPairEpi + 2);  // + a loading and an MMA warp
 
 template <int TN>
 struct PairPlan {
-  static constexpr uint32_t kBHalf = TN / 2 * 128u;
-  static constexpr uint32_t kStage = kTile + kBHalf;
-  static constexpr int kStages = TN == 256 ? 6 : 8;
-  static constexpr uint32_t kSmem = kPairStage0 + kStages * kStage + 1024u;
-};
-
-template <int V>
-struct Const {
-  __device__ constexpr int operator()() const { return V; }
-};
-
-__device__ __forceinline__ void load_bias(const float* bias, int n, int N, float (&v)[8]) {
-#pragma unroll
-  for (int i = 0; i < 8; ++i) v[i] = n + i < N ? __ldg(bias + n + i) : 0.f;
-}
-
-// A lane's residual values of one epilogue step, as they lie in memory: 8
-// adjacent features of PASS rows.  Only where whole rows move in 16 bytes
-// (the other rows read their residual as they are written).
-template <bool F16, int FC, int PASS>
-struct Residual {
-  uint4 raw[PASS][2];
-  __device__ __forceinline__ void fetch(const LinearParams& p, int t, int step, int n, int n0) {
-    if (!p.vec || n0 + FC > p.N) return;
-#pragma unroll
-    for (int q = 0; q < PASS; ++q) {
-      if (t + q * step >= p.T) continue;
-      const size_t at = (size_t)(t + q * step) * p.ldr + n;
-      if (p.out_f32) {
-        raw[q][0] = *reinterpret_cast<const uint4*>(static_cast<const float*>(p.res) + at);
-        raw[q][1] = *reinterpret_cast<const uint4*>(static_cast<const float*>(p.res) + at + 4);
-      } else {
-        raw[q][0] = *reinterpret_cast<const uint4*>(static_cast<const uint16_t*>(p.res) + at);
-      }
-    }
-  }
-  __device__ __forceinline__ void add(const LinearParams& p, int q, float (&v)[8]) const {
-    const uint32_t w[8] = {raw[q][0].x, raw[q][0].y, raw[q][0].z, raw[q][0].w,
-                           raw[q][1].x, raw[q][1].y, raw[q][1].z, raw[q][1].w};
-    if (p.out_f32) {
-#pragma unroll
-      for (int k = 0; k < 8; ++k) v[k] += __uint_as_float(w[k]);
-    } else {
-#pragma unroll
-      for (int k = 0; k < 8; ++k) v[k] += from16<F16>((uint16_t)(w[k >> 1] >> (16 * (k & 1))));
-    }
-  }
+  static constexpr uint32_t kStage = kTile + TN / 2 * 128u;
+  static constexpr uint32_t kSquares = kPairEpi * 2048u;
+  static constexpr int kStages = (int)((kMaxSmem - 1024u - kSquares) / kStage);
+  static constexpr uint32_t kSmem = kStages * kStage + kSquares + 1024u;
 };
 
 // Tile number -> (token tile, feature tile): columns of 8 token tiles, so that
@@ -624,21 +769,19 @@ __global__ void __launch_bounds__(kPairThreads, 1)
   using P = PairPlan<TN>;
   constexpr int ST = P::kStages;
   constexpr int FN = GATED ? TN / 2 : TN;  // features per tile
-  constexpr int FC = GATED ? 16 : 32;      // features of an epilogue step
   extern __shared__ uint8_t smem_raw[];
   __shared__ __align__(8) uint64_t bars[2 * ST + 4];
   __shared__ uint32_t tmem_slot;
-  const uint32_t s0 = (smem_u32(smem_raw) + 1023u) & ~1023u;
-  const uint32_t op0 = s0 + kPairStage0;
+  const uint32_t op0 = (smem_u32(smem_raw) + 1023u) & ~1023u;
   const uint32_t full = smem_u32(bars), empty = full + 8u * ST, accfull = empty + 8u * ST, accfree = accfull + 16u;
-  const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
+  const int tid = threadIdx.x, warp = __shfl_sync(kAll, tid >> 5, 0), lane = tid & 31;
   const uint32_t rank = tc::cluster_rank();
   const int MT = (p.T + 255) / 256, FT = (p.N + FN - 1) / FN;
   const int ntiles = MT * FT, npairs = gridDim.x / 2, pair = blockIdx.x / 2;
   const int KB = (p.K + kKB - 1) / kKB;
 
   if (warp == kPairEpi && lane == 0) {
-    tc::prefetch_map(&map_w);
+    tc::prefetch_map(GATED && rank ? &map_u : &map_w);
     tc::prefetch_map(&map_x);
   }
   if (tid == 0) {
@@ -657,185 +800,116 @@ __global__ void __launch_bounds__(kPairThreads, 1)
   tc::fence_after_sync();
   const uint32_t tmem = tmem_slot;
 
+  // (whole warps run the loops, one lane issues, as in linear_tile_kernel)
   if (warp == kPairEpi) {
-    if (lane == 0) {
-      bool ok = true;
-      uint32_t i = 0;
-      const uint32_t full0 = tc::map_rank(full, 0);  // both CTAs' copies count on the even CTA's barriers
-      const void* mb = GATED && rank ? &map_u : &map_w;
+    const bool lead = tc::elect_one();
+    bool ok = true;
+    uint32_t s = 0, phase = 1, filled = 0;
+    const uint32_t full0 = tc::map_rank(full, 0);  // both CTAs' copies count on the even CTA's barriers
+    const void* mb = GATED && rank ? &map_u : &map_w;
 #pragma unroll 1
-      for (int tile = pair; tile < ntiles && ok; tile += npairs) {
-        int mt, ft;
-        pair_tile(tile, MT, FT, mt, ft);
-        const int y_a = mt * 256 + (int)rank * 128;
-        const int y_b = ft * FN + (GATED ? 0 : (int)rank * (TN / 2));
+    for (int tile = pair; tile < ntiles && ok; tile += npairs) {
+      int mt, ft;
+      pair_tile(tile, MT, FT, mt, ft);
+      const int y_a = mt * 256 + (int)rank * 128;
+      const int y_b = ft * FN + (GATED ? 0 : (int)rank * (TN / 2));
 #pragma unroll 1
-        for (int kb = 0; kb < KB; ++kb, ++i) {
-          const uint32_t s = i % ST;
-          if (i >= ST) ok = bar_wait(empty + 8u * s, (i / ST - 1u) & 1u);
-          if (!ok) break;
-          const uint32_t st = op0 + s * P::kStage;
+      for (int kb = 0; kb < KB; ++kb) {
+        if (filled == ST)
+          ok = __all_sync(kAll, bar_wait(empty + 8u * s, phase));
+        else
+          ++filled;
+        if (!ok) break;
+        const uint32_t st = op0 + s * P::kStage;
+        if (lead) {
           if (rank == 0) bar_expect(full + 8u * s, 2 * P::kStage);
           tc::tma2_2d(st, &map_x, kb * kKB, y_a, full0 + 8u * s);
           tc::tma2_2d(st + kTile, mb, kb * kKB, y_b, full0 + 8u * s);
         }
+        __syncwarp();
+        if (++s == ST) s = 0, phase ^= 1u;
       }
-      // the last stages' arrivals from the even CTA, before this block may leave
-      for (uint32_t j = i > ST ? i - ST : 0; j < i && ok; ++j) ok = bar_wait(empty + 8u * (j % ST), (j / ST) & 1u);
-      if (!ok) let_issued_work_end();
     }
+    // the last stages' arrivals from the even CTA, before this block may leave
+    if (filled < ST) s = 0, phase = 0;
+    for (uint32_t j = 0; j < filled && ok; ++j) {
+      ok = __all_sync(kAll, bar_wait(empty + 8u * s, phase));
+      if (++s == ST) s = 0, phase ^= 1u;
+    }
+    if (!ok) let_issued_work_end();
   } else if (warp == kPairEpi + 1) {
-    if (rank == 0 && lane == 0) {
+    if (rank == 0) {
       constexpr uint32_t idesc = tc::idesc_f16(256, TN, !F16);
+      const bool lead = tc::elect_one();
       bool ok = true;
-      uint32_t i = 0, it = 0;
+      uint32_t s = 0, phase = 0, it = 0;
 #pragma unroll 1
       for (int tile = pair; tile < ntiles && ok; tile += npairs, ++it) {
         const uint32_t b = it & 1u;
-        if (it >= 2) ok = bar_wait(accfree + 8u * b, (it / 2 - 1u) & 1u);
+        if (it >= 2) ok = __all_sync(kAll, bar_wait(accfree + 8u * b, (it / 2 - 1u) & 1u));
         if (!ok) break;
         tc::fence_after_sync();
 #pragma unroll 1
-        for (int kb = 0; kb < KB; ++kb, ++i) {
-          const uint32_t s = i % ST;
-          ok = bar_wait(full + 8u * s, (i / ST) & 1u);
+        for (int kb = 0; kb < KB; ++kb) {
+          ok = __all_sync(kAll, bar_wait(full + 8u * s, phase));
           if (!ok) break;
           tc::fence_after_sync();
           const uint32_t st = op0 + s * P::kStage;
+          const uint32_t a = tc::desc_lo(st), w = tc::desc_lo(st + kTile);
+          if (lead) {
 #pragma unroll
-          for (int k = 0; k < 4; ++k)
-            tc::mma2_f16_ss(tmem + b * TN, tc::smem_desc_sw128(st + 32u * k), tc::smem_desc_sw128(st + kTile + 32u * k),
-                            idesc, (kb > 0 || k > 0) ? 1u : 0u);
-          tc::commit2(empty + 8u * s);
+            for (int k = 0; k < 4; ++k)
+              tc::mma2_f16_lo(tmem + b * TN, a + 2u * k, w + 2u * k, idesc, (kb > 0 || k > 0) ? 1u : 0u);
+            tc::commit2(empty + 8u * s);
+          }
+          __syncwarp();
+          if (++s == ST) s = 0, phase ^= 1u;
         }
-        if (ok) tc::commit2(accfull + 8u * b);
+        if (ok && lead) tc::commit2(accfull + 8u * b);
+        __syncwarp();
       }
       if (!ok) let_issued_work_end();
     }
   } else {
-    // Epilogue: warp w reads TMEM lanes 32 (w % 4) .. (its tokens) and half
-    // w / 4 of the columns, 32 of them at a time (with a gate 16 and their 16
-    // ups), in "lane = token" order, and passes the raw sums through a private
-    // 32 x 32 fp32 square of shared memory (16-byte chunks XOR-swizzled by
-    // token) into "lanes along features" order: a lane then holds 8 adjacent
-    // features of a token, and residual and output move in whole sectors.
+    // Epilogue: warp w has TMEM quarter w % 4 (32 tokens) and half w / 4 of the
+    // feature groups, a unit at a time; a unit's residual is fetched one unit
+    // ahead, the first one's while the tile's MMAs still run.
+    constexpr int GT = FN / 32, UN = 2 * (GT / 2);  // groups of a tile, units of a warp
     const int quarter = warp & 3, half = warp >> 2;
-    const uint32_t sq = s0 + (uint32_t)warp * 4096u;
     const uint32_t accfree0 = tc::map_rank(accfree, 0);
-    constexpr int LR = FC / 8, RP = 32 / LR, PASS = LR;  // lanes of a row, rows of a pass, passes
-    const int ch = lane % LR;
-    Residual<F16, FC, PASS> res;
+    Epilogue<F16, GATED> epi(p, lane, op0 + ST * P::kStage + (uint32_t)warp * 2048u);
     uint32_t it = 0;
-    bool ok = true;
 #pragma unroll 1
     for (int tile = pair; tile < ntiles; tile += npairs, ++it) {
       int mt, ft;
       pair_tile(tile, MT, FT, mt, ft);
       const uint32_t b = it & 1u;
-      const int tok0 = mt * 256 + (int)rank * 128 + 32 * quarter;
-      // residual rows are fetched a step ahead, those of the first step while
-      // the tile's MMAs still run
-      if (p.res) res.fetch(p, tok0 + lane / LR, RP, ft * FN + half * (FN / 2) + 8 * ch, ft * FN + half * (FN / 2));
-      ok = __all_sync(kAll, bar_wait(accfull + 8u * b, (it / 2) & 1u));
+      const int tok0 = mt * 256 + (int)rank * 128 + 32 * quarter, f0 = ft * FN + half * (FN / 2);
+      epi.fetch(tok0, f0);
+      const bool ok = __all_sync(kAll, bar_wait(accfull + 8u * b, (it / 2) & 1u));
       if (!ok) break;
       tc::fence_after_sync();
       const uint32_t acc = tmem + b * TN + ((uint32_t)(32 * quarter) << 16);
 #pragma unroll 1
-      for (int c0 = half * (FN / 2); c0 < (half + 1) * (FN / 2); c0 += FC) {
-        const int n0 = ft * FN + c0;
-        const bool whole = p.vec && n0 + FC <= p.N;
-        const int n = n0 + 8 * ch;
-        float bg[8], bu[8];
-        if (p.bias) load_bias(p.bias, n, p.N, bg);
-        if (GATED && p.bias_up) load_bias(p.bias_up, n, p.N, bu);
-        {
-          uint32_t g[32];
-          if constexpr (GATED) {
-            uint32_t(&lo)[16] = *reinterpret_cast<uint32_t(*)[16]>(g);
-            uint32_t(&hi)[16] = *reinterpret_cast<uint32_t(*)[16]>(g + 16);
-            tc::ld_32x32b_x16(acc + (uint32_t)c0, lo);
-            tc::ld_32x32b_x16(acc + (uint32_t)(TN / 2 + c0), hi);
-          } else {
-            tc::ld_32x32b_x32(acc + (uint32_t)c0, g);
-          }
-          tc::wait_ld();
-          if (c0 + FC >= (half + 1) * (FN / 2)) {
-            // the last read of this accumulator by this warp
-            tc::fence_before_sync();
-            __syncwarp();
-            if (lane == 0) tc::arrive_cluster(accfree0 + 8u * b);
-          }
-          if (n0 >= p.N || tok0 >= p.T) continue;
-#pragma unroll
-          for (int j = 0; j < 8; ++j)
-            sts_f4(sq + (uint32_t)lane * 128u + (((uint32_t)j ^ (lane & 7u)) << 4), __uint_as_float(g[4 * j]),
-                   __uint_as_float(g[4 * j + 1]), __uint_as_float(g[4 * j + 2]), __uint_as_float(g[4 * j + 3]));
-        }
-        __syncwarp();
-        // one switch per step: each activation has its own straight-line passes
-        auto passes = [&](auto act) {
-#pragma unroll
-          for (int q = 0; q < PASS; ++q) {
-            const int r = lane / LR + q * RP, t = tok0 + r;
-            const uint32_t row = sq + (uint32_t)r * 128u, x = (uint32_t)(r & 7);
-            float v[8];
-            [[maybe_unused]] float u[8];
-            read8(row, 2u * ch, x, v);
-            if constexpr (GATED) read8(row, 2u * ch + 4u, x, u);
-            if (p.bias) {
-#pragma unroll
-              for (int k = 0; k < 8; ++k) v[k] += bg[k];
-            }
-            activate(v, act());
-            if constexpr (GATED) {
-              if (p.bias_up) {
-#pragma unroll
-                for (int k = 0; k < 8; ++k) u[k] += bu[k];
-              }
-#pragma unroll
-              for (int k = 0; k < 8; ++k) v[k] *= u[k];
-            }
-            if (!whole) {
-              sts_f4(row + (((2u * ch) ^ x) << 4), v[0], v[1], v[2], v[3]);
-              sts_f4(row + (((2u * ch + 1u) ^ x) << 4), v[4], v[5], v[6], v[7]);
-            } else if (t < p.T) {
-              if (p.res) res.add(p, q, v);
-              store_row<F16>(p, (size_t)t * p.ldo + n, v);
-            }
-          }
-        };
-        switch (p.act) {
-          case MOE_ACT_SILU: passes(Const<MOE_ACT_SILU>()); break;
-          case MOE_ACT_GELU: passes(Const<MOE_ACT_GELU>()); break;
-          case MOE_ACT_GELU_TANH: passes(Const<MOE_ACT_GELU_TANH>()); break;
-          case MOE_ACT_RELU: passes(Const<MOE_ACT_RELU>()); break;
-          default: passes(Const<MOE_ACT_NONE>()); break;
-        }
-        if (p.res && c0 + FC < (half + 1) * (FN / 2)) res.fetch(p, tok0 + lane / LR, RP, n + FC, n0 + FC);
-        __syncwarp();
-        if (!whole) {
-          // rows that start anywhere, or the last features: one element per lane
-          const int k = lane % FC, nl = n0 + k;
-#pragma unroll 4
-          for (int r = lane / FC; r < 32; r += 32 / FC) {
-            const int t = tok0 + r;
-            if (t >= p.T || nl >= p.N) continue;
-            float v;
-            asm volatile("ld.shared.f32 %0, [%1];"
-                         : "=f"(v)
-                         : "r"(sq + (uint32_t)r * 128u + ((uint32_t)((k >> 2) ^ (r & 7)) << 4) + 4u * (uint32_t)(k & 3))
-                         : "memory");
-            const size_t o = (size_t)t * p.ldo + nl;
-            if (p.out_f32) {
-              if (p.res) v += static_cast<const float*>(p.res)[(size_t)t * p.ldr + nl];
-              static_cast<float*>(p.out)[o] = v;
-            } else {
-              if (p.res) v += from16<F16>(static_cast<const uint16_t*>(p.res)[(size_t)t * p.ldr + nl]);
-              static_cast<uint16_t*>(p.out)[o] = to16<F16>(v);
-            }
-          }
+      for (int j = 0; j < UN; ++j) {
+        const int grp = half * (GT / 2) + (j >> 1), tok = tok0 + 16 * (j & 1), n = f0 + 32 * (j >> 1);
+        const uint32_t at = acc + ((uint32_t)(16 * (j & 1)) << 16) + (uint32_t)(32 * grp);
+        if ((j & 1) == 0) epi.load_bias(n);
+        float v[16], u[GATED ? 16 : 1];
+        load_unit(at, v);
+        if constexpr (GATED) load_unit(at + TN / 2, u);
+        tc::wait_ld();
+        if (j == UN - 1) {
+          // the last read of this accumulator by this warp
+          tc::fence_before_sync();
           __syncwarp();
+          if (lane == 0) tc::arrive_cluster(accfree0 + 8u * b);
         }
+        uint32_t r[2][8];
+#pragma unroll
+        for (int k = 0; k < 16; ++k) r[k >> 3][k & 7] = epi.raw[k >> 3][k & 7];
+        if (j + 1 < UN) epi.fetch(tok0 + 16 * ((j + 1) & 1), f0 + 32 * ((j + 1) >> 1));
+        if (n < p.N && tok < p.T) epi.unit(tok, n, v, u, r);
       }
     }
   }
@@ -889,11 +963,22 @@ cudaError_t allow_smem(uint32_t smem) {
   return e;
 }
 
+struct Maps {
+  CUtensorMap w, u, x;
+};
+// Maps of a call: weights in boxes of `rows` rows, x in boxes of BT rows.
+template <bool F16, bool GATED>
+bool make_maps(const LinearParams& p, int rows, int BT, Maps* m) {
+  if (!make_map(&m->w, F16, p.w, p.K, p.N, p.ldw, rows) || !make_map(&m->x, F16, p.x, p.K, p.T, p.ldx, BT)) return false;
+  if (GATED) return make_map(&m->u, F16, p.w_up, p.K, p.N, p.ldw_up, rows);
+  m->u = m->w;
+  return true;
+}
+
 // A launch with clusters along x.
-template <auto Kernel>
-cudaError_t launch_cluster(dim3 grid, int threads, int cluster, uint32_t smem, const CUtensorMap& w,
-                           const CUtensorMap& u, const CUtensorMap& x, const LinearParams& p, cudaStream_t st) {
-  const cudaError_t e = allow_smem<Kernel>(smem);
+template <auto Kernel, class... Args>
+cudaError_t launch_cluster(dim3 grid, int threads, int cluster, uint32_t smem, cudaStream_t st, const Args&... args) {
+  const cudaError_t e = allow_smem<Kernel>(kMaxSmem);
   if (e != cudaSuccess) return e;
   cudaLaunchConfig_t c = {};
   c.gridDim = grid;
@@ -907,43 +992,29 @@ cudaError_t launch_cluster(dim3 grid, int threads, int cluster, uint32_t smem, c
   a[0].val.clusterDim.z = 1;
   c.attrs = a;
   c.numAttrs = 1;
-  return cudaLaunchKernelEx(&c, Kernel, w, u, x, p);
+  return cudaLaunchKernelEx(&c, Kernel, args...);
 }
 
-template <bool F16, bool GATED, int NT>
-cudaError_t launch_split_t(const LinearParams& p, int S, cudaStream_t st) {
-  CUtensorMap w, u, x;
-  if (!make_map(&w, F16, p.w, p.K, p.N, p.ldw, 128) || !make_map(&x, F16, p.x, p.K, p.T, p.ldx, NT)) return cudaErrorInvalidValue;
-  u = w;
-  if (GATED && !make_map(&u, F16, p.w_up, p.K, p.N, p.ldw_up, 128)) return cudaErrorInvalidValue;
+template <bool F16, bool GATED, int FN>
+cudaError_t launch_tile_t(const LinearParams& p, int BT, int S, cudaStream_t st) {
+  Maps m;
+  if (!make_maps<F16, GATED>(p, FN, BT, &m)) return cudaErrorInvalidValue;
   constexpr int NA = GATED ? 2 : 1;
-  constexpr uint32_t smem = split_stages(NT, NA) * split_stage(NT, NA) + 1024u;
-  const dim3 grid(S, (p.N + 127) / 128, (p.T + NT - 1) / NT);
-  return launch_cluster<linear_split_kernel<F16, GATED, NT>>(grid, kSplitThreads, S, smem, w, u, x, p, st);
-}
-
-template <bool F16, bool GATED>
-cudaError_t launch_split(const LinearParams& p, int S, cudaStream_t st) {
-  if (p.T <= 16) return launch_split_t<F16, GATED, 16>(p, S, st);
-  if (p.T <= 32) return launch_split_t<F16, GATED, 32>(p, S, st);
-  if (p.T <= 64) return launch_split_t<F16, GATED, 64>(p, S, st);
-  if (GATED || p.T <= 128) return launch_split_t<F16, GATED, 128>(p, S, st);
-  if constexpr (!GATED) return launch_split_t<F16, GATED, 256>(p, S, st);
-  return cudaErrorInvalidValue;
+  const TilePlan q = tile_plan(BT, NA * FN, NA, FN, S);
+  const dim3 grid(S, (p.N + FN - 1) / FN, (p.T + BT - 1) / BT);
+  return launch_cluster<linear_tile_kernel<F16, GATED, FN>>(grid, kTileThreads, S, q.total, st, m.w, m.u, m.x, p, q);
 }
 
 template <bool F16, bool GATED, int TN>
 cudaError_t launch_pair_t(const LinearParams& p, int sms, cudaStream_t st) {
-  CUtensorMap w, u, x;
   constexpr int FN = GATED ? TN / 2 : TN;
-  if (!make_map(&w, F16, p.w, p.K, p.N, p.ldw, TN / 2) || !make_map(&x, F16, p.x, p.K, p.T, p.ldx, 128)) return cudaErrorInvalidValue;
-  u = w;
-  if (GATED && !make_map(&u, F16, p.w_up, p.K, p.N, p.ldw_up, TN / 2)) return cudaErrorInvalidValue;
+  Maps m;
+  if (!make_maps<F16, GATED>(p, TN / 2, 128, &m)) return cudaErrorInvalidValue;
   const int64_t tiles = (int64_t)((p.T + 255) / 256) * ((p.N + FN - 1) / FN);
   if (tiles > 0x3fffffff) return cudaErrorInvalidValue;
   const int pairs = (int)(tiles < sms / 2 ? tiles : sms / 2);
-  return launch_cluster<linear_pair_kernel<F16, GATED, TN>>(dim3(2 * pairs), kPairThreads, 2, PairPlan<TN>::kSmem, w, u,
-                                                            x, p, st);
+  return launch_cluster<linear_pair_kernel<F16, GATED, TN>>(dim3(2 * pairs), kPairThreads, 2, PairPlan<TN>::kSmem,
+                                                                  st, m.w, m.u, m.x, p);
 }
 
 template <bool F16, bool GATED, int TM>
@@ -956,17 +1027,24 @@ cudaError_t launch_rows(const LinearParams& p, cudaStream_t st) {
 }
 
 template <bool F16, bool GATED>
+cudaError_t launch_tensor(const LinearParams& p, int sms, cudaStream_t st) {
+  if (p.T <= 256) {
+    const int BT = p.T <= 16 ? 16 : p.T <= 32 ? 32 : p.T <= 64 ? 64 : 128, KB = (p.K + kKB - 1) / kKB;
+    const int FN = 64;
+    const int tiles = (p.N + FN - 1) / FN * ((p.T + BT - 1) / BT);
+    int S = 1;
+    while (S < kMaxSplit && 2 * S * tiles <= sms && 2 * S <= KB) S *= 2;
+    return launch_tile_t<F16, GATED, FN>(p, BT, S, st);
+  }
+  return launch_pair_t<F16, GATED, 256>(p, sms, st);
+}
+
+template <bool F16, bool GATED>
 cudaError_t launch_any(const LinearParams& p, int sms, cudaStream_t st) {
   if (p.T <= 8) return launch_rows<F16, GATED, 8>(p, st);
   if (p.T <= kRowsTok) return launch_rows<F16, GATED, 16>(p, st);
   if (!encoder()) return cudaErrorNotSupported;
-  if (p.T <= 256) {
-    const int tiles = (p.N + 127) / 128 * (GATED && p.T > 128 ? 2 : 1), KB = (p.K + kKB - 1) / kKB;
-    int S = 1;
-    while (S < 8 && 2 * S * tiles <= sms && 2 * S <= KB) S *= 2;
-    return launch_split<F16, GATED>(p, S, st);
-  }
-  return launch_pair_t<F16, GATED, 256>(p, sms, st);
+  return launch_tensor<F16, GATED>(p, sms, st);
 }
 
 }  // namespace
