@@ -963,6 +963,7 @@ moe_status moe_linear_forward(const moe_linear_config* cfg, const moe_linear_wei
     return aligned(out, bytes) && (T == 1 || ldo * osz % bytes == 0) &&
            (!residual || (aligned(residual, bytes) && (T == 1 || ldr * osz % bytes == 0)));
   };
+  p.bias_vec = aligned(wts->bias, 16) && aligned(cfg->gated ? wts->bias_up : nullptr, 16);
   p.vec = starts_on(16) ? 2 : starts_on(2 * osz) ? 1 : 0;
   p.x = static_cast<const uint16_t*>(x);
   p.w = static_cast<const uint16_t*>(wts->w);

@@ -318,6 +318,9 @@ __device__ __forceinline__ void bar_init(uint32_t a, uint32_t n) {
 __device__ __forceinline__ void bar_expect(uint32_t a, uint32_t bytes) {
   asm volatile("mbarrier.arrive.expect_tx.shared::cta.b64 _, [%0], %1;" ::"r"(a), "r"(bytes) : "memory");
 }
+__device__ __forceinline__ void sts_v4(uint32_t a, uint32_t x, uint32_t y, uint32_t z, uint32_t w) {
+  asm volatile("st.shared.v4.b32 [%0], {%1,%2,%3,%4};" ::"r"(a), "r"(x), "r"(y), "r"(z), "r"(w) : "memory");
+}
 __device__ __forceinline__ float4 lds_f4(uint32_t a) {
   float4 v;
   asm volatile("ld.shared.v4.f32 {%0,%1,%2,%3}, [%4];" : "=f"(v.x), "=f"(v.y), "=f"(v.z), "=f"(v.w) : "r"(a) : "memory");
@@ -326,173 +329,52 @@ __device__ __forceinline__ float4 lds_f4(uint32_t a) {
 
 constexpr uint32_t kTile = 128u * 128u;  // bytes of a 128-row operand tile of one stage
 
-// ---- epilogue from accumulator fragments ------------------------------------------------
-// Both tcgen05 kernels have tokens as rows of the accumulator and features as
-// its columns, and read it in units of 16 tokens x 32 features as fragments:
-// lane (g, t) holds tokens g, g + 8 and of each 8 features i = 0..3 features 2t,
-// 2t + 1.  Rounded to pairs, the four words of a token are transposed among
-// the four lanes that share it (4 shuffles), so that a lane holds 8 adjacent
-// features and four lanes write a token's 64 bytes in 16-byte pieces; the
-// residual comes the same way back.  (Through shared memory instead: 3 times
-// the shared-memory traffic, which the MMAs need.)  Rows that do not start on
-// 16-byte boundaries are written in pairs of features, or through a 16 x 32
-// square of shared memory as whole rows of single ones.
-
-// Word k of lane t becomes word t of lane k, among 4 neighbouring lanes.
-__device__ __forceinline__ void transpose4(uint32_t (&w)[4], int t) {
-  const bool odd = t & 1, up = t & 2;
-  uint32_t a = odd ? w[0] : w[1], b = odd ? w[2] : w[3];
-  a = __shfl_xor_sync(kAll, a, 1), b = __shfl_xor_sync(kAll, b, 1);
-  if (odd)
-    w[0] = a, w[2] = b;
-  else
-    w[1] = a, w[3] = b;
-  a = up ? w[0] : w[2], b = up ? w[1] : w[3];
-  a = __shfl_xor_sync(kAll, a, 2), b = __shfl_xor_sync(kAll, b, 2);
-  if (up)
-    w[0] = a, w[1] = b;
-  else
-    w[2] = a, w[3] = b;
-}
+// ---- epilogue of the tcgen05 kernels -----------------------------------------------------
+// Tokens are the rows of the accumulator (TMEM lanes) and features its
+// columns; a warp reads units of 32 tokens x 32 features, a token per lane.
+// Bias, activation, gate and residual happen in that order of values; the
+// rounded rows go to a square of the warp's shared memory, 16-byte pieces
+// XOR-ed by the row as the tensor map's swizzle has it, and leave by a TMA
+// store, which also cuts off what lies behind T and N.  That is about 20
+// instructions per 512 outputs where rows written by the lanes took 200
+// (4096 x 256 -> 8192 features: XXX us, was 55).  Rows that do not start on
+// 16-byte boundaries take the square as fp32 and are written by the lanes, a
+// row of 32 features at a time.
+constexpr uint32_t kSquare = 4096u;  // bytes per warp: 32 x 32 fp32, or two of 16 bits
 
 template <bool F16, bool GATED>
 struct Epilogue {
   const LinearParams& p;
-  const int lane, g, t;      // t = lane % 4, g = lane / 4
-  const uint32_t square;     // 2 KB of shared memory of this warp
-  float b[8], bu[8];         // biases of the unit's features
-  uint32_t raw[2][8];        // residual of tokens g, g + 8 as read: 8 adjacent features
+  const CUtensorMap* map;  // of out, in boxes of 32 x 32
+  const int lane;
+  const uint32_t square;
+  uint32_t turn = 0;
+  uint4 raw[4];  // 16-bit residual of the next unit
 
-  __device__ __forceinline__ Epilogue(const LinearParams& p_, int lane_, uint32_t square_)
-      : p(p_), lane(lane_), g(lane_ >> 2), t(lane_ & 3), square(square_) {}
-  // value k of this lane is feature 8 (k / 2) + 2t + k % 2 of the unit
-  __device__ __forceinline__ int feature(int k) const { return 8 * (k >> 1) + 2 * t + (k & 1); }
-  __device__ __forceinline__ bool whole(int n0) const { return p.vec == 2 && n0 + 32 <= p.N; }
-  __device__ __forceinline__ void load_bias(int n0) {
-    if (p.bias) {
-#pragma unroll
-      for (int k = 0; k < 8; ++k) b[k] = n0 + feature(k) < p.N ? __ldg(p.bias + n0 + feature(k)) : 0.f;
-    }
-    if (GATED && p.bias_up) {
-#pragma unroll
-      for (int k = 0; k < 8; ++k) bu[k] = n0 + feature(k) < p.N ? __ldg(p.bias_up + n0 + feature(k)) : 0.f;
-    }
-  }
-  // residual of the unit at token t0, feature n0, ahead of its use
+  __device__ __forceinline__ Epilogue(const LinearParams& p_, const CUtensorMap* map_, int lane_, uint32_t square_)
+      : p(p_), map(map_), lane(lane_), square(square_) {}
+
+  // 16-bit residual of the unit at token t0, feature n0, ahead of its use
   __device__ __forceinline__ void fetch(int t0, int n0) {
-    if (!p.res || !whole(n0)) return;
+    if (!p.res || p.out_f32 || p.vec < 2 || n0 + 32 > p.N || t0 + lane >= p.T) return;
+    const uint4* src = reinterpret_cast<const uint4*>(static_cast<const uint16_t*>(p.res) + (size_t)(t0 + lane) * p.ldr + n0);
 #pragma unroll
-    for (int h = 0; h < 2; ++h) {
-      const int tok = t0 + g + 8 * h;
-      if (tok >= p.T) continue;
-      const size_t at = (size_t)tok * p.ldr + n0 + 8 * t;
-      uint4 a, c = make_uint4(0u, 0u, 0u, 0u);
-      if (p.out_f32) {
-        a = *reinterpret_cast<const uint4*>(static_cast<const float*>(p.res) + at);
-        c = *reinterpret_cast<const uint4*>(static_cast<const float*>(p.res) + at + 4);
-      } else {
-        a = *reinterpret_cast<const uint4*>(static_cast<const uint16_t*>(p.res) + at);
+    for (int i = 0; i < 4; ++i) raw[i] = src[i];
+  }
+  __device__ __forceinline__ void add_bias(const float* bias, int n0, float (&v)[32]) const {
+    if (p.bias_vec && n0 + 32 <= p.N) {
+#pragma unroll
+      for (int i = 0; i < 8; ++i) {
+        const float4 b = __ldg(reinterpret_cast<const float4*>(bias + n0) + i);
+        v[4 * i] += b.x, v[4 * i + 1] += b.y, v[4 * i + 2] += b.z, v[4 * i + 3] += b.w;
       }
-      raw[h][0] = a.x, raw[h][1] = a.y, raw[h][2] = a.z, raw[h][3] = a.w;
-      raw[h][4] = c.x, raw[h][5] = c.y, raw[h][6] = c.z, raw[h][7] = c.w;
+    } else {
+#pragma unroll
+      for (int i = 0; i < 32; ++i)
+        if (n0 + i < p.N) v[i] += __ldg(bias + n0 + i);
     }
   }
-  // bias, activation and gate of a token's 8 values (h: token g + 8 h)
-  template <int ACT>
-  __device__ __forceinline__ void values(int h, const float (&v)[16], const float (&u)[GATED ? 16 : 1], float (&y)[8]) {
-#pragma unroll
-    for (int k = 0; k < 8; ++k) y[k] = v[4 * (k >> 1) + 2 * h + (k & 1)];
-    if (p.bias) {
-#pragma unroll
-      for (int k = 0; k < 8; ++k) y[k] += b[k];
-    }
-    activate(y, ACT);
-    if constexpr (GATED) {
-#pragma unroll
-      for (int k = 0; k < 8; ++k) {
-        const float w = u[4 * (k >> 1) + 2 * h + (k & 1)];
-        y[k] *= p.bias_up ? w + bu[k] : w;
-      }
-    }
-  }
-  template <int ACT>
-  __device__ __forceinline__ void rows(int t0, int n0, const float (&v)[16], const float (&u)[GATED ? 16 : 1],
-                                       uint32_t (&r)[2][8]) {
-    const bool full = whole(n0);
-#pragma unroll
-    for (int h = 0; h < 2; ++h) {
-      const int tok = t0 + g + 8 * h;
-      float y[8];
-      values<ACT>(h, v, u, y);
-      const size_t o = (size_t)tok * p.ldo + n0;
-      if (full && !p.out_f32) {
-        uint32_t w[4];
-        if (p.res) {
-          uint32_t e[4] = {r[h][0], r[h][1], r[h][2], r[h][3]};
-          transpose4(e, t);
-#pragma unroll
-          for (int k = 0; k < 8; ++k) y[k] += from16<F16>((uint16_t)(e[k >> 1] >> (16 * (k & 1))));
-        }
-#pragma unroll
-        for (int i = 0; i < 4; ++i) w[i] = pack16<F16>(y[2 * i], y[2 * i + 1]);
-        transpose4(w, t);
-        if (tok < p.T)
-          *reinterpret_cast<uint4*>(static_cast<uint16_t*>(p.out) + o + 8 * t) = make_uint4(w[0], w[1], w[2], w[3]);
-      } else if (full) {
-        uint32_t lo[4], hi[4];  // the even and the odd features
-#pragma unroll
-        for (int i = 0; i < 4; ++i) lo[i] = __float_as_uint(y[2 * i]), hi[i] = __float_as_uint(y[2 * i + 1]);
-        transpose4(lo, t), transpose4(hi, t);
-        if (tok < p.T) {
-          float z[8];
-#pragma unroll
-          for (int i = 0; i < 4; ++i) z[2 * i] = __uint_as_float(lo[i]), z[2 * i + 1] = __uint_as_float(hi[i]);
-          if (p.res) {
-#pragma unroll
-            for (int k = 0; k < 8; ++k) z[k] += __uint_as_float(r[h][k]);
-          }
-          store_row<F16>(p, o + 8 * t, z);
-        }
-      } else if (p.vec) {
-        const size_t ro = (size_t)tok * p.ldr + n0;
-#pragma unroll
-        for (int i = 0; i < 4; ++i) {
-          const int f = 8 * i + 2 * t;
-          if (tok >= p.T || n0 + f >= p.N) continue;
-          if (n0 + f + 1 < p.N) {
-            if (p.out_f32) {
-              float2 q = make_float2(y[2 * i], y[2 * i + 1]);
-              if (p.res) {
-                const float2 e = *reinterpret_cast<const float2*>(static_cast<const float*>(p.res) + ro + f);
-                q.x += e.x, q.y += e.y;
-              }
-              *reinterpret_cast<float2*>(static_cast<float*>(p.out) + o + f) = q;
-            } else {
-              if (p.res) {
-                const uint32_t e = *reinterpret_cast<const uint32_t*>(static_cast<const uint16_t*>(p.res) + ro + f);
-                y[2 * i] += from16<F16>((uint16_t)e), y[2 * i + 1] += from16<F16>((uint16_t)(e >> 16));
-              }
-              *reinterpret_cast<uint32_t*>(static_cast<uint16_t*>(p.out) + o + f) = pack16<F16>(y[2 * i], y[2 * i + 1]);
-            }
-          } else {
-            put(y[2 * i], ro + f, o + f);
-          }
-        }
-      } else {
-#pragma unroll
-        for (int i = 0; i < 4; ++i)
-          asm volatile("st.shared.v2.f32 [%0], {%1, %2};" ::"r"(square + cell(g + 8 * h, 8 * i + 2 * t)), "f"(y[2 * i]),
-                       "f"(y[2 * i + 1])
-                       : "memory");
-      }
-    }
-  }
-  // Byte of feature f of token r in the square: rows of 128 bytes, 16-byte
-  // pieces XOR-ed by the row so that the writes above meet different banks.
-  __device__ __forceinline__ static uint32_t cell(int r, int f) {
-    return (uint32_t)(128 * r + 16 * ((f >> 2) ^ (r & 7)) + 4 * (f & 3));
-  }
-  __device__ __forceinline__ void put(float y, size_t ro, size_t o) {
+  __device__ __forceinline__ void put(float y, size_t ro, size_t o) const {
     if (p.out_f32) {
       if (p.res) y += static_cast<const float*>(p.res)[ro];
       static_cast<float*>(p.out)[o] = y;
@@ -501,36 +383,106 @@ struct Epilogue {
       static_cast<uint16_t*>(p.out)[o] = to16<F16>(y);
     }
   }
-  // finishes a unit; r: its residual as fetched.  One switch per unit: each
-  // activation has its own straight-line code.
-  __device__ __forceinline__ void unit(int t0, int n0, const float (&v)[16], const float (&u)[GATED ? 16 : 1],
-                                       uint32_t (&r)[2][8]) {
-    switch (p.act) {
-      case MOE_ACT_SILU: rows<MOE_ACT_SILU>(t0, n0, v, u, r); break;
-      case MOE_ACT_GELU: rows<MOE_ACT_GELU>(t0, n0, v, u, r); break;
-      case MOE_ACT_GELU_TANH: rows<MOE_ACT_GELU_TANH>(t0, n0, v, u, r); break;
-      case MOE_ACT_RELU: rows<MOE_ACT_RELU>(t0, n0, v, u, r); break;
-      default: rows<MOE_ACT_NONE>(t0, n0, v, u, r); break;
+  // Byte of 16-byte piece j of row r, rows of 64 or of 128 bytes.
+  __device__ __forceinline__ static uint32_t piece64(int r, int j) { return (uint32_t)(64 * r + 16 * (j ^ (r >> 1 & 3))); }
+  __device__ __forceinline__ static uint32_t piece128(int r, int j) { return (uint32_t)(128 * r + 16 * (j ^ (r & 7))); }
+
+  // Finishes the unit at token t0, feature n0 from its sums (v, u: changed).
+  __device__ __forceinline__ void unit(int t0, int n0, float (&v)[32], float (&u)[GATED ? 32 : 1]) {
+    if (p.bias) add_bias(p.bias, n0, v);
+    activate(v, p.act);
+    if constexpr (GATED) {
+      if (p.bias_up) add_bias(p.bias_up, n0, u);
+#pragma unroll
+      for (int i = 0; i < 32; ++i) v[i] *= u[i];
     }
-    if (p.vec == 0) {
-      __syncwarp();
-      if (n0 + lane < p.N) {
-#pragma unroll 4
-        for (int r0 = 0; r0 < 16; ++r0) {
-          if (t0 + r0 >= p.T) break;
-          float y;
-          asm volatile("ld.shared.f32 %0, [%1];" : "=f"(y) : "r"(square + cell(r0, lane)) : "memory");
-          put(y, (size_t)(t0 + r0) * p.ldr + n0 + lane, (size_t)(t0 + r0) * p.ldo + n0 + lane);
+    if (p.vec == 2) {
+      // a piece of the residual behind N is not there to be read in 16 bytes
+      const bool whole = n0 + 32 <= p.N, live = t0 + lane < p.T;
+      if (!p.out_f32) {
+        if (p.res) {
+          if (whole) {
+#pragma unroll
+            for (int i = 0; i < 4; ++i) {
+              const uint32_t w[4] = {raw[i].x, raw[i].y, raw[i].z, raw[i].w};
+#pragma unroll
+              for (int k = 0; k < 8; ++k) v[8 * i + k] += from16<F16>((uint16_t)(w[k >> 1] >> (16 * (k & 1))));
+            }
+          } else if (live) {
+            const uint16_t* src = static_cast<const uint16_t*>(p.res) + (size_t)(t0 + lane) * p.ldr + n0;
+#pragma unroll
+            for (int i = 0; i < 32; ++i)
+              if (n0 + i < p.N) v[i] += from16<F16>(src[i]);
+          }
         }
+        // two squares of 2 KB in turn: the store before the last has been read out
+        const uint32_t sq = square + (turn++ & 1u) * (kSquare / 2);
+        if (lane == 0) tc::store_wait_read<1>();
+        __syncwarp();
+#pragma unroll
+        for (int j = 0; j < 4; ++j)
+          sts_v4(sq + piece64(lane, j), pack16<F16>(v[8 * j], v[8 * j + 1]), pack16<F16>(v[8 * j + 2], v[8 * j + 3]),
+                 pack16<F16>(v[8 * j + 4], v[8 * j + 5]), pack16<F16>(v[8 * j + 6], v[8 * j + 7]));
+        send(sq, t0, n0);
+      } else {
+        if (p.res && live) {
+          const float* src = static_cast<const float*>(p.res) + (size_t)(t0 + lane) * p.ldr + n0;
+          if (whole) {
+#pragma unroll
+            for (int i = 0; i < 8; ++i) {
+              const float4 e = *reinterpret_cast<const float4*>(src + 4 * i);
+              v[4 * i] += e.x, v[4 * i + 1] += e.y, v[4 * i + 2] += e.z, v[4 * i + 3] += e.w;
+            }
+          } else {
+#pragma unroll
+            for (int i = 0; i < 32; ++i)
+              if (n0 + i < p.N) v[i] += src[i];
+          }
+        }
+        if (lane == 0) tc::store_wait_read<0>();
+        __syncwarp();
+        to_square(v);
+        send(square, t0, n0);
       }
-      __syncwarp();
+      return;
     }
+    __syncwarp();
+    to_square(v);
+    __syncwarp();
+    if (n0 + lane < p.N) {
+#pragma unroll 4
+      for (int r = 0; r < 32; ++r) {
+        if (t0 + r >= p.T) break;
+        float y;
+        asm volatile("ld.shared.f32 %0, [%1];" : "=f"(y) : "r"(square + piece128(r, lane >> 2) + 4u * (lane & 3)) : "memory");
+        put(y, (size_t)(t0 + r) * p.ldr + n0 + lane, (size_t)(t0 + r) * p.ldo + n0 + lane);
+      }
+    }
+    __syncwarp();
+  }
+  __device__ __forceinline__ void to_square(const float (&v)[32]) const {
+#pragma unroll
+    for (int j = 0; j < 8; ++j)
+      sts_v4(square + piece128(lane, j), __float_as_uint(v[4 * j]), __float_as_uint(v[4 * j + 1]),
+             __float_as_uint(v[4 * j + 2]), __float_as_uint(v[4 * j + 3]));
+  }
+  __device__ __forceinline__ void send(uint32_t sq, int t0, int n0) const {
+    tc::fence_proxy_async_smem();
+    __syncwarp();
+    if (lane == 0) {
+      tc::tma_store_2d(map, n0, t0, sq);
+      tc::store_commit();
+    }
+  }
+  // before the block leaves its shared memory
+  __device__ __forceinline__ void drain() const {
+    if (lane == 0) tc::store_wait_read<0>();
   }
 };
 
-// The fragments of a unit.
-__device__ __forceinline__ void load_unit(uint32_t taddr, float (&v)[16]) {
-  tc::ld_16x256b_x4(taddr, reinterpret_cast<uint32_t(&)[16]>(v));
+// The sums of a unit.
+__device__ __forceinline__ void load_unit(uint32_t taddr, float (&v)[32]) {
+  tc::ld_32x32b_x32(taddr, reinterpret_cast<uint32_t(&)[32]>(v));
 }
 
 // ---- some tokens: a cluster per tile, K split over its CTAs ------------------------------
@@ -558,8 +510,8 @@ __host__ __device__ inline TilePlan tile_plan(int BT, int rows, int na, int fn, 
   TilePlan q;
   q.BT = BT, q.S = S;
   q.stage = (uint32_t)(BT + rows) * 128u;
-  const int units = (BT / 16) * (fn / 32);
-  const uint32_t exchange = (uint32_t)((units + S - 1) / S * (S - 1) * na) * 2048u;
+  const int units = (BT + 31) / 32 * (fn / 32);
+  const uint32_t exchange = (uint32_t)((units + S - 1) / S * (S - 1) * na) * kSquare;
   const uint32_t tail = kTile - (uint32_t)BT * 128u > exchange ? kTile - (uint32_t)BT * 128u : exchange;
   const int fit = (int)((kMaxSmem - 1024u - tail) / q.stage);
   q.stages = fit < kTileStages ? fit : kTileStages;
@@ -571,9 +523,10 @@ __host__ __device__ inline TilePlan tile_plan(int BT, int rows, int na, int fn, 
 template <bool F16, bool GATED, int FN>
 __global__ void __launch_bounds__(kTileThreads, 1)
     linear_tile_kernel(const __grid_constant__ CUtensorMap map_w, const __grid_constant__ CUtensorMap map_u,
-                       const __grid_constant__ CUtensorMap map_x, const LinearParams p, const TilePlan plan) {
+                       const __grid_constant__ CUtensorMap map_x, const __grid_constant__ CUtensorMap map_out,
+                       const LinearParams p, const TilePlan plan) {
   constexpr int NA = GATED ? 2 : 1, CN = NA * FN, G = FN / 32;
-  constexpr uint32_t kCols = CN < 32 ? 32 : CN;  // TMEM columns (a power of two)
+  constexpr uint32_t kCols = CN;  // TMEM columns, a power of two from 32
   extern __shared__ uint8_t smem_raw[];
   __shared__ __align__(8) uint64_t bars[2 * kTileStages + 1];
   __shared__ uint32_t tmem_slot;
@@ -605,22 +558,20 @@ __global__ void __launch_bounds__(kTileThreads, 1)
   tc::cluster_arrive();  // (1) this CTA runs: its shared memory may be written
   const uint32_t tmem = tmem_slot;
 
-  // units of this warp: token blocks 2 q, 2 q + 1 of its TMEM quarter, every
-  // other group of features
+  // units of this warp: the tokens of its TMEM quarter, every other group of features
   const int quarter = warp & 3, half = warp >> 2;
-  const int nt = min(plan.BT, p.T - t0);
-  auto each_unit = [&](auto&& f) {
-#pragma unroll 1
-    for (int j = 0; j < (G + 1) / 2 * 2; ++j) {
-      const int rb = 2 * quarter + (j & 1), grp = half + 2 * (j >> 1);
-      if (grp < G && 16 * rb < nt && n0 + 32 * grp < p.N) f(rb, grp, rb * G + grp);
-    }
-  };
+  const int tok0 = t0 + 32 * quarter;
+  const bool busy = warp < kTileEpi && 32 * quarter < plan.BT && tok0 < p.T;
   const uint32_t acc = tmem + ((uint32_t)(32 * quarter) << 16);
-  auto load = [&](int rb, int grp, float (&v)[16], float (&u)[GATED ? 16 : 1]) {
-    const uint32_t at = acc + ((uint32_t)(16 * (rb & 1)) << 16) + (uint32_t)grp * 32u;
-    load_unit(at, v);
-    if constexpr (GATED) load_unit(at + FN, u);
+  auto each_unit = [&](auto&& f) {
+    if (!busy) return;
+#pragma unroll 1
+    for (int grp = half; grp < G; grp += 2)
+      if (n0 + 32 * grp < p.N) f(grp, (uint32_t)(quarter * G + grp));
+  };
+  auto load = [&](int grp, float (&v)[32], float (&u)[GATED ? 32 : 1]) {
+    load_unit(acc + (uint32_t)(32 * grp), v);
+    if constexpr (GATED) load_unit(acc + (uint32_t)(FN + 32 * grp), u);
     tc::wait_ld();
   };
 
@@ -679,53 +630,58 @@ __global__ void __launch_bounds__(kTileThreads, 1)
     const bool ok = __all_sync(kAll, bar_wait(accfull, 0));
     tc::fence_after_sync();
     if (ok && S > 1)
-      each_unit([&](int rb, int grp, int unit) {
-        const uint32_t owner = (uint32_t)unit % S;
+      each_unit([&](int grp, uint32_t unit) {
+        const uint32_t owner = unit % S;
         if (owner == rank) return;
-        float v[16], u[GATED ? 16 : 1];
-        load(rb, grp, v, u);
-        const uint32_t slot = (uint32_t)unit / S * (S - 1) + (rank < owner ? rank : rank - 1);
-        const uint32_t dst = tc::map_rank(s0 + plan.slots + slot * (NA * 2048u) + 16u * (uint32_t)lane, owner);
-        const uint32_t* w = reinterpret_cast<const uint32_t*>(v);
+        float v[32], u[GATED ? 32 : 1];
+        load(grp, v, u);
+        const uint32_t slot = unit / S * (S - 1) + (rank < owner ? rank : rank - 1);
+        const uint32_t dst = tc::map_rank(s0 + plan.slots + slot * (NA * kSquare) + 16u * (uint32_t)lane, owner);
+        auto push = [&](uint32_t at, const float* w) {
 #pragma unroll
-        for (int i = 0; i < 4; ++i) tc::st_cluster_v4(dst + 512u * i, w[4 * i], w[4 * i + 1], w[4 * i + 2], w[4 * i + 3]);
-        if constexpr (GATED) {
-          const uint32_t* z = reinterpret_cast<const uint32_t*>(u);
-#pragma unroll
-          for (int i = 0; i < 4; ++i)
-            tc::st_cluster_v4(dst + 2048u + 512u * i, z[4 * i], z[4 * i + 1], z[4 * i + 2], z[4 * i + 3]);
-        }
+          for (int i = 0; i < 8; ++i)
+            tc::st_cluster_v4(at + 512u * i, __float_as_uint(w[4 * i]), __float_as_uint(w[4 * i + 1]),
+                              __float_as_uint(w[4 * i + 2]), __float_as_uint(w[4 * i + 3]));
+        };
+        push(dst, v);
+        if constexpr (GATED) push(dst + kSquare, u);
       });
   }
   __syncwarp();
   tc::cluster_arrive();  // (2) partial sums are where they belong
   tc::cluster_wait();
   if (warp < kTileEpi) {
-    Epilogue<F16, GATED> epi(p, lane, s0 + (uint32_t)warp * 2048u);  // (the stages are done with)
-    each_unit([&](int rb, int grp, int unit) {
-      if ((uint32_t)unit % S != rank) return;
-      epi.fetch(t0 + 16 * rb, n0 + 32 * grp);
-      epi.load_bias(n0 + 32 * grp);
-      float own[16], own_u[GATED ? 16 : 1], v[16] = {}, u[GATED ? 16 : 1] = {};
-      load(rb, grp, own, own_u);
-      const uint32_t src = s0 + plan.slots + (uint32_t)unit / S * (S - 1) * (NA * 2048u) + 16u * (uint32_t)lane;
+    Epilogue<F16, GATED> epi(p, &map_out, lane, s0 + (uint32_t)warp * kSquare);  // (the stages are done with)
+    each_unit([&](int grp, uint32_t unit) {
+      if (unit % S != rank) return;
+      epi.fetch(tok0, n0 + 32 * grp);
+      const uint32_t src = s0 + plan.slots + unit / S * (S - 1) * (NA * kSquare) + 16u * (uint32_t)lane;
+      float v[32], u[GATED ? 32 : 1];
+      load(grp, v, u);
+      if (S > 1) {  // the sum over ranks in their order, whichever of them adds
+        auto add = [&](uint32_t at, float (&w)[32]) {
+          float sum[32];
 #pragma unroll 1
-      for (uint32_t r = 0; r < S; ++r) {  // in rank order, whoever adds
-        const uint32_t at = src + (r < rank ? r : r - 1) * (NA * 2048u);
+          for (uint32_t r = 0; r < S; ++r) {
+            const uint32_t from = at + (r < rank ? r : r - 1) * (NA * kSquare);
 #pragma unroll
-        for (int i = 0; i < 4; ++i) {
-          const float4 q = r == rank ? make_float4(own[4 * i], own[4 * i + 1], own[4 * i + 2], own[4 * i + 3])
-                                     : lds_f4(at + 512u * i);
-          v[4 * i] += q.x, v[4 * i + 1] += q.y, v[4 * i + 2] += q.z, v[4 * i + 3] += q.w;
-          if constexpr (GATED) {
-            const float4 z = r == rank ? make_float4(own_u[4 * i], own_u[4 * i + 1], own_u[4 * i + 2], own_u[4 * i + 3])
-                                       : lds_f4(at + 2048u + 512u * i);
-            u[4 * i] += z.x, u[4 * i + 1] += z.y, u[4 * i + 2] += z.z, u[4 * i + 3] += z.w;
+            for (int i = 0; i < 8; ++i) {
+              const float4 q = r == rank ? make_float4(w[4 * i], w[4 * i + 1], w[4 * i + 2], w[4 * i + 3])
+                                         : lds_f4(from + 512u * i);
+              sum[4 * i] = r ? sum[4 * i] + q.x : q.x, sum[4 * i + 1] = r ? sum[4 * i + 1] + q.y : q.y;
+              sum[4 * i + 2] = r ? sum[4 * i + 2] + q.z : q.z, sum[4 * i + 3] = r ? sum[4 * i + 3] + q.w : q.w;
+            }
           }
-        }
+#pragma unroll
+          for (int i = 0; i < 32; ++i) w[i] = sum[i];
+        };
+        add(src, v);
+        if constexpr (GATED) add(src + kSquare, u);
       }
-      epi.unit(t0 + 16 * rb, n0 + 32 * grp, v, u, epi.raw);
+      epi.unit(tok0, n0 + 32 * grp, v, u);
     });
+    epi.drain();
+    __syncwarp();
   }
   tc::fence_before_sync();
   __syncthreads();
@@ -747,7 +703,7 @@ constexpr int kPairThreads = 32 * (kPairEpi + 2);  // + a loading and an MMA war
 template <int TN>
 struct PairPlan {
   static constexpr uint32_t kStage = kTile + TN / 2 * 128u;
-  static constexpr uint32_t kSquares = kPairEpi * 2048u;
+  static constexpr uint32_t kSquares = kPairEpi * kSquare;
   static constexpr int kStages = (int)((kMaxSmem - 1024u - kSquares) / kStage);
   static constexpr uint32_t kSmem = kStages * kStage + kSquares + 1024u;
 };
@@ -765,7 +721,8 @@ __device__ __forceinline__ void pair_tile(int tile, int MT, int FT, int& mt, int
 template <bool F16, bool GATED, int TN>
 __global__ void __launch_bounds__(kPairThreads, 1)
     linear_pair_kernel(const __grid_constant__ CUtensorMap map_w, const __grid_constant__ CUtensorMap map_u,
-                       const __grid_constant__ CUtensorMap map_x, const LinearParams p) {
+                       const __grid_constant__ CUtensorMap map_x, const __grid_constant__ CUtensorMap map_out,
+                       const LinearParams p) {
   using P = PairPlan<TN>;
   constexpr int ST = P::kStages;
   constexpr int FN = GATED ? TN / 2 : TN;  // features per tile
@@ -872,32 +829,30 @@ __global__ void __launch_bounds__(kPairThreads, 1)
     }
   } else {
     // Epilogue: warp w has TMEM quarter w % 4 (32 tokens) and half w / 4 of the
-    // feature groups, a unit at a time; a unit's residual is fetched one unit
-    // ahead, the first one's while the tile's MMAs still run.
-    constexpr int GT = FN / 32, UN = 2 * (GT / 2);  // groups of a tile, units of a warp
+    // features, a unit at a time; a unit's residual is fetched one unit ahead,
+    // the first one's while the tile's MMAs still run.
+    constexpr int UN = FN / 64;  // units of a warp
     const int quarter = warp & 3, half = warp >> 2;
     const uint32_t accfree0 = tc::map_rank(accfree, 0);
-    Epilogue<F16, GATED> epi(p, lane, op0 + ST * P::kStage + (uint32_t)warp * 2048u);
+    Epilogue<F16, GATED> epi(p, &map_out, lane, op0 + ST * P::kStage + (uint32_t)warp * kSquare);
     uint32_t it = 0;
 #pragma unroll 1
     for (int tile = pair; tile < ntiles; tile += npairs, ++it) {
       int mt, ft;
       pair_tile(tile, MT, FT, mt, ft);
       const uint32_t b = it & 1u;
-      const int tok0 = mt * 256 + (int)rank * 128 + 32 * quarter, f0 = ft * FN + half * (FN / 2);
-      epi.fetch(tok0, f0);
+      const int tok = mt * 256 + (int)rank * 128 + 32 * quarter, c0 = half * (FN / 2), f0 = ft * FN + c0;
+      epi.fetch(tok, f0);
       const bool ok = __all_sync(kAll, bar_wait(accfull + 8u * b, (it / 2) & 1u));
       if (!ok) break;
       tc::fence_after_sync();
-      const uint32_t acc = tmem + b * TN + ((uint32_t)(32 * quarter) << 16);
+      const uint32_t acc = tmem + b * TN + ((uint32_t)(32 * quarter) << 16) + (uint32_t)c0;
 #pragma unroll 1
       for (int j = 0; j < UN; ++j) {
-        const int grp = half * (GT / 2) + (j >> 1), tok = tok0 + 16 * (j & 1), n = f0 + 32 * (j >> 1);
-        const uint32_t at = acc + ((uint32_t)(16 * (j & 1)) << 16) + (uint32_t)(32 * grp);
-        if ((j & 1) == 0) epi.load_bias(n);
-        float v[16], u[GATED ? 16 : 1];
-        load_unit(at, v);
-        if constexpr (GATED) load_unit(at + TN / 2, u);
+        const int n = f0 + 32 * j;
+        float v[32], u[GATED ? 32 : 1];
+        load_unit(acc + 32u * (uint32_t)j, v);
+        if constexpr (GATED) load_unit(acc + (uint32_t)(TN / 2 + 32 * j), u);
         tc::wait_ld();
         if (j == UN - 1) {
           // the last read of this accumulator by this warp
@@ -905,13 +860,11 @@ __global__ void __launch_bounds__(kPairThreads, 1)
           __syncwarp();
           if (lane == 0) tc::arrive_cluster(accfree0 + 8u * b);
         }
-        uint32_t r[2][8];
-#pragma unroll
-        for (int k = 0; k < 16; ++k) r[k >> 3][k & 7] = epi.raw[k >> 3][k & 7];
-        if (j + 1 < UN) epi.fetch(tok0 + 16 * ((j + 1) & 1), f0 + 32 * ((j + 1) >> 1));
-        if (n < p.N && tok < p.T) epi.unit(tok, n, v, u, r);
+        if (n < p.N && tok < p.T) epi.unit(tok, n, v, u);
+        if (j + 1 < UN) epi.fetch(tok, n + 32);
       }
     }
+    epi.drain();
   }
   __syncwarp();
   tc::fence_before_sync();
@@ -963,16 +916,30 @@ cudaError_t allow_smem(uint32_t smem) {
   return e;
 }
 
+// out in boxes of 32 x 32 elements, swizzled by the box's row length.
+bool make_out_map(CUtensorMap* m, bool f16, const LinearParams& p) {
+  const cuuint64_t dims[2] = {(cuuint64_t)p.N, (cuuint64_t)p.T};
+  const cuuint64_t strides[1] = {(cuuint64_t)((p.out_f32 ? 4 : 2) * p.ldo)};
+  const cuuint32_t box[2] = {32, 32}, step[2] = {1, 1};
+  return encoder()(m,
+                   p.out_f32 ? CU_TENSOR_MAP_DATA_TYPE_FLOAT32
+                   : f16     ? CU_TENSOR_MAP_DATA_TYPE_FLOAT16
+                             : CU_TENSOR_MAP_DATA_TYPE_BFLOAT16,
+                   2, p.out, dims, strides, box, step, CU_TENSOR_MAP_INTERLEAVE_NONE,
+                   p.out_f32 ? CU_TENSOR_MAP_SWIZZLE_128B : CU_TENSOR_MAP_SWIZZLE_64B, CU_TENSOR_MAP_L2_PROMOTION_NONE,
+                   CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
+}
+
 struct Maps {
-  CUtensorMap w, u, x;
+  CUtensorMap w, u, x, out;
 };
 // Maps of a call: weights in boxes of `rows` rows, x in boxes of BT rows.
 template <bool F16, bool GATED>
 bool make_maps(const LinearParams& p, int rows, int BT, Maps* m) {
   if (!make_map(&m->w, F16, p.w, p.K, p.N, p.ldw, rows) || !make_map(&m->x, F16, p.x, p.K, p.T, p.ldx, BT)) return false;
-  if (GATED) return make_map(&m->u, F16, p.w_up, p.K, p.N, p.ldw_up, rows);
-  m->u = m->w;
-  return true;
+  m->u = m->out = m->w;  // (unused ones are valid all the same)
+  return (!GATED || make_map(&m->u, F16, p.w_up, p.K, p.N, p.ldw_up, rows)) &&
+         (p.vec != 2 || make_out_map(&m->out, F16, p));
 }
 
 // A launch with clusters along x.
@@ -1002,7 +969,8 @@ cudaError_t launch_tile_t(const LinearParams& p, int BT, int S, cudaStream_t st)
   constexpr int NA = GATED ? 2 : 1;
   const TilePlan q = tile_plan(BT, NA * FN, NA, FN, S);
   const dim3 grid(S, (p.N + FN - 1) / FN, (p.T + BT - 1) / BT);
-  return launch_cluster<linear_tile_kernel<F16, GATED, FN>>(grid, kTileThreads, S, q.total, st, m.w, m.u, m.x, p, q);
+  return launch_cluster<linear_tile_kernel<F16, GATED, FN>>(grid, kTileThreads, S, q.total, st, m.w, m.u, m.x, m.out,
+                                                          p, q);
 }
 
 template <bool F16, bool GATED, int TN>
@@ -1014,7 +982,7 @@ cudaError_t launch_pair_t(const LinearParams& p, int sms, cudaStream_t st) {
   if (tiles > 0x3fffffff) return cudaErrorInvalidValue;
   const int pairs = (int)(tiles < sms / 2 ? tiles : sms / 2);
   return launch_cluster<linear_pair_kernel<F16, GATED, TN>>(dim3(2 * pairs), kPairThreads, 2, PairPlan<TN>::kSmem,
-                                                                  st, m.w, m.u, m.x, p);
+                                                                  st, m.w, m.u, m.x, m.out, p);
 }
 
 template <bool F16, bool GATED, int TM>
