@@ -361,6 +361,13 @@ struct Epilogue {
 #pragma unroll
     for (int i = 0; i < 4; ++i) raw[i] = src[i];
   }
+  // brings the unit's biases into the L1 cache
+  __device__ __forceinline__ void touch_bias(int n0) const {
+    if (p.bias && n0 + lane < p.N) {
+      const float a = __ldg(p.bias + n0 + lane), b = GATED && p.bias_up ? __ldg(p.bias_up + n0 + lane) : 0.f;
+      asm volatile("" ::"f"(a), "f"(b));
+    }
+  }
   __device__ __forceinline__ void add_bias(const float* bias, int n0, float (&v)[32]) const {
     if (p.bias_vec && n0 + 32 <= p.N) {
 #pragma unroll
@@ -497,7 +504,7 @@ __device__ __forceinline__ void load_unit(uint32_t taddr, float (&v)[32]) {
 constexpr int kTileEpi = 8;                         // warps that read TMEM
 constexpr int kTileThreads = 32 * (kTileEpi + 2);   // + a loading and an MMA warp
 constexpr int kTileStages = 12;                     // at most
-constexpr int kMaxSplit = 8;                        // CTAs of a cluster (the portable size)
+constexpr int kMaxSplit = 4;                        // CTAs of a cluster (16 clusters of 8 do not fit the GPCs at once)
 constexpr uint32_t kMaxSmem = 227u * 1024u - 512u;  // dynamic shared memory next to the static
 
 // Shared-memory plan of a tile: stages, their bytes, and the slots for other
@@ -538,15 +545,31 @@ __global__ void __launch_bounds__(kTileThreads, 1)
   const int KB = (p.K + kKB - 1) / kKB;
   const int kb0 = (int)((int64_t)KB * rank / S), kb1 = (int)((int64_t)KB * (rank + 1) / S);
 
-  if (warp == kTileEpi && lane == 0) {
-    tc::prefetch_map(&map_w);
-    tc::prefetch_map(&map_x);
-    if (GATED) tc::prefetch_map(&map_u);
-  }
-  if (tid == 0) {
-    for (int s = 0; s < plan.stages; ++s) bar_init(full + 8u * s, 1), bar_init(empty + 8u * s, 1);
-    bar_init(accfull, 1);
-    mbar_fence_init();
+  // The loading and the MMA warp run their loops as whole warps, so that
+  // addresses and descriptors stay in uniform registers, and one lane issues:
+  // with the loops inside a one-lane branch a step took 350 ns whatever its size.
+  const bool lead = tc::elect_one();
+  auto copy = [&](int kb, uint32_t s) {  // by the loading warp's leader
+    const uint32_t st = s0 + s * plan.stage, w = st + (uint32_t)plan.BT * 128u, bar = full + 8u * s;
+    bar_expect(bar, plan.stage);
+    tc::tma_2d(w, &map_w, kb * kKB, n0, bar);
+    if constexpr (GATED) tc::tma_2d(w + FN * 128u, &map_u, kb * kKB, n0, bar);
+    tc::tma_2d(st, &map_x, kb * kKB, t0, bar);
+  };
+  const int first = min(kb1 - kb0, plan.stages);
+  if (warp == kTileEpi) {
+    // the first copies are on their way before the block has met
+    if (lead) {
+      for (int s = 0; s < plan.stages; ++s) bar_init(full + 8u * s, 1), bar_init(empty + 8u * s, 1);
+      bar_init(accfull, 1);
+      mbar_fence_init();
+    }
+    __syncwarp();
+#pragma unroll 1
+    for (int i = 0; i < first; ++i) {
+      if (lead) copy(kb0 + i, (uint32_t)i);
+      __syncwarp();
+    }
   }
   if (warp == kTileEpi + 1) {
     tc::tmem_alloc(smem_u32(&tmem_slot), kCols);
@@ -575,24 +598,16 @@ __global__ void __launch_bounds__(kTileThreads, 1)
     tc::wait_ld();
   };
 
-  // The loading and the MMA warp run their loops as whole warps, so that
-  // addresses and descriptors stay in uniform registers, and one lane issues:
-  // with the loops inside a one-lane branch a step took 350 ns whatever its size.
+  Epilogue<F16, GATED> epi(p, &map_out, lane, s0 + (uint32_t)warp * kSquare);  // (in the stages, once they are done with)
+  int mine = -1;
   if (warp == kTileEpi) {
-    const bool lead = tc::elect_one();
     bool ok = true;
-    uint32_t s = 0, phase = 1;  // (an empty stage's barrier counts as a phase ago)
+    uint32_t s = 0, phase = 0;
 #pragma unroll 1
-    for (int kb = kb0; kb < kb1; ++kb) {
-      if (kb - kb0 >= plan.stages) ok = __all_sync(kAll, bar_wait(empty + 8u * s, phase));
+    for (int kb = kb0 + first; kb < kb1; ++kb) {
+      ok = __all_sync(kAll, bar_wait(empty + 8u * s, phase));
       if (!ok) break;
-      const uint32_t st = s0 + s * plan.stage, w = st + (uint32_t)plan.BT * 128u, bar = full + 8u * s;
-      if (lead) {
-        bar_expect(bar, plan.stage);
-        tc::tma_2d(w, &map_w, kb * kKB, n0, bar);
-        if constexpr (GATED) tc::tma_2d(w + FN * 128u, &map_u, kb * kKB, n0, bar);
-        tc::tma_2d(st, &map_x, kb * kKB, t0, bar);
-      }
+      if (lead) copy(kb, s);
       __syncwarp();
       if (++s == (uint32_t)plan.stages) s = 0, phase ^= 1u;
     }
@@ -601,7 +616,6 @@ __global__ void __launch_bounds__(kTileThreads, 1)
     tc::cluster_wait();  // (1)
   } else if (warp == kTileEpi + 1) {
     constexpr uint32_t idesc = tc::idesc_f16(128, CN, !F16);
-    const bool lead = tc::elect_one();
     bool ok = true;
     uint32_t s = 0, phase = 0;
 #pragma unroll 1
@@ -627,6 +641,13 @@ __global__ void __launch_bounds__(kTileThreads, 1)
     tc::cluster_wait();  // (1)
   } else {
     tc::cluster_wait();  // (1)
+    // this warp's first unit: its residual and biases come while the MMAs run
+    each_unit([&](int grp, uint32_t unit) {
+      if (mine >= 0 || unit % S != rank) return;
+      mine = grp;
+      epi.fetch(tok0, n0 + 32 * grp);
+      epi.touch_bias(n0 + 32 * grp);
+    });
     const bool ok = __all_sync(kAll, bar_wait(accfull, 0));
     tc::fence_after_sync();
     if (ok && S > 1)
@@ -651,29 +672,26 @@ __global__ void __launch_bounds__(kTileThreads, 1)
   tc::cluster_arrive();  // (2) partial sums are where they belong
   tc::cluster_wait();
   if (warp < kTileEpi) {
-    Epilogue<F16, GATED> epi(p, &map_out, lane, s0 + (uint32_t)warp * kSquare);  // (the stages are done with)
     each_unit([&](int grp, uint32_t unit) {
       if (unit % S != rank) return;
-      epi.fetch(tok0, n0 + 32 * grp);
+      if (grp != mine) epi.fetch(tok0, n0 + 32 * grp);
       const uint32_t src = s0 + plan.slots + unit / S * (S - 1) * (NA * kSquare) + 16u * (uint32_t)lane;
       float v[32], u[GATED ? 32 : 1];
       load(grp, v, u);
       if (S > 1) {  // the sum over ranks in their order, whichever of them adds
-        auto add = [&](uint32_t at, float (&w)[32]) {
-          float sum[32];
-#pragma unroll 1
-          for (uint32_t r = 0; r < S; ++r) {
-            const uint32_t from = at + (r < rank ? r : r - 1) * (NA * kSquare);
+        auto add = [&](uint32_t at, float* w) {
 #pragma unroll
-            for (int i = 0; i < 8; ++i) {
-              const float4 q = r == rank ? make_float4(w[4 * i], w[4 * i + 1], w[4 * i + 2], w[4 * i + 3])
-                                         : lds_f4(from + 512u * i);
-              sum[4 * i] = r ? sum[4 * i] + q.x : q.x, sum[4 * i + 1] = r ? sum[4 * i + 1] + q.y : q.y;
-              sum[4 * i + 2] = r ? sum[4 * i + 2] + q.z : q.z, sum[4 * i + 3] = r ? sum[4 * i + 3] + q.w : q.w;
+          for (int i = 0; i < 8; ++i) {
+            const float4 own = make_float4(w[4 * i], w[4 * i + 1], w[4 * i + 2], w[4 * i + 3]);
+            float4 sum = rank == 0 ? own : lds_f4(at + 512u * i);
+#pragma unroll
+            for (uint32_t r = 1; r < kMaxSplit; ++r) {
+              if (r >= S) continue;
+              const float4 q = r == rank ? own : lds_f4(at + 512u * i + (r < rank ? r : r - 1) * (NA * kSquare));
+              sum.x += q.x, sum.y += q.y, sum.z += q.z, sum.w += q.w;
             }
+            w[4 * i] = sum.x, w[4 * i + 1] = sum.y, w[4 * i + 2] = sum.z, w[4 * i + 3] = sum.w;
           }
-#pragma unroll
-          for (int i = 0; i < 32; ++i) w[i] = sum[i];
         };
         add(src, v);
         if constexpr (GATED) add(src + kSquare, u);
@@ -994,17 +1012,52 @@ cudaError_t launch_rows(const LinearParams& p, cudaStream_t st) {
   return cudaGetLastError();
 }
 
+// How long each way of doing a product takes, in ns, from measurements of the
+// parts (steps of 64 columns of K): what a launch and a tile cost besides their
+// steps, a step by what its copies move per SM (about 110 bytes per ns) or by
+// its MMAs, an epilogue unit.
+struct Way {
+  int pair, width, S;  // pair: TN; tile: FN, CTAs of a cluster
+  float ns;
+};
+float max_f(float a, float b) { return a > b ? a : b; }
+Way best_way(int T, int K, int N, bool gated, int sms) {
+  const int KB = (K + kKB - 1) / kKB, na = gated ? 2 : 1;
+  Way best = {0, 0, 0, 1e30f};
+  const int BT = T <= 32 ? 32 : T <= 64 ? 64 : 128;
+  for (int FN = 32; FN <= (gated ? 64 : 128); FN *= 2) {
+    const int64_t tiles = (int64_t)((N + FN - 1) / FN) * ((T + BT - 1) / BT);
+    if (tiles > 8 * sms) continue;
+    for (int S = 1; S <= kMaxSplit && S <= KB; S *= 2) {
+      const int64_t waves = (tiles * S + (S == 4 ? 127 : sms - 1)) / (S == 4 ? 128 : sms);
+      const float step = max_f(170.f, (float)(BT + na * FN) * 128.f / 110.f);
+      const int units = (FN / 32 + 1) / 2;  // of a warp
+      const float tail = S == 1 ? 500.f * units : 1100.f + 300.f * (S - 1) + 500.f * ((units + S - 1) / S);
+      const float ns = (float)waves * (2500.f + (float)((KB + S - 1) / S) * step + na * tail);
+      if (ns < best.ns) best = {0, FN, S, ns};
+    }
+  }
+  for (int TN = 128; TN <= 256; TN *= 2) {
+    const int FN = TN / na;
+    const int64_t tiles = (int64_t)((T + 255) / 256) * ((N + FN - 1) / FN);
+    const int64_t waves = (tiles + sms / 2 - 1) / (sms / 2);
+    const float steps = (float)KB * (TN == 256 ? 300.f : 220.f), epilogue = 500.f * FN / 64 * na;
+    const float ns = 4000.f + (float)waves * max_f(steps, epilogue) + epilogue;
+    if (ns < best.ns) best = {TN, 0, 1, ns};
+  }
+  return best;
+}
+
 template <bool F16, bool GATED>
 cudaError_t launch_tensor(const LinearParams& p, int sms, cudaStream_t st) {
-  if (p.T <= 256) {
-    const int BT = p.T <= 16 ? 16 : p.T <= 32 ? 32 : p.T <= 64 ? 64 : 128, KB = (p.K + kKB - 1) / kKB;
-    const int FN = 64;
-    const int tiles = (p.N + FN - 1) / FN * ((p.T + BT - 1) / BT);
-    int S = 1;
-    while (S < kMaxSplit && 2 * S * tiles <= sms && 2 * S <= KB) S *= 2;
-    return launch_tile_t<F16, GATED, FN>(p, BT, S, st);
-  }
-  return launch_pair_t<F16, GATED, 256>(p, sms, st);
+  const Way w = best_way(p.T, p.K, p.N, GATED, sms);
+  if (w.pair == 256) return launch_pair_t<F16, GATED, 256>(p, sms, st);
+  if (w.pair == 128) return launch_pair_t<F16, GATED, 128>(p, sms, st);
+  const int BT = p.T <= 32 ? 32 : p.T <= 64 ? 64 : 128;
+  if (w.width == 32) return launch_tile_t<F16, GATED, 32>(p, BT, w.S, st);
+  if (w.width == 64) return launch_tile_t<F16, GATED, 64>(p, BT, w.S, st);
+  if constexpr (!GATED) return launch_tile_t<F16, GATED, 128>(p, BT, w.S, st);
+  return cudaErrorInvalidValue;
 }
 
 template <bool F16, bool GATED>
