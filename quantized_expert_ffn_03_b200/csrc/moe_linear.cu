@@ -342,7 +342,10 @@ constexpr uint32_t kTile = 128u * 128u;  // bytes of a 128-row operand tile of o
 // row of 32 features at a time.
 constexpr uint32_t kSquare = 4096u;  // bytes per warp: 32 x 32 fp32, or two of 16 bits
 
-template <bool F16, bool GATED>
+// DIRECT: the lanes write their tokens' 64 bytes themselves, which takes more
+// store instructions but no wait for the store to have read shared memory:
+// for a block that ends with it.
+template <bool F16, bool GATED, bool DIRECT>
 struct Epilogue {
   const LinearParams& p;
   const CUtensorMap* map;  // of out, in boxes of 32 x 32
@@ -421,6 +424,15 @@ struct Epilogue {
             for (int i = 0; i < 32; ++i)
               if (n0 + i < p.N) v[i] += from16<F16>(src[i]);
           }
+        }
+        if (DIRECT && whole) {
+          if (!live) return;
+          uint4* dst = reinterpret_cast<uint4*>(static_cast<uint16_t*>(p.out) + (size_t)(t0 + lane) * p.ldo + n0);
+#pragma unroll
+          for (int j = 0; j < 4; ++j)
+            dst[j] = make_uint4(pack16<F16>(v[8 * j], v[8 * j + 1]), pack16<F16>(v[8 * j + 2], v[8 * j + 3]),
+                                pack16<F16>(v[8 * j + 4], v[8 * j + 5]), pack16<F16>(v[8 * j + 6], v[8 * j + 7]));
+          return;
         }
         // two squares of 2 KB in turn: the store before the last has been read out
         const uint32_t sq = square + (turn++ & 1u) * (kSquare / 2);
@@ -558,13 +570,16 @@ __global__ void __launch_bounds__(kTileThreads, 1)
   };
   const int first = min(kb1 - kb0, plan.stages);
   if (warp == kTileEpi) {
-    // the first copies are on their way before the block has met
+    // the first copies are on their way before the block has met, and the
+    // block does not wait for them to be issued (the copy engine takes in
+    // about 50 bytes per clock)
     if (lead) {
       for (int s = 0; s < plan.stages; ++s) bar_init(full + 8u * s, 1), bar_init(empty + 8u * s, 1);
       bar_init(accfull, 1);
       mbar_fence_init();
     }
     __syncwarp();
+    asm volatile("bar.arrive 1, %0;" ::"n"(kTileThreads) : "memory");
 #pragma unroll 1
     for (int i = 0; i < first; ++i) {
       if (lead) copy(kb0 + i, (uint32_t)i);
@@ -576,7 +591,7 @@ __global__ void __launch_bounds__(kTileThreads, 1)
     tc::tmem_relinquish();
   }
   tc::fence_before_sync();
-  __syncthreads();
+  if (warp != kTileEpi) named_sync(1, kTileThreads);
   tc::fence_after_sync();
   tc::cluster_arrive();  // (1) this CTA runs: its shared memory may be written
   const uint32_t tmem = tmem_slot;
@@ -598,7 +613,7 @@ __global__ void __launch_bounds__(kTileThreads, 1)
     tc::wait_ld();
   };
 
-  Epilogue<F16, GATED> epi(p, &map_out, lane, s0 + (uint32_t)warp * kSquare);  // (in the stages, once they are done with)
+  Epilogue<F16, GATED, true> epi(p, &map_out, lane, s0 + (uint32_t)warp * kSquare);  // (in the stages, once they are done with)
   int mine = -1;
   if (warp == kTileEpi) {
     bool ok = true;
@@ -852,7 +867,7 @@ __global__ void __launch_bounds__(kPairThreads, 1)
     constexpr int UN = FN / 64;  // units of a warp
     const int quarter = warp & 3, half = warp >> 2;
     const uint32_t accfree0 = tc::map_rank(accfree, 0);
-    Epilogue<F16, GATED> epi(p, &map_out, lane, op0 + ST * P::kStage + (uint32_t)warp * kSquare);
+    Epilogue<F16, GATED, false> epi(p, &map_out, lane, op0 + ST * P::kStage + (uint32_t)warp * kSquare);
     uint32_t it = 0;
 #pragma unroll 1
     for (int tile = pair; tile < ntiles; tile += npairs, ++it) {
