@@ -201,6 +201,8 @@ __global__ void __launch_bounds__(32 * kRowsWarps, 4) linear_rows_kernel(const L
   constexpr int NA = GATED ? 2 : 1, NX = TM / 8;
   extern __shared__ __align__(128) uint8_t smem_raw[];
   __shared__ float red[kRowsWarps][NA][TM][kRowsFeat];
+  next_may_start();
+  prior_wait();
   const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5, g = lane >> 2, t = lane & 3;
   const int n0 = blockIdx.x * kRowsFeat;
   const bool wl = n0 + g < p.N;
@@ -557,6 +559,7 @@ __global__ void __launch_bounds__(kTileThreads, 1)
   const int KB = (p.K + kKB - 1) / kKB;
   const int kb0 = (int)((int64_t)KB * rank / S), kb1 = (int)((int64_t)KB * (rank + 1) / S);
 
+  next_may_start();
   // The loading and the MMA warp run their loops as whole warps, so that
   // addresses and descriptors stay in uniform registers, and one lane issues:
   // with the loops inside a one-lane branch a step took 350 ns whatever its size.
@@ -580,6 +583,7 @@ __global__ void __launch_bounds__(kTileThreads, 1)
     }
     __syncwarp();
     asm volatile("bar.arrive 1, %0;" ::"n"(kTileThreads) : "memory");
+    prior_wait();
 #pragma unroll 1
     for (int i = 0; i < first; ++i) {
       if (lead) copy(kb0 + i, (uint32_t)i);
@@ -591,7 +595,10 @@ __global__ void __launch_bounds__(kTileThreads, 1)
     tc::tmem_relinquish();
   }
   tc::fence_before_sync();
-  if (warp != kTileEpi) named_sync(1, kTileThreads);
+  if (warp != kTileEpi) {
+    named_sync(1, kTileThreads);
+    prior_wait();
+  }
   tc::fence_after_sync();
   tc::cluster_arrive();  // (1) this CTA runs: its shared memory may be written
   const uint32_t tmem = tmem_slot;
@@ -770,6 +777,7 @@ __global__ void __launch_bounds__(kPairThreads, 1)
   const int ntiles = MT * FT, npairs = gridDim.x / 2, pair = blockIdx.x / 2;
   const int KB = (p.K + kKB - 1) / kKB;
 
+  next_may_start();
   if (warp == kPairEpi && lane == 0) {
     tc::prefetch_map(GATED && rank ? &map_u : &map_w);
     tc::prefetch_map(&map_x);
@@ -789,6 +797,7 @@ __global__ void __launch_bounds__(kPairThreads, 1)
   tc::cluster_wait();
   tc::fence_after_sync();
   const uint32_t tmem = tmem_slot;
+  prior_wait();
 
   // (whole warps run the loops, one lane issues, as in linear_tile_kernel)
   if (warp == kPairEpi) {
@@ -975,24 +984,10 @@ bool make_maps(const LinearParams& p, int rows, int BT, Maps* m) {
          (p.vec != 2 || make_out_map(&m->out, F16, p));
 }
 
-// A launch with clusters along x.
 template <auto Kernel, class... Args>
 cudaError_t launch_cluster(dim3 grid, int threads, int cluster, uint32_t smem, cudaStream_t st, const Args&... args) {
   const cudaError_t e = allow_smem<Kernel>(kMaxSmem);
-  if (e != cudaSuccess) return e;
-  cudaLaunchConfig_t c = {};
-  c.gridDim = grid;
-  c.blockDim = dim3(threads);
-  c.dynamicSmemBytes = smem;
-  c.stream = st;
-  cudaLaunchAttribute a[1];
-  a[0].id = cudaLaunchAttributeClusterDimension;
-  a[0].val.clusterDim.x = cluster;
-  a[0].val.clusterDim.y = 1;
-  a[0].val.clusterDim.z = 1;
-  c.attrs = a;
-  c.numAttrs = 1;
-  return cudaLaunchKernelEx(&c, Kernel, args...);
+  return e != cudaSuccess ? e : launch_early(Kernel, grid, threads, smem, cluster, st, args...);
 }
 
 template <bool F16, bool GATED, int FN>
@@ -1023,8 +1018,7 @@ cudaError_t launch_rows(const LinearParams& p, cudaStream_t st) {
   constexpr uint32_t smem = rows_smem(GATED ? 2 : 1);
   const cudaError_t e = allow_smem<linear_rows_kernel<F16, GATED, TM>>(smem);
   if (e != cudaSuccess) return e;
-  linear_rows_kernel<F16, GATED, TM><<<(p.N + kRowsFeat - 1) / kRowsFeat, 32 * kRowsWarps, smem, st>>>(p);
-  return cudaGetLastError();
+  return launch_early(linear_rows_kernel<F16, GATED, TM>, (p.N + kRowsFeat - 1) / kRowsFeat, 32 * kRowsWarps, smem, 1, st, p);
 }
 
 // How long each way of doing a product takes, in ns, from measurements of the

@@ -24,6 +24,29 @@ struct LinearParams {
   int64_t ldx, ldw, ldw_up, ldr, ldo;
 };
 
+// A launch of `kernel` that may start before the kernel ahead of it in the
+// stream has ended (it waits for that itself: prior_wait), with clusters of
+// `cluster` blocks along x.
+template <class... P, class... A>
+cudaError_t launch_early(void (*kernel)(P...), dim3 grid, int threads, size_t smem, int cluster, cudaStream_t st,
+                         const A&... args) {
+  cudaLaunchConfig_t c = {};
+  c.gridDim = grid;
+  c.blockDim = dim3(threads);
+  c.dynamicSmemBytes = smem;
+  c.stream = st;
+  cudaLaunchAttribute a[2];
+  a[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+  a[0].val.programmaticStreamSerializationAllowed = 1;
+  a[1].id = cudaLaunchAttributeClusterDimension;
+  a[1].val.clusterDim.x = cluster;
+  a[1].val.clusterDim.y = 1;
+  a[1].val.clusterDim.z = 1;
+  c.attrs = a;
+  c.numAttrs = cluster > 1 ? 2 : 1;
+  return cudaLaunchKernelEx(&c, kernel, args...);
+}
+
 // f16: the 16-bit type is fp16, else bf16.  sms: the device's SM count.
 cudaError_t launch_linear(const LinearParams& p, bool f16, int sms, cudaStream_t st);
 cudaError_t read_linear_error(uint32_t* code, cudaStream_t st);

@@ -328,6 +328,8 @@ __global__ void __launch_bounds__(32 * kRouteWarps, NV <= 16 ? 7 : NV == 32 ? 5 
   __shared__ float cval_all[kRouteWarps][32];
   const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
   const int64_t t = (int64_t)blockIdx.x * kRouteWarps + warp;
+  next_may_start();
+  prior_wait();
   if (t >= p.T) return;
   uint64_t* key = keys_all + (size_t)warp * p.E;
   float* val = reinterpret_cast<float*>(key);  // groups: the values by expert
@@ -536,8 +538,7 @@ cudaError_t launch_route_nv(const RouteParams& p, cudaStream_t st) {
                                                (int)(sizeof(uint64_t) * kRouteWarps * kRouteMaxExperts));
     if (e != cudaSuccess) return e;
   }
-  route_kernel<T, NV><<<(p.T + kRouteWarps - 1) / kRouteWarps, 32 * kRouteWarps, smem, st>>>(p);
-  return cudaGetLastError();
+  return launch_early(route_kernel<T, NV>, (p.T + kRouteWarps - 1) / kRouteWarps, 32 * kRouteWarps, smem, 1, st, p);
 }
 
 template <typename T>
