@@ -390,25 +390,36 @@ MOE_GROUP_MAX, MOE_GROUP_TOP2 = 0, 1
 
 _DTYPE_NAMES = {MOE_BF16: ("bfloat16", "int16", "uint16"), MOE_F16: ("float16", "int16", "uint16"),
                 MOE_F32: ("float32",)}
-_dtype_sets = {}
+_dtype_sets = {}  # code -> torch types of its elements (16-bit types also as integer views)
+_logit_codes = {}  # torch type -> code
+_torch_c = _int32 = None
 
 
-def _is_dtype(t, code):
-    """Whether tensor t holds elements of the code (16-bit types also as integer views)."""
-    s = _dtype_sets.get(code)
-    if s is None:
-        import torch
-        s = _dtype_sets[code] = frozenset(getattr(torch, n) for n in _DTYPE_NAMES[code])
-    return t.dtype in s
+def _types():
+    """Looks torch up, once; the package imports without it."""
+    global _torch_c, _int32
+    import torch
+    _dtype_sets.update({c: frozenset(getattr(torch, n) for n in names) for c, names in _DTYPE_NAMES.items()})
+    _logit_codes.update({torch.float32: MOE_F32, torch.bfloat16: MOE_BF16, torch.float16: MOE_F16})
+    _int32, _torch_c = torch.int32, torch._C
+    torch.cuda.current_stream()  # initialises CUDA
 
 
 def _bad(what):
     raise MoeError(MOE_ERR_INVALID_ARG, what)
 
 
+def _current():
+    """(current CUDA device, raw handle of its current stream)."""
+    if _torch_c is None:
+        _types()
+    dev = _torch_c._cuda_getDevice()
+    return dev, _torch_c._cuda_getCurrentRawStream(dev)
+
+
 def _rows(t, name, shape, code, dev):
     """Row stride of a 2-d CUDA tensor with adjacent columns; raises otherwise."""
-    if t.shape != shape or not _is_dtype(t, code):
+    if t.shape != shape or t.dtype not in _dtype_sets[code]:
         _bad("%s must be %s of type %s, got %s %s" % (name, tuple(shape), _DTYPE_NAMES[code][0], tuple(t.shape), t.dtype))
     if t.get_device() != dev:
         _bad("%s must be on the current CUDA device" % name)
@@ -419,25 +430,11 @@ def _rows(t, name, shape, code, dev):
 
 
 def _vec(t, name, n, dev):
-    if t.shape != (n,) or not _is_dtype(t, MOE_F32) or (n > 1 and t.stride(0) != 1):
+    if t.shape != (n,) or t.dtype not in _dtype_sets[MOE_F32] or (n > 1 and t.stride(0) != 1):
         _bad("%s must be a contiguous float32 vector of %d" % (name, n))
     if t.get_device() != dev:
         _bad("%s must be on the current CUDA device" % name)
     return t.data_ptr()
-
-
-_torch_c = None
-
-
-def _current():
-    """(current CUDA device, raw handle of its current stream)."""
-    global _torch_c
-    if _torch_c is None:
-        import torch
-        _torch_c = torch._C
-        torch.cuda.current_stream()  # initialises CUDA
-    dev = _torch_c._cuda_getDevice()
-    return dev, _torch_c._cuda_getCurrentRawStream(dev)
 
 
 def linear_config(in_features, out_features, act=MOE_ACT_NONE, gated=False, dtype=MOE_BF16, out_dtype=None):
@@ -448,7 +445,11 @@ def linear_config(in_features, out_features, act=MOE_ACT_NONE, gated=False, dtyp
 def linear_weights(cfg, w, bias=None, w_up=None, bias_up=None):
     """w, w_up: CUDA tensors [out_features][in_features]; bias, bias_up: float32 [out_features] or None.
     The result keeps the tensors alive."""
+    if _torch_c is None:
+        _types()
     shape, dev = (cfg.out_features, cfg.in_features), w.get_device()
+    if dev < 0:
+        _bad("w must be on a CUDA device")
     if (w_up is not None) != bool(cfg.gated) or (bias_up is not None and w_up is None):
         _bad("w_up goes with a gated config, bias_up with w_up")
     ld = _rows(w, "w", shape, cfg.dtype, dev)
@@ -456,7 +457,7 @@ def linear_weights(cfg, w, bias=None, w_up=None, bias_up=None):
     wts = MoeLinearWeights(w.data_ptr(), _ptr(w_up), None if bias is None else _vec(bias, "bias", shape[0], dev),
                            None if bias_up is None else _vec(bias_up, "bias_up", shape[0], dev), ld, ld_up)
     wts.kept = (w, bias, w_up, bias_up)
-    wts.made_for = (shape, cfg.dtype, cfg.gated, dev)
+    wts.made_for = (shape[0], shape[1], cfg.dtype, cfg.gated, dev)
     return wts
 
 
@@ -464,17 +465,20 @@ def moe_linear_forward(cfg, wts, x, out, residual=None, stream=None):
     """out = act(x w^T + bias) [* (x w_up^T + bias_up)] [+ residual] (see moe.h).  x [T][in], out and
     residual [T][out]: CUDA tensors with adjacent columns; out may be residual itself."""
     dev, st = _current()
-    T, N, K = x.shape[0], cfg.out_features, cfg.in_features
-    if wts.made_for != ((N, K), cfg.dtype, cfg.gated, dev):
+    N, K, code, gated, at = wts.made_for
+    if cfg.in_features != K or cfg.out_features != N or cfg.dtype != code or cfg.gated != gated or at != dev:
         _bad("the weights were made for another config or device")
-    ldx = _rows(x, "x", (T, K), cfg.dtype, dev)
-    ldo = _rows(out, "out", (T, N), cfg.out_dtype, dev)
-    res, ldr = None, 0
-    if residual is not None:
-        ldr = _rows(residual, "residual", (T, N), cfg.out_dtype, dev)
-        res = residual.data_ptr()
-    _check(_lib.moe_linear_forward(C.byref(cfg), C.byref(wts), x.data_ptr(), ldx, res, ldr, T, out.data_ptr(), ldo,
-                                   st if stream is None else _stream(stream)))
+    T, out_code = x.shape[0], cfg.out_dtype
+    ldx = _rows(x, "x", (T, K), code, dev)
+    ldo = _rows(out, "out", (T, N), out_code, dev)
+    if residual is None:
+        res, ldr = None, 0
+    else:
+        res, ldr = residual.data_ptr(), _rows(residual, "residual", (T, N), out_code, dev)
+    err = _lib.moe_linear_forward(C.byref(cfg), C.byref(wts), x.data_ptr(), ldx, res, ldr, T, out.data_ptr(), ldo,
+                                  st if stream is None else _stream(stream))
+    if err:
+        _check(err)
 
 
 def moe_linear_device_error(stream=None):
@@ -489,10 +493,10 @@ def route_config(n_experts, top_k, score=MOE_SCORE_SOFTMAX, n_groups=1, topk_gro
     return MoeRouteConfig(n_experts, top_k, score, n_groups, topk_groups, group_score, 1 if renormalise else 0, scale)
 
 
-def _route_out(cfg, T, idx, w, dev):
-    shape = (T, cfg.top_k)
-    if idx.shape != shape or w.shape != shape or not idx.is_contiguous() or not w.is_contiguous() \
-            or str(idx.dtype) != "torch.int32" or not _is_dtype(w, MOE_F32):
+def _route_out(T, K, idx, w, dev):
+    shape = (T, K)
+    if idx.shape != shape or w.shape != shape or idx.dtype is not _int32 or w.dtype not in _dtype_sets[MOE_F32] \
+            or not idx.is_contiguous() or not w.is_contiguous():
         _bad("idx and w must be contiguous int32 and float32 tensors of %s" % (shape,))
     if idx.get_device() != dev or w.get_device() != dev:
         _bad("idx and w must be on the current CUDA device")
@@ -502,13 +506,15 @@ def moe_route_from_logits(cfg, logits, idx, w, select_bias=None, stream=None):
     """Expert choice (see moe.h).  logits: float32, bfloat16 or float16 CUDA tensor [T][E] with adjacent
     columns; idx int32 [T][K], w float32 [T][K] (written)."""
     dev, st = _current()
-    T = logits.shape[0]
-    code = MOE_F32 if _is_dtype(logits, MOE_F32) else MOE_BF16 if str(logits.dtype) == "torch.bfloat16" else MOE_F16
-    ld = _rows(logits, "logits", (T, cfg.n_experts), code, dev)
-    _route_out(cfg, T, idx, w, dev)
-    bias = None if select_bias is None else _vec(select_bias, "select_bias", cfg.n_experts, dev)
-    _check(_lib.moe_route_from_logits(C.byref(cfg), logits.data_ptr(), code, ld, bias, T, idx.data_ptr(),
-                                      w.data_ptr(), st if stream is None else _stream(stream)))
+    T, E = logits.shape[0], cfg.n_experts
+    code = _logit_codes.get(logits.dtype, MOE_F32)
+    ld = _rows(logits, "logits", (T, E), code, dev)
+    _route_out(T, cfg.top_k, idx, w, dev)
+    bias = None if select_bias is None else _vec(select_bias, "select_bias", E, dev)
+    err = _lib.moe_route_from_logits(C.byref(cfg), logits.data_ptr(), code, ld, bias, T, idx.data_ptr(), w.data_ptr(),
+                                     st if stream is None else _stream(stream))
+    if err:
+        _check(err)
 
 
 def moe_route_workspace_bytes(cfg, T):
@@ -529,7 +535,7 @@ def moe_route_topk(cfg, x, wr, idx, w, router_bias=None, select_bias=None, logit
         _rows(logits_out, "logits_out", (T, E), MOE_F32, dev)
     if workspace is not None and (workspace.get_device() != dev or not workspace.is_contiguous()):
         _bad("workspace must be contiguous, on the current CUDA device")
-    _route_out(cfg, T, idx, w, dev)
+    _route_out(T, cfg.top_k, idx, w, dev)
     rb = None if router_bias is None else _vec(router_bias, "router_bias", E, dev)
     sb = None if select_bias is None else _vec(select_bias, "select_bias", E, dev)
     _check(_lib.moe_route_topk(C.byref(cfg), H, x.data_ptr(), wr.data_ptr(), rb, sb, T, idx.data_ptr(), w.data_ptr(),
