@@ -166,17 +166,21 @@ __device__ __forceinline__ void mma16816(float (&c)[4], uint32_t a0, uint32_t a1
 }
 
 // A block takes 8 features (the N of m16n8k16 steps) and up to 16 tokens (its
-// M; TM of them); its 8 warps take the 64-column units of K in turn.  Lane
+// M; TM of them); its W warps take the 64-column units of K in turn.  Lane
 // (g, t) of a warp fetches 16 bytes of weight row g at columns 8t.. of each
 // 32-column half unit: the order of columns within a sum is free, so those 8
 // values serve as fragments of two k16 steps without a shuffle, and x is
-// read the same way.  Weights go through a ring of kRowsDepth units of shared
-// memory by cp.async, where each lane reads back what it copied itself: no
-// barrier, no registers held by loads in flight, and about 190 KB on their
-// way per SM (4 blocks of 48 KB).
-constexpr int kRowsFeat = 8, kRowsTok = 16, kRowsWarps = 8, kRowsDepth = 6;
+// read the same way.  Weights go through a ring of units in shared memory by
+// cp.async, where each lane reads back what it copied itself: no barrier, and
+// no registers held by loads in flight.  32 warps an SM with 3 units each on
+// their way (96 KB) suffice; deeper rings take the L1 cache from x (one token,
+// 4096 x 4096: 8.3 us with 4 slots, 8.8 with 6, 8.9 with 3).  With few blocks a
+// block takes more warps, so that an SM has its 32 all the same (512 features:
+// 3.5 us with 32, 4.4 with 8).
+constexpr int kRowsFeat = 8, kRowsTok = 16;
 constexpr uint32_t kRowsUnit = 1024u;  // bytes of a warp's unit: 8 rows x 64 columns
-constexpr uint32_t rows_smem(int na) { return (uint32_t)(kRowsWarps * kRowsDepth * na) * kRowsUnit; }
+__host__ __device__ constexpr int rows_depth(int na) { return na == 1 ? 4 : 3; }
+__host__ __device__ constexpr uint32_t rows_smem(int na, int warps) { return (uint32_t)(warps * rows_depth(na) * na) * kRowsUnit; }
 
 // 16 bytes of a row from column k; columns from K on read as zero and are
 // never touched in memory.
@@ -196,11 +200,11 @@ __device__ __forceinline__ uint4 row_load16(const uint16_t* row, int k, int K, b
   return make_uint4(h[0], h[1], h[2], h[3]);
 }
 
-template <bool F16, bool GATED, int TM>
-__global__ void __launch_bounds__(32 * kRowsWarps, 4) linear_rows_kernel(const LinearParams p) {
-  constexpr int NA = GATED ? 2 : 1, NX = TM / 8;
+template <bool F16, bool GATED, int TM, int W>
+__global__ void __launch_bounds__(32 * W, 32 / W) linear_rows_kernel(const LinearParams p) {
+  constexpr int NA = GATED ? 2 : 1, NX = TM / 8, kDepth = rows_depth(NA);
   extern __shared__ __align__(128) uint8_t smem_raw[];
-  __shared__ float red[kRowsWarps][NA][TM][kRowsFeat];
+  __shared__ float red[W][NA][TM][kRowsFeat];
   next_may_start();
   prior_wait();
   const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5, g = lane >> 2, t = lane & 3;
@@ -209,12 +213,12 @@ __global__ void __launch_bounds__(32 * kRowsWarps, 4) linear_rows_kernel(const L
   const uint16_t* wr[NA];
   wr[0] = p.w + (size_t)(wl ? n0 + g : 0) * p.ldw;
   if constexpr (GATED) wr[1] = p.w_up + (size_t)(wl ? n0 + g : 0) * p.ldw_up;
-  const uint32_t ring = smem_u32(smem_raw) + (uint32_t)(warp * kRowsDepth * NA) * kRowsUnit + 16u * (uint32_t)lane;
-  const int units = (p.K + kKB - 1) / kKB, mine = (units - warp + kRowsWarps - 1) / kRowsWarps;
+  const uint32_t ring = smem_u32(smem_raw) + (uint32_t)(warp * kDepth * NA) * kRowsUnit + 16u * (uint32_t)lane;
+  const int units = (p.K + kKB - 1) / kKB, mine = (units - warp + W - 1) / W;
   auto fetch = [&](int i) {  // this warp's unit i, or an empty group behind the last
     if (i < mine) {
-      const int k = kKB * (warp + kRowsWarps * i) + 8 * t;
-      const uint32_t dst = ring + (uint32_t)(i % kRowsDepth * NA) * kRowsUnit;
+      const int k = kKB * (warp + W * i) + 8 * t;
+      const uint32_t dst = ring + (uint32_t)(i % kDepth * NA) * kRowsUnit;
 #pragma unroll
       for (int a = 0; a < NA; ++a) {
         row_copy16(dst + (uint32_t)a * kRowsUnit, wr[a], k, p.K, wl);
@@ -224,7 +228,7 @@ __global__ void __launch_bounds__(32 * kRowsWarps, 4) linear_rows_kernel(const L
     asm volatile("cp.async.commit_group;" ::: "memory");
   };
 #pragma unroll
-  for (int i = 0; i < kRowsDepth - 1; ++i) fetch(i);
+  for (int i = 0; i < kDepth - 1; ++i) fetch(i);
 
   bool xl[NX];
   const uint16_t* xr[NX];
@@ -234,17 +238,27 @@ __global__ void __launch_bounds__(32 * kRowsWarps, 4) linear_rows_kernel(const L
     xr[j] = p.x + (size_t)(xl[j] ? g + 8 * j : 0) * p.ldx;
   }
   float acc[NA][4] = {};
-#pragma unroll 1
-  for (int i = 0; i < mine; ++i) {
-    const int k = kKB * (warp + kRowsWarps * i) + 8 * t;
-    uint4 xv[NX][2];
+  // x comes a unit ahead (its way from L2 takes as long as a turn) where the
+  // registers for it leave room for 4 blocks per SM
+  uint4 next[NX][2];
+  auto load_x = [&](int i) {
+    const int k = kKB * (warp + W * i) + 8 * t;
 #pragma unroll
     for (int j = 0; j < NX; ++j) {
-      xv[j][0] = row_load16(xr[j], k, p.K, xl[j]);
-      xv[j][1] = row_load16(xr[j], k + 32, p.K, xl[j]);
+      next[j][0] = row_load16(xr[j], k, p.K, xl[j] && i < mine);
+      next[j][1] = row_load16(xr[j], k + 32, p.K, xl[j] && i < mine);
     }
-    asm volatile("cp.async.wait_group %0;" ::"n"(kRowsDepth - 2) : "memory");
-    const uint32_t src = ring + (uint32_t)(i % kRowsDepth * NA) * kRowsUnit;
+  };
+  if (TM == 8) load_x(0);
+#pragma unroll 1
+  for (int i = 0; i < mine; ++i) {
+    if (TM != 8) load_x(i);
+    uint4 xv[NX][2];
+#pragma unroll
+    for (int j = 0; j < NX; ++j) xv[j][0] = next[j][0], xv[j][1] = next[j][1];
+    if (TM == 8) load_x(i + 1);
+    asm volatile("cp.async.wait_group %0;" ::"n"(kDepth - 2) : "memory");
+    const uint32_t src = ring + (uint32_t)(i % kDepth * NA) * kRowsUnit;
     uint4 wv[NA][2];
 #pragma unroll
     for (int a = 0; a < NA; ++a)
@@ -254,7 +268,7 @@ __global__ void __launch_bounds__(32 * kRowsWarps, 4) linear_rows_kernel(const L
                      : "=r"(wv[a][h].x), "=r"(wv[a][h].y), "=r"(wv[a][h].z), "=r"(wv[a][h].w)
                      : "r"(src + (uint32_t)a * kRowsUnit + 512u * (uint32_t)h)
                      : "memory");
-    fetch(i + kRowsDepth - 1);  // into the slot that the last turn read
+    fetch(i + kDepth - 1);  // into the slot that the last turn read
 #pragma unroll
     for (int a = 0; a < NA; ++a)
 #pragma unroll
@@ -275,7 +289,7 @@ __global__ void __launch_bounds__(32 * kRowsWarps, 4) linear_rows_kernel(const L
 #pragma unroll
     for (int a = 0; a < NA; ++a)
 #pragma unroll
-      for (int w = 0; w < kRowsWarps; ++w) s[a] += red[w][a][c][f];
+      for (int w = 0; w < W; ++w) s[a] += red[w][a][c][f];
     finish_one<F16>(p, c, n0 + f, s[0], s[1]);
   }
 }
@@ -1013,12 +1027,21 @@ cudaError_t launch_pair_t(const LinearParams& p, int sms, cudaStream_t st) {
                                                                   st, m.w, m.u, m.x, m.out, p);
 }
 
-template <bool F16, bool GATED, int TM>
-cudaError_t launch_rows(const LinearParams& p, cudaStream_t st) {
-  constexpr uint32_t smem = rows_smem(GATED ? 2 : 1);
-  const cudaError_t e = allow_smem<linear_rows_kernel<F16, GATED, TM>>(smem);
+template <bool F16, bool GATED, int TM, int W>
+cudaError_t launch_rows_w(const LinearParams& p, cudaStream_t st) {
+  constexpr uint32_t smem = rows_smem(GATED ? 2 : 1, W);
+  const cudaError_t e = allow_smem<linear_rows_kernel<F16, GATED, TM, W>>(smem);
   if (e != cudaSuccess) return e;
-  return launch_early(linear_rows_kernel<F16, GATED, TM>, (p.N + kRowsFeat - 1) / kRowsFeat, 32 * kRowsWarps, smem, 1, st, p);
+  return launch_early(linear_rows_kernel<F16, GATED, TM, W>, (p.N + kRowsFeat - 1) / kRowsFeat, 32 * W, smem, 1, st, p);
+}
+
+// Warps of a block: 32 an SM, as long as there are units of K for them.
+template <bool F16, bool GATED, int TM>
+cudaError_t launch_rows(const LinearParams& p, int sms, cudaStream_t st) {
+  const int blocks = (p.N + kRowsFeat - 1) / kRowsFeat;
+  if (blocks <= sms && p.K > 8 * kKB) return launch_rows_w<F16, GATED, TM, 32>(p, st);
+  if (blocks <= 2 * sms && p.K > 8 * kKB) return launch_rows_w<F16, GATED, TM, 16>(p, st);
+  return launch_rows_w<F16, GATED, TM, 8>(p, st);
 }
 
 // How long each way of doing a product takes, in ns, from measurements of the
@@ -1050,8 +1073,8 @@ Way best_way(int T, int K, int N, bool gated, int sms) {
     const int FN = TN / na;
     const int64_t tiles = (int64_t)((T + 255) / 256) * ((N + FN - 1) / FN);
     const int64_t waves = (tiles + sms / 2 - 1) / (sms / 2);
-    const float steps = (float)KB * (TN == 256 ? 300.f : 220.f), epilogue = 500.f * FN / 64 * na;
-    const float ns = 4000.f + (float)waves * max_f(steps, epilogue) + epilogue;
+    const float steps = (float)KB * (TN == 256 ? 300.f : 205.f), epilogue = (TN == 256 ? 450.f : 500.f) * FN / 64 * na;
+    const float ns = 3300.f + (float)waves * max_f(steps, epilogue) + epilogue;
     if (ns < best.ns) best = {TN, 0, 1, ns};
   }
   return best;
@@ -1071,8 +1094,11 @@ cudaError_t launch_tensor(const LinearParams& p, int sms, cudaStream_t st) {
 
 template <bool F16, bool GATED>
 cudaError_t launch_any(const LinearParams& p, int sms, cudaStream_t st) {
-  if (p.T <= 8) return launch_rows<F16, GATED, 8>(p, st);
-  if (p.T <= kRowsTok) return launch_rows<F16, GATED, 16>(p, st);
+  // 9 to 16 tokens: weights beyond about 40 MB stream faster by TMA (8192 x 8192:
+  // 27 us against 35; 4096 x 4096: 9.5 against 9.3)
+  const bool heavy = (int64_t)p.N * p.K * (GATED ? 2 : 1) > (20 << 20) && encoder();
+  if (p.T <= 8) return launch_rows<F16, GATED, 8>(p, sms, st);
+  if (p.T <= kRowsTok && !heavy) return launch_rows<F16, GATED, 16>(p, sms, st);
   if (!encoder()) return cudaErrorNotSupported;
   return launch_tensor<F16, GATED>(p, sms, st);
 }

@@ -45,10 +45,11 @@ __device__ __forceinline__ float logit_of(const T* row, int e) {
   return l != l ? -INFINITY : fminf(l, FLT_MAX);
 }
 
+// The warp's largest value; NaN counts as none.
 __device__ __forceinline__ float warp_maxf(float v) {
-#pragma unroll
-  for (int o = 16; o; o >>= 1) v = fmaxf(v, __shfl_xor_sync(kAll, v, o));
-  return v;
+  float m;
+  asm volatile("redux.sync.max.f32 %0, %1, 0xffffffff;" : "=f"(m) : "f"(v));
+  return m;
 }
 
 // ---- the choice in fp64, for what the fp32 values below leave open ------------------------
@@ -257,8 +258,8 @@ __device__ __noinline__ void route_exact(const RouteParams& p, int64_t t, uint64
 // than lanes goes to route_exact.  Without a bias experts are ordered by their
 // logits, which needs no bound.
 //
-// Top-K in one go instead of K rounds over E: each lane's largest value; the
-// K-th largest of those 32 is a bound that at least K values reach; the values
+// Top-K without K rounds over E: each lane's largest value; the K-th largest
+// of those 32 is a bound that at least K values reach; the values
 // that reach it (a few more than K of E) are gathered one per lane, and each
 // lane counts how many beat its own.
 __device__ __forceinline__ uint32_t order32(float v) {
@@ -276,18 +277,16 @@ __device__ __forceinline__ float fast_exp(float x) {
   return y;
 }
 
-// The k-th largest (k from 0) of the lanes' values: a bitonic sort, descending.
-__device__ __forceinline__ float warp_kth(float v, int k) {
-  const int lane = threadIdx.x & 31;
-#pragma unroll
-  for (int size = 2; size <= 32; size <<= 1)
-#pragma unroll
-    for (int o = size >> 1; o; o >>= 1) {
-      const float other = __shfl_xor_sync(kAll, v, o);
-      const bool keep_max = ((lane & o) == 0) == ((lane & size) == 0);
-      v = keep_max ? fmaxf(v, other) : fminf(v, other);
-    }
-  return __shfl_sync(kAll, v, k);
+// A bound that at least K lanes reach: the K-th largest of the lanes' values, or
+// less where some are equal (equal ones leave together).
+__device__ __forceinline__ float warp_kth(float v, int K) {
+  float m = v;
+#pragma unroll 1
+  for (int k = 0; k < K; ++k) {
+    m = warp_maxf(v);
+    if (v >= m) v = -INFINITY;
+  }
+  return m;
 }
 
 template <bool LONG>
@@ -298,8 +297,6 @@ template <>
 struct MaskOf<true> {
   using type = uint64_t;
 };
-__device__ __forceinline__ int count_bits(uint32_t m) { return __popc(m); }
-__device__ __forceinline__ int count_bits(uint64_t m) { return __popcll(m); }
 __device__ __forceinline__ int lowest_bit(uint32_t m) { return __ffs(m) - 1; }
 __device__ __forceinline__ int lowest_bit(uint64_t m) { return __ffsll(m) - 1; }
 
@@ -319,7 +316,7 @@ struct Wide {
 };
 
 // NV: values per lane, a multiple of Wide<T>::W with 32 NV >= E.
-template <typename T, int NV>
+template <typename T, int NV, bool BIAS>
 __global__ void __launch_bounds__(32 * kRouteWarps, NV <= 16 ? 7 : NV == 32 ? 5 : 3) route_kernel(const RouteParams p) {
   constexpr int W = Wide<T>::W;
   extern __shared__ uint64_t keys_all[];
@@ -337,7 +334,7 @@ __global__ void __launch_bounds__(32 * kRouteWarps, NV <= 16 ? 7 : NV == 32 ? 5 
   uint64_t* ckey = ckey_all[warp];
   float* cval = cval_all[warp];
   const T* row = static_cast<const T*>(p.logits) + (size_t)t * p.ldl;
-  const bool by_value = p.bias != nullptr;
+  constexpr bool by_value = BIAS;
   // value i of this lane is expert place(i): W adjacent ones per 16-byte load
   auto place = [&](int i) { return W * (lane + 32 * (i / W)) + i % W; };
 
@@ -459,7 +456,7 @@ __global__ void __launch_bounds__(32 * kRouteWarps, NV <= 16 ? 7 : NV == 32 ? 5 
   float best = -INFINITY;
 #pragma unroll
   for (int i = 0; i < NV; ++i) best = fmaxf(best, v[i]);
-  float bound = warp_kth(best, p.K - 1);
+  float bound = warp_kth(best, p.K);
   if (by_value) bound -= 2.f * eps + 0x1p-22f * fabsf(bound);
   using Mask = typename MaskOf<(NV > 32)>::type;
   Mask mask = 0;
@@ -471,21 +468,13 @@ __global__ void __launch_bounds__(32 * kRouteWarps, NV <= 16 ? 7 : NV == 32 ? 5 
     for (int i = 0; i < NV; ++i)
       if ((grouped ? lane + 32 * i : place(i)) >= entries) mask &= ~((Mask)1 << i);
   }
-  const int mine = count_bits(mask);
-  int at = mine;
-#pragma unroll
-  for (int o = 1; o < 32; o <<= 1) {
-    const int x = __shfl_up_sync(kAll, at, o);
-    if (lane >= o) at += x;
+  int count = 0;
+  for (uint32_t with; (with = __ballot_sync(kAll, mask != 0)) != 0 && count <= 32; mask &= mask - 1) {
+    const int at = count + __popc(with & ((1u << lane) - 1u)), i = lowest_bit(mask);
+    if (mask && at < 32) cand[at] = grouped ? lane + 32 * i : place(i);
+    count += __popc(with);
   }
-  const int count = __shfl_sync(kAll, at, 31);
   if (count > 32) open = true;
-  if (!open) {
-    for (at -= mine; mask; mask &= mask - 1) {
-      const int i = lowest_bit(mask);
-      cand[at++] = grouped ? lane + 32 * i : place(i);
-    }
-  }
   __syncwarp();
 
   // ---- one candidate per lane: its rank, whether the order is certain ----
@@ -533,12 +522,13 @@ __global__ void __launch_bounds__(32 * kRouteWarps, NV <= 16 ? 7 : NV == 32 ? 5 
 template <typename T, int NV>
 cudaError_t launch_route_nv(const RouteParams& p, cudaStream_t st) {
   const size_t smem = sizeof(uint64_t) * kRouteWarps * (size_t)p.E;
+  const auto kernel = p.bias ? route_kernel<T, NV, true> : route_kernel<T, NV, false>;
   if (smem > 48 * 1024) {  // the largest E only
-    const cudaError_t e = cudaFuncSetAttribute(route_kernel<T, NV>, cudaFuncAttributeMaxDynamicSharedMemorySize,
+    const cudaError_t e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize,
                                                (int)(sizeof(uint64_t) * kRouteWarps * kRouteMaxExperts));
     if (e != cudaSuccess) return e;
   }
-  return launch_early(route_kernel<T, NV>, (p.T + kRouteWarps - 1) / kRouteWarps, 32 * kRouteWarps, smem, 1, st, p);
+  return launch_early(kernel, (p.T + kRouteWarps - 1) / kRouteWarps, 32 * kRouteWarps, smem, 1, st, p);
 }
 
 template <typename T>
