@@ -1028,6 +1028,7 @@ moe_status moe_route_from_logits(const moe_route_config* cfg, const void* logits
   p.top2 = cfg->group_score == MOE_GROUP_TOP2;
   p.per = p.E / p.n_groups;
   p.per_inv = p.per > 1 ? (uint32_t)(((1ull << 32) + p.per - 1) / p.per) : 0;
+  p.bias_vec = aligned(select_bias, 16);
   p.vec = aligned(logits, 16) && p.E * size % 16 == 0 && (T == 1 || ldl * size % 16 == 0);
   for (p.lane_shift = 5; (p.n_groups << p.lane_shift) > 32;) --p.lane_shift;
   p.renorm = cfg->renormalise;

@@ -59,6 +59,7 @@ struct RouteParams {
   int per;           // experts of a group
   uint32_t per_inv;  // ceil(2^32 / per): q / per as a high product, for per > 1
   int lane_shift;    // log2 of the lanes that share a group
+  int bias_vec;      // the bias starts on a 16-byte boundary
   int vec;           // every row of logits is whole 16-byte pieces on 16-byte boundaries
   int renorm;
   float scale;

@@ -341,6 +341,21 @@ __global__ void __launch_bounds__(32 * kRouteWarps, NV <= 16 ? 7 : NV == 32 ? 5 
   // value i of this lane is expert place(i): W adjacent ones per 16-byte load
   auto place = [&](int i) { return W * (lane + 32 * (i / W)) + i % W; };
 
+  // the biases are asked for before the logits are waited for
+  float b[BIAS ? NV : 1];
+  if constexpr (BIAS) {
+#pragma unroll
+    for (int i = 0; i < NV; i += 4) {
+      if (p.vec && p.bias_vec) {
+        const float4 q = place(i) < p.E ? __ldg(reinterpret_cast<const float4*>(p.bias + place(i))) : make_float4(0.f, 0.f, 0.f, 0.f);
+        b[i] = q.x, b[i + 1] = q.y, b[i + 2] = q.z, b[i + 3] = q.w;
+      } else {
+#pragma unroll
+        for (int j = 0; j < 4; ++j) b[i + j] = place(i + j) < p.E ? __ldg(p.bias + place(i + j)) : 0.f;
+      }
+    }
+  }
+
   // ---- logits -> v: what experts are ordered by (values, or logits without a bias) ----
   float v[NV];
   float top = -INFINITY, inv = 1.f;
@@ -378,7 +393,7 @@ __global__ void __launch_bounds__(32 * kRouteWarps, NV <= 16 ? 7 : NV == 32 ? 5 
   if (by_value) {
 #pragma unroll
     for (int i = 0; i < NV; ++i)
-      v[i] = place(i) < p.E ? rank32(score(v[i]) + __ldg(p.bias + place(i))) : -INFINITY;
+      v[i] = place(i) < p.E ? rank32(score(v[i]) + b[BIAS ? i : 0]) : -INFINITY;
   }
 
   // ---- groups: v becomes the values of the kept groups' experts, entry q of
