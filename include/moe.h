@@ -166,7 +166,8 @@ moe_status moe_topk_from_logits(const moe_config* cfg, const float* logits, int 
  * groups of MOE_GROUP_MAX, are ordered by their logits), so it does not hang
  * on how an fp32 sigmoid rounds.  Weights are fp32: within 2^-18 of the
  * formula (typically 2^-23), or within 2^-126.
- * Limits: E <= 2048, K <= 32, n_groups <= 32, K <= topk_groups * E / n_groups. */
+ * Limits: E <= 2048, K <= 32, n_groups <= 32, K <= topk_groups * E / n_groups,
+ * T <= 2^30. */
 enum { MOE_SCORE_SOFTMAX = 0, MOE_SCORE_SIGMOID = 1 };
 enum { MOE_GROUP_MAX = 0, MOE_GROUP_TOP2 = 1 };
 typedef struct {
@@ -213,7 +214,8 @@ moe_status moe_route_topk(const moe_route_config* cfg, int hidden, const void* x
  * or MOE_F32).  Rows are ldx, ldw, ldw_up, ldr, ldo elements apart.  x, w and
  * w_up must start on a 16-byte boundary with row strides that are multiples of
  * 8; residual and out need their element's alignment only (16-byte aligned
- * rows are written faster).  K and N are any positive numbers up to 2^20.
+ * rows are written faster).  K and N are any positive numbers up to 2^20, T at
+ * most 2^30.
  * out may be the residual buffer itself (same address and stride: the result
  * replaces it); otherwise out must not overlap any input.  T == 0 is a no-op.
  * Needs no workspace; results are the same from run to run (sums split over

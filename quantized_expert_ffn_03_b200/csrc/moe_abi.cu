@@ -919,7 +919,7 @@ moe_status moe_selftest_bounded_wait(void* workspace, size_t ws_bytes, uint64_t 
 
 // ---- dense product with its epilogue, and expert choice ------------------------------
 
-constexpr int kLinearMaxFeatures = 1 << 20;
+constexpr int kLinearMaxFeatures = 1 << 20, kLinearMaxTokens = 1 << 30;
 
 static bool is16(int dtype) { return dtype == MOE_BF16 || dtype == MOE_F16; }
 
@@ -934,6 +934,7 @@ moe_status moe_linear_forward(const moe_linear_config* cfg, const moe_linear_wei
     return fail(MOE_ERR_UNSUPPORTED, "dtype must be MOE_BF16 or MOE_F16, out_dtype the same or MOE_F32");
   if (cfg->act < MOE_ACT_NONE || cfg->act > MOE_ACT_RELU || (cfg->gated != 0 && cfg->gated != 1))
     return fail(MOE_ERR_INVALID_ARG, "unknown act %d or gated %d", cfg->act, cfg->gated);
+  if (T > kLinearMaxTokens) return fail(MOE_ERR_UNSUPPORTED, "T must be <= %d", kLinearMaxTokens);
   if (T == 0) return ok();
   if (!wts || !wts->w || (cfg->gated && !wts->w_up) || !x || !out) return fail(MOE_ERR_INVALID_ARG, "NULL pointer");
   if (!aligned(x, 16) || !aligned(wts->w, 16) || (cfg->gated && !aligned(wts->w_up, 16)))
@@ -964,7 +965,7 @@ moe_status moe_linear_forward(const moe_linear_config* cfg, const moe_linear_wei
            (!residual || (aligned(residual, bytes) && (T == 1 || ldr * osz % bytes == 0)));
   };
   p.bias_vec = aligned(wts->bias, 16) && aligned(cfg->gated ? wts->bias_up : nullptr, 16);
-  p.vec = starts_on(16) ? 2 : starts_on(2 * osz) ? 1 : 0;
+  p.vec = starts_on(16);
   p.x = static_cast<const uint16_t*>(x);
   p.w = static_cast<const uint16_t*>(wts->w);
   p.w_up = cfg->gated ? static_cast<const uint16_t*>(wts->w_up) : nullptr;
@@ -1012,6 +1013,7 @@ moe_status moe_route_from_logits(const moe_route_config* cfg, const void* logits
   if (s != MOE_OK) return s;
   if (T < 0) return fail(MOE_ERR_INVALID_ARG, "T < 0");
   if (!is16(dtype) && dtype != MOE_F32) return fail(MOE_ERR_UNSUPPORTED, "logits must be MOE_F32, MOE_BF16 or MOE_F16");
+  if (T > kLinearMaxTokens) return fail(MOE_ERR_UNSUPPORTED, "T must be <= %d", kLinearMaxTokens);
   if (T == 0) return ok();
   if (!logits || !idx || !w) return fail(MOE_ERR_INVALID_ARG, "NULL pointer");
   if (ldl < cfg->n_experts) return fail(MOE_ERR_INVALID_ARG, "row stride of the logits must be >= n_experts");

@@ -351,11 +351,10 @@ constexpr uint32_t kTile = 128u * 128u;  // bytes of a 128-row operand tile of o
 // Bias, activation, gate and residual happen in that order of values; the
 // rounded rows go to a square of the warp's shared memory, 16-byte pieces
 // XOR-ed by the row as the tensor map's swizzle has it, and leave by a TMA
-// store, which also cuts off what lies behind T and N.  That is about 20
-// instructions per 512 outputs where rows written by the lanes took 200
-// (4096 x 256 -> 8192 features: XXX us, was 55).  Rows that do not start on
-// 16-byte boundaries take the square as fp32 and are written by the lanes, a
-// row of 32 features at a time.
+// store, which also cuts off what lies behind T and N (4096 tokens x 256 ->
+// 8192 features: 21 us, of which the bare writing takes 18; with rows written
+// by the lanes from accumulator fragments 55).  Rows that do not start on
+// 16-byte boundaries take the square as fp32 and are written by the lanes.
 constexpr uint32_t kSquare = 4096u;  // bytes per warp: 32 x 32 fp32, or two of 16 bits
 
 // DIRECT: the lanes write their tokens' 64 bytes themselves, which takes more
@@ -375,7 +374,7 @@ struct Epilogue {
 
   // 16-bit residual of the unit at token t0, feature n0, ahead of its use
   __device__ __forceinline__ void fetch(int t0, int n0) {
-    if (!p.res || p.out_f32 || p.vec < 2 || n0 + 32 > p.N || t0 + lane >= p.T) return;
+    if (!p.res || p.out_f32 || !p.vec || n0 + 32 > p.N || t0 + lane >= p.T) return;
     const uint4* src = reinterpret_cast<const uint4*>(static_cast<const uint16_t*>(p.res) + (size_t)(t0 + lane) * p.ldr + n0);
 #pragma unroll
     for (int i = 0; i < 4; ++i) raw[i] = src[i];
@@ -400,15 +399,6 @@ struct Epilogue {
         if (n0 + i < p.N) v[i] += __ldg(bias + n0 + i);
     }
   }
-  __device__ __forceinline__ void put(float y, size_t ro, size_t o) const {
-    if (p.out_f32) {
-      if (p.res) y += static_cast<const float*>(p.res)[ro];
-      static_cast<float*>(p.out)[o] = y;
-    } else {
-      if (p.res) y += from16<F16>(static_cast<const uint16_t*>(p.res)[ro]);
-      static_cast<uint16_t*>(p.out)[o] = to16<F16>(y);
-    }
-  }
   // Byte of 16-byte piece j of row r, rows of 64 or of 128 bytes.
   __device__ __forceinline__ static uint32_t piece64(int r, int j) { return (uint32_t)(64 * r + 16 * (j ^ (r >> 1 & 3))); }
   __device__ __forceinline__ static uint32_t piece128(int r, int j) { return (uint32_t)(128 * r + 16 * (j ^ (r & 7))); }
@@ -422,7 +412,7 @@ struct Epilogue {
 #pragma unroll
       for (int i = 0; i < 32; ++i) v[i] *= u[i];
     }
-    if (p.vec == 2) {
+    if (p.vec) {
       // a piece of the residual behind N is not there to be read in 16 bytes
       const bool whole = n0 + 32 <= p.N, live = t0 + lane < p.T;
       if (!p.out_f32) {
@@ -481,16 +471,78 @@ struct Epilogue {
       }
       return;
     }
-    __syncwarp();
-    to_square(v);
-    __syncwarp();
-    if (n0 + lane < p.N) {
+    if (p.out_f32) {
+      __syncwarp();
+      to_square(v);
+      __syncwarp();
+      if (n0 + lane < p.N) {
 #pragma unroll 4
-      for (int r = 0; r < 32; ++r) {
-        if (t0 + r >= p.T) break;
-        float y;
-        asm volatile("ld.shared.f32 %0, [%1];" : "=f"(y) : "r"(square + piece128(r, lane >> 2) + 4u * (lane & 3)) : "memory");
-        put(y, (size_t)(t0 + r) * p.ldr + n0 + lane, (size_t)(t0 + r) * p.ldo + n0 + lane);
+        for (int r = 0; r < 32; ++r) {
+          if (t0 + r >= p.T) break;
+          float y;
+          asm volatile("ld.shared.f32 %0, [%1];" : "=f"(y) : "r"(square + piece128(r, lane >> 2) + 4u * (lane & 3)) : "memory");
+          if (p.res) y += static_cast<const float*>(p.res)[(size_t)(t0 + r) * p.ldr + n0 + lane];
+          static_cast<float*>(p.out)[(size_t)(t0 + r) * p.ldo + n0 + lane] = y;
+        }
+      }
+      __syncwarp();
+      return;
+    }
+    // 16-bit rows that start anywhere: a token's values are paired as the
+    // 4-byte words of its row in memory fall (from feature 0 or 1), and the
+    // words are written two rows at a time; features left over at the ends
+    // are written alone
+    const uint16_t* res = static_cast<const uint16_t*>(p.res);
+    uint16_t* out = static_cast<uint16_t*>(p.out);
+    if (res) {
+      __syncwarp();
+#pragma unroll 1
+      for (int r = 0; r < 32; r += 16) {
+        uint16_t e[16];
+#pragma unroll
+        for (int i = 0; i < 16; ++i)
+          e[i] = n0 + lane < p.N && t0 + r + i < p.T ? res[(size_t)(t0 + r + i) * p.ldr + n0 + lane] : (uint16_t)0;
+#pragma unroll
+        for (int i = 0; i < 16; ++i)
+          asm volatile("st.shared.u16 [%0], %1;" ::"r"(square + piece64(r + i, lane >> 3) + 2u * (lane & 7)), "h"(e[i])
+                       : "memory");
+      }
+      __syncwarp();
+#pragma unroll
+      for (int j = 0; j < 4; ++j) {
+        const float4 q = lds_f4(square + piece64(lane, j));
+        const uint32_t w[4] = {__float_as_uint(q.x), __float_as_uint(q.y), __float_as_uint(q.z), __float_as_uint(q.w)};
+#pragma unroll
+        for (int k = 0; k < 8; ++k) v[8 * j + k] += from16<F16>((uint16_t)(w[k >> 1] >> (16 * (k & 1))));
+      }
+    }
+    auto odd_row = [&](int t) { return (int)((reinterpret_cast<uintptr_t>(out + (size_t)t * p.ldo + n0) >> 1) & 1); };
+    const int odd = odd_row(t0 + lane), left = min(32, p.N - n0);
+    uint32_t w[16];
+#pragma unroll
+    for (int j = 0; j < 16; ++j)
+      w[j] = pack16<F16>(odd ? v[2 * j + 1] : v[2 * j], odd ? v[j < 15 ? 2 * j + 2 : 31] : v[2 * j + 1]);
+    __syncwarp();
+#pragma unroll
+    for (int j = 0; j < 4; ++j) sts_v4(square + piece64(lane, j), w[4 * j], w[4 * j + 1], w[4 * j + 2], w[4 * j + 3]);
+    __syncwarp();
+    const int j = lane & 15;
+#pragma unroll 4
+    for (int r = lane >> 4; r < 32; r += 2) {
+      const int o = odd_row(t0 + r);
+      uint32_t x;
+      asm volatile("ld.shared.b32 %0, [%1];" : "=r"(x) : "r"(square + piece64(r, j >> 2) + 4u * (j & 3)) : "memory");
+      if (t0 + r < p.T && 2 * j + o + 1 < left)
+        *reinterpret_cast<uint32_t*>(out + (size_t)(t0 + r) * p.ldo + n0 + 2 * j + o) = x;
+    }
+    if (t0 + lane < p.T) {
+      uint16_t* row = out + (size_t)(t0 + lane) * p.ldo + n0;
+      if (odd) row[0] = to16<F16>(v[0]);
+      const int last = (left - odd) >> 1;  // a word with one feature, if any
+      if ((left - odd) & 1) {
+        uint16_t x;
+        asm volatile("ld.shared.u16 %0, [%1];" : "=h"(x) : "r"(square + piece64(lane, last >> 2) + 4u * (last & 3)) : "memory");
+        row[left - 1] = x;
       }
     }
     __syncwarp();
@@ -995,7 +1047,7 @@ bool make_maps(const LinearParams& p, int rows, int BT, Maps* m) {
   if (!make_map(&m->w, F16, p.w, p.K, p.N, p.ldw, rows) || !make_map(&m->x, F16, p.x, p.K, p.T, p.ldx, BT)) return false;
   m->u = m->out = m->w;  // (unused ones are valid all the same)
   return (!GATED || make_map(&m->u, F16, p.w_up, p.K, p.N, p.ldw_up, rows)) &&
-         (p.vec != 2 || make_out_map(&m->out, F16, p));
+         (!p.vec || make_out_map(&m->out, F16, p));
 }
 
 template <auto Kernel, class... Args>

@@ -12,7 +12,7 @@ struct LinearParams {
   int T, K, N;
   int act;       // MOE_ACT_*
   int out_f32;   // output (and residual) fp32, else the 16-bit input type
-  int vec;       // rows of out (and residual) start on 2: 16-byte boundaries, 1: boundaries of two elements
+  int vec;       // every row of out (and residual) starts on a 16-byte boundary
   int bias_vec;  // the biases start on 16-byte boundaries
   const uint16_t* x;
   const uint16_t* w;

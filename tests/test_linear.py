@@ -176,6 +176,36 @@ def test_tokens_do_not_depend_on_each_other_and_runs_repeat(T):
 
 
 @pytest.mark.gpu
+@pytest.mark.parametrize("T,N", [(20, 63), (300, 1001), (513, 510), (40, 33)])
+@pytest.mark.parametrize("off", [0, 1])
+def test_rows_that_start_anywhere(T, N, off):
+    """Odd row lengths, a first row that starts between two 4-byte boundaries, a residual laid out otherwise."""
+    import torch
+    d = make(T, 200, N, act="relu", bias=True, res=True, seed=8)
+    buf = torch.full((T * N + 8,), SENTINEL, dtype=torch.bfloat16, device="cuda")
+    view = buf[off:off + T * N].view(T, N)
+    wide = torch.zeros(T, N + 3, dtype=torch.bfloat16, device="cuda")
+    wide[:, 1:N + 1] = d["res"]
+    M.moe_linear_forward(d["cfg"], d["wts"], d["x"], view, residual=wide[:, 1:N + 1])
+    check(view, *d["ref"])
+    assert (buf[:off] == SENTINEL).all() and (buf[off + T * N:] == SENTINEL).all()
+
+
+@pytest.mark.gpu
+@pytest.mark.parametrize("T", [3, 20, 300])
+def test_offsets_beyond_32_bits(T):
+    """Rows of x, residual and out that lie more than 2^32 bytes apart in all."""
+    import torch
+    d = make(T, 128, 96, res=True, seed=9)
+    ld = ((5 << 30) // 2 // (T - 1) + 7) // 8 * 8  # elements of 2 bytes: 5 GB from the first row to the last
+    far = lambda a: torch.empty((T - 1) * ld + a.shape[1], dtype=a.dtype, device="cuda").as_strided(  # noqa: E731
+        a.shape, (ld, 1)).copy_(a)
+    x, res = far(d["x"]), far(d["res"])
+    M.moe_linear_forward(d["cfg"], d["wts"], x, res, residual=res)
+    check(res, *d["ref"])
+
+
+@pytest.mark.gpu
 def test_zero_tokens_writes_nothing():
     import torch
     cfg = M.linear_config(64, 32)
@@ -268,7 +298,7 @@ def test_refusals_on_the_host():
                dict(res=4096, ldr=40), dict(res=4099, ldr=32), dict(bias=18), dict(out=1024)]:
         assert call(good, **kw) == 1, kw
         assert M.last_error()
-    assert call(good, ldx=1 << 40) == 2
+    assert call(good, ldx=1 << 40) == 2 and call(good, T=(1 << 30) + 1) == 2
     gated = M.linear_config(64, 32, gated=True)
     assert call(gated, w_up=24, ldw_up=64) == 1 and call(gated, w_up=32, ldw_up=60) == 1
     assert lib.moe_linear_forward(None, None, None, 0, None, 0, 0, None, 0, None) == 1

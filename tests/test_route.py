@@ -176,6 +176,14 @@ def test_masked_and_non_finite_rows(score, renorm, groups, keep):
 
 
 @pytest.mark.gpu
+def test_offsets_beyond_32_bits():
+    import torch
+    T, ld = 40, 1 << 25
+    l = torch.empty((T - 1) * ld + 64, device="cuda").as_strided((T, 64), (ld, 1)).copy_(draw(T, 64, 17))
+    check(l, 5, bias_of(64, 17), score="sigmoid")
+
+
+@pytest.mark.gpu
 def test_graph_replay_and_other_stream():
     import torch
     l = draw(40, 256, 11)
@@ -276,7 +284,7 @@ def test_refusals_on_the_host():
     for kw in [dict(T=-1), dict(logits=None), dict(idx=None), dict(w=None), dict(ldl=63), dict(logits=18),
                dict(bias=2), dict(idx=33), dict(w=50)]:
         assert call(good, **kw) == 1, kw
-    assert call(good, dtype=7) == 2
+    assert call(good, dtype=7) == 2 and call(good, T=(1 << 30) + 1) == 2
     assert M.moe_route_workspace_bytes(good, 3) == 768
 
     def topk(cfg, hidden=64, x=1024, wr=2048, T=2, idx=32, w=48, lo=None, ws=4096, nb=1 << 20):
