@@ -2,15 +2,15 @@
 //   y[t][n] = act(x[t] . w[n] + bias[n]) [* (x[t] . w_up[n] + bias_up[n])] [+ res[t][n]]
 // fp32 accumulation and epilogue, one rounding to the output type.
 //
-// Three kernels, one per regime of T (choose_* below):
-//   rows   few tokens: the weights stream once through registers into
+// Three kernels, by how many tokens there are (launch_any, best_way):
+//   rows   up to 16: the weights stream once through shared memory into
 //          m16n8k16 steps (HBM bound);
-//   split  up to a few hundred tokens: 128 features x all tokens per cluster,
-//          TMA -> tcgen05, K split over the cluster's CTAs and joined through
-//          distributed shared memory (HBM / L2 bound);
-//   pair   many tokens: persistent pairs of CTAs, 256-token tiles, tcgen05
-//          with both CTAs' operands, epilogue under the next tile's MMAs
-//          (tensor bound).
+//   tile   some hundreds: tiles of up to 128 tokens x 32 to 128 features,
+//          TMA -> tcgen05, K split over a cluster whose CTAs join their sums
+//          through distributed shared memory (HBM and L2 bound);
+//   pair   more: persistent pairs of CTAs, 256 tokens x 128 or 256 columns,
+//          tcgen05 on both CTAs' operands, each tile's epilogue under the next
+//          one's MMAs (tensor bound).
 #include <cuda.h>
 #include <cuda_bf16.h>
 #include <cuda_fp16.h>
@@ -109,47 +109,6 @@ __device__ __forceinline__ void finish_one(const LinearParams& p, int t, int n, 
   }
 }
 
-// W (4 or 8) adjacent values of a row of out or residual, on a boundary of
-// their size.
-template <bool F16, int W>
-__device__ __forceinline__ void load_row(const LinearParams& p, const void* base, size_t at, float (&v)[W]) {
-  if (p.out_f32) {
-#pragma unroll
-    for (int i = 0; i < W; i += 4) {
-      const float4 e = *reinterpret_cast<const float4*>(static_cast<const float*>(base) + at + i);
-      v[i] = e.x, v[i + 1] = e.y, v[i + 2] = e.z, v[i + 3] = e.w;
-    }
-  } else {
-    uint32_t w[W / 2];
-    const uint16_t* src = static_cast<const uint16_t*>(base) + at;
-    if constexpr (W == 8) {
-      const uint4 e = *reinterpret_cast<const uint4*>(src);
-      w[0] = e.x, w[1] = e.y, w[2] = e.z, w[3] = e.w;
-    } else {
-      const uint2 e = *reinterpret_cast<const uint2*>(src);
-      w[0] = e.x, w[1] = e.y;
-    }
-#pragma unroll
-    for (int i = 0; i < W; ++i) v[i] = from16<F16>((uint16_t)(w[i >> 1] >> (16 * (i & 1))));
-  }
-}
-template <bool F16, int W>
-__device__ __forceinline__ void store_row(const LinearParams& p, size_t at, const float (&v)[W]) {
-  if (p.out_f32) {
-#pragma unroll
-    for (int i = 0; i < W; i += 4)
-      *reinterpret_cast<float4*>(static_cast<float*>(p.out) + at + i) = make_float4(v[i], v[i + 1], v[i + 2], v[i + 3]);
-  } else {
-    uint32_t w[W / 2];
-#pragma unroll
-    for (int i = 0; i < W / 2; ++i) w[i] = pack16<F16>(v[2 * i], v[2 * i + 1]);
-    uint16_t* dst = static_cast<uint16_t*>(p.out) + at;
-    if constexpr (W == 8)
-      *reinterpret_cast<uint4*>(dst) = make_uint4(w[0], w[1], w[2], w[3]);
-    else
-      *reinterpret_cast<uint2*>(dst) = make_uint2(w[0], w[1]);
-  }
-}
 // ---- few tokens: weights streamed once through registers ------------------------------
 
 template <bool F16>
@@ -354,7 +313,7 @@ constexpr uint32_t kTile = 128u * 128u;  // bytes of a 128-row operand tile of o
 // store, which also cuts off what lies behind T and N (4096 tokens x 256 ->
 // 8192 features: 21 us, of which the bare writing takes 18; with rows written
 // by the lanes from accumulator fragments 55).  Rows that do not start on
-// 16-byte boundaries take the square as fp32 and are written by the lanes.
+// 16-byte boundaries are written by the lanes, from the square in row order.
 constexpr uint32_t kSquare = 4096u;  // bytes per warp: 32 x 32 fp32, or two of 16 bits
 
 // DIRECT: the lanes write their tokens' 64 bytes themselves, which takes more

@@ -475,7 +475,7 @@ __global__ void __launch_bounds__(32 * kRouteWarps, NV <= 16 ? 7 : NV == 32 ? 5 
 #pragma unroll
   for (int i = 0; i < NV; ++i) best = fmaxf(best, v[i]);
   float bound = warp_kth(best, p.K);
-  if (by_value) bound -= 2.f * eps + 0x1p-22f * fabsf(bound);
+  if (by_value && fabsf(bound) != INFINITY) bound -= 2.f * eps + 0x1p-22f * fabsf(bound);
   using Mask = typename MaskOf<(NV > 32)>::type;
   Mask mask = 0;
 #pragma unroll

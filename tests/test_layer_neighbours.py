@@ -140,3 +140,59 @@ def test_a_block_around_the_layer(T):
                                         w_in=w.cpu().numpy().astype(np.float64))
     assert_outputs_close(from_dev_bits(ho), h_ref, "h_out")
     assert_outputs_close(from_dev_bits(yo), y_ref, "y_norm")
+
+
+@pytest.mark.gpu
+@pytest.mark.parametrize("T", [1, 12, 60, 700])
+@pytest.mark.parametrize("graph", [False, True])
+def test_dependent_calls_back_to_back(T, graph):
+    """Kernels that start before the one ahead has ended wait for its results: a chain of products, choices and
+    torch operations, each reading what the one before wrote, gives the same bits with and without waits between."""
+    import torch
+    g = torch.Generator(device="cuda").manual_seed(T)
+    H, E = 1024, 64
+    w = [(torch.randn(H, H, generator=g, device="cuda") * 0.03).bfloat16() for _ in range(3)]
+    cfg = M.linear_config(H, H, act=M.MOE_ACT_SILU, gated=True)
+    wts = [M.linear_weights(cfg, w[i], w_up=w[(i + 1) % 3]) for i in range(3)]
+    wr = (torch.randn(E, H, generator=g, device="cuda") * 0.05).bfloat16()
+    rc = M.route_config(E, 4, M.MOE_SCORE_SIGMOID, 8, 3, M.MOE_GROUP_TOP2)
+    x0 = torch.randn(T, H, generator=g, device="cuda").bfloat16()
+    sb = torch.zeros(E, device="cuda")
+    bufs = [torch.empty_like(x0) for _ in range(2)]
+    idx, wt = torch.empty(T, 4, dtype=torch.int32, device="cuda"), torch.empty(T, 4, device="cuda")
+    logits = torch.empty(T, E, device="cuda")
+    seen = torch.zeros(24, T, 4, dtype=torch.int32, device="cuda")
+
+    def chain(wait):
+        bufs[0].copy_(x0)
+        for i in range(24):
+            a, b = bufs[i % 2], bufs[(i + 1) % 2]
+            M.moe_linear_forward(cfg, wts[i % 3], a, b, residual=a)
+            wait()
+            if i % 4 == 1:
+                b.mul_(0.5)
+                wait()
+            M.moe_route_topk(rc, b, wr, idx, wt, select_bias=sb, logits_out=logits)
+            wait()
+            if i % 3 == 0:
+                sb.copy_(wt[0].sum() * logits[-1] * 0.01)
+                wait()
+            seen[i].copy_(idx)
+        return bufs[0].clone(), seen.clone(), wt.clone()
+
+    sb.zero_()
+    want = chain(torch.cuda.synchronize)
+    for _ in range(5):
+        sb.zero_()
+        if graph:
+            torch.cuda.synchronize()
+            gr = torch.cuda.CUDAGraph()
+            with torch.cuda.graph(gr):
+                got = chain(lambda: None)
+            sb.zero_()
+            gr.replay()
+        else:
+            got = chain(lambda: None)
+        torch.cuda.synchronize()
+        assert all(torch.equal(a, b) for a, b in zip(want, got))
+    assert M.moe_linear_device_error() == (M.MOE_OK, 0)

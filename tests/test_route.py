@@ -170,9 +170,14 @@ def test_masked_and_non_finite_rows(score, renorm, groups, keep):
     off[10:44] = -np.inf
     nan = np.zeros(48, np.float32)
     nan[2] = np.nan
-    for bias in (None, bias_of(48, 3), off, nan, np.full(48, -np.inf, np.float32)):
+    always = bias_of(48, 4)
+    always[[3, 20, 41]] = np.inf  # experts that every token takes
+    huge = (1e30 * np.arange(48)).astype(np.float32)
+    for bias in (None, bias_of(48, 3), off, nan, np.full(48, -np.inf, np.float32), always, huge,
+                 np.full(48, np.inf, np.float32)):
         for gs in ("max", "top2"):
-            check(l, 5, bias, score=score, renorm=renorm, groups=groups, keep=keep, group_score=gs, scale=1.5)
+            for K in (1, 5):
+                check(l, K, bias, score=score, renorm=renorm, groups=groups, keep=keep, group_score=gs, scale=1.5)
 
 
 @pytest.mark.gpu
