@@ -545,7 +545,9 @@ static __device__ __noinline__ bool mbar_wait(uint64_t* bar, uint32_t parity, ui
 // A kernel launched with programmatic stream serialisation may start while the
 // one before it in the stream still runs: prior_wait returns when that one has
 // ended and its writes are visible (at once in a kernel launched otherwise), so
-// it comes before any access to global memory; next_may_start lets the kernel
+// it comes before any access to global memory.  Behind it no __ldg: another
+// block of the SM may have left a line of the read-only path there that the
+// kernel ahead has overwritten since.  next_may_start lets the kernel
 // behind start its own blocks as this one's leave room.
 __device__ __forceinline__ void next_may_start() { asm volatile("griddepcontrol.launch_dependents;" ::: "memory"); }
 __device__ __forceinline__ void prior_wait() { asm volatile("griddepcontrol.wait;" ::: "memory"); }

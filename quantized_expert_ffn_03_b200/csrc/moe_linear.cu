@@ -94,11 +94,11 @@ __device__ __forceinline__ uint32_t pack16(float a, float b) {
 // residual is read before the store, so out may be the residual buffer.
 template <bool F16>
 __device__ __forceinline__ void finish_one(const LinearParams& p, int t, int n, float g, float u) {
-  if (p.bias) g += __ldg(p.bias + n);
+  if (p.bias) g += p.bias[n];
   float a[1] = {g};
   activate(a, p.act);
   float y = a[0];
-  if (p.w_up) y *= p.bias_up ? u + __ldg(p.bias_up + n) : u;
+  if (p.w_up) y *= p.bias_up ? u + p.bias_up[n] : u;
   const size_t o = (size_t)t * p.ldo + n;
   if (p.out_f32) {
     if (p.res) y += static_cast<const float*>(p.res)[(size_t)t * p.ldr + n];
@@ -151,11 +151,11 @@ __device__ __forceinline__ void row_copy16(uint32_t dst, const uint16_t* row, in
 }
 __device__ __forceinline__ uint4 row_load16(const uint16_t* row, int k, int K, bool live) {
   if (!live || k >= K) return make_uint4(0u, 0u, 0u, 0u);
-  if (k + 8 <= K) return __ldg(reinterpret_cast<const uint4*>(row + k));
+  if (k + 8 <= K) return *reinterpret_cast<const uint4*>(row + k);
   uint32_t h[4] = {0u, 0u, 0u, 0u};
 #pragma unroll
   for (int i = 0; i < 7; ++i)
-    if (k + i < K) h[i >> 1] |= (uint32_t)__ldg(row + k + i) << (16 * (i & 1));
+    if (k + i < K) h[i >> 1] |= (uint32_t)row[k + i] << (16 * (i & 1));
   return make_uint4(h[0], h[1], h[2], h[3]);
 }
 
@@ -341,7 +341,7 @@ struct Epilogue {
   // brings the unit's biases into the L1 cache
   __device__ __forceinline__ void touch_bias(int n0) const {
     if (p.bias && n0 + lane < p.N) {
-      const float a = __ldg(p.bias + n0 + lane), b = GATED && p.bias_up ? __ldg(p.bias_up + n0 + lane) : 0.f;
+      const float a = p.bias[n0 + lane], b = GATED && p.bias_up ? p.bias_up[n0 + lane] : 0.f;
       asm volatile("" ::"f"(a), "f"(b));
     }
   }
@@ -349,13 +349,13 @@ struct Epilogue {
     if (p.bias_vec && n0 + 32 <= p.N) {
 #pragma unroll
       for (int i = 0; i < 8; ++i) {
-        const float4 b = __ldg(reinterpret_cast<const float4*>(bias + n0) + i);
+        const float4 b = reinterpret_cast<const float4*>(bias + n0)[i];
         v[4 * i] += b.x, v[4 * i + 1] += b.y, v[4 * i + 2] += b.z, v[4 * i + 3] += b.w;
       }
     } else {
 #pragma unroll
       for (int i = 0; i < 32; ++i)
-        if (n0 + i < p.N) v[i] += __ldg(bias + n0 + i);
+        if (n0 + i < p.N) v[i] += bias[n0 + i];
     }
   }
   // Byte of 16-byte piece j of row r, rows of 64 or of 128 bytes.

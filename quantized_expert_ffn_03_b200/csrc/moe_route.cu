@@ -15,7 +15,7 @@ namespace {
 constexpr int kRouteWarps = 4;
 constexpr unsigned kAll = 0xffffffffu;
 
-__device__ __forceinline__ float load_logit(const float* p) { return __ldg(p); }
+__device__ __forceinline__ float load_logit(const float* p) { return *p; }
 __device__ __forceinline__ float load_logit(const __nv_bfloat16* p) { return __bfloat162float(*p); }
 __device__ __forceinline__ float load_logit(const __half* p) { return __half2float(*p); }
 
@@ -80,7 +80,7 @@ __device__ __forceinline__ Scorer64 scorer64(const RouteParams& p, const T* row,
 }
 template <typename T>
 __device__ __forceinline__ double value64(const RouteParams& p, const Scorer64& score, const T* row, int e) {
-  return rank64(score(logit_of(row, e)) + (p.bias ? (double)__ldg(p.bias + e) : 0.0));
+  return rank64(score(logit_of(row, e)) + (p.bias ? (double)p.bias[e] : 0.0));
 }
 
 // The rank of this lane's candidate, expert e (the first `count` lanes have one).
@@ -308,7 +308,7 @@ template <typename T>
 struct Wide {
   static constexpr int W = 16 / sizeof(T);
   static __device__ __forceinline__ void load(const T* p, float (&v)[W]) {
-    const uint4 u = __ldg(reinterpret_cast<const uint4*>(p));
+    const uint4 u = *reinterpret_cast<const uint4*>(p);
     const T* h = reinterpret_cast<const T*>(&u);
 #pragma unroll
     for (int i = 0; i < W; ++i) v[i] = to_float(h[i]);
@@ -347,11 +347,11 @@ __global__ void __launch_bounds__(32 * kRouteWarps, NV <= 16 ? 7 : NV == 32 ? 5 
 #pragma unroll
     for (int i = 0; i < NV; i += 4) {
       if (p.vec && p.bias_vec) {
-        const float4 q = place(i) < p.E ? __ldg(reinterpret_cast<const float4*>(p.bias + place(i))) : make_float4(0.f, 0.f, 0.f, 0.f);
+        const float4 q = place(i) < p.E ? *reinterpret_cast<const float4*>(p.bias + place(i)) : make_float4(0.f, 0.f, 0.f, 0.f);
         b[i] = q.x, b[i + 1] = q.y, b[i + 2] = q.z, b[i + 3] = q.w;
       } else {
 #pragma unroll
-        for (int j = 0; j < 4; ++j) b[i + j] = place(i + j) < p.E ? __ldg(p.bias + place(i + j)) : 0.f;
+        for (int j = 0; j < 4; ++j) b[i + j] = place(i + j) < p.E ? p.bias[place(i + j)] : 0.f;
       }
     }
   }
@@ -502,7 +502,7 @@ __global__ void __launch_bounds__(32 * kRouteWarps, NV <= 16 ? 7 : NV == 32 ? 5 
     if (grouped) e = expert(e);
     // its value again, by the same operations
     const float l = fminf(rank32(load_logit(row + e)), FLT_MAX);
-    const float x = by_value ? rank32(score(l) + __ldg(p.bias + e)) : l;
+    const float x = by_value ? rank32(score(l) + p.bias[e]) : l;
     const uint64_t mine64 = live ? (uint64_t)order32(x) << 32 | (uint32_t)~e : 0ull;
     ckey[lane] = mine64;
     __syncwarp();

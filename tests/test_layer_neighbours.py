@@ -151,7 +151,7 @@ def test_dependent_calls_back_to_back(T, graph):
     import torch
     g = torch.Generator(device="cuda").manual_seed(T)
     H, E = 1024, 64
-    w = [(torch.randn(H, H, generator=g, device="cuda") * 0.03).bfloat16() for _ in range(3)]
+    w = [(torch.randn(H, H, generator=g, device="cuda") * 0.01).bfloat16() for _ in range(3)]
     cfg = M.linear_config(H, H, act=M.MOE_ACT_SILU, gated=True)
     wts = [M.linear_weights(cfg, w[i], w_up=w[(i + 1) % 3]) for i in range(3)]
     wr = (torch.randn(E, H, generator=g, device="cuda") * 0.05).bfloat16()
@@ -170,7 +170,7 @@ def test_dependent_calls_back_to_back(T, graph):
             M.moe_linear_forward(cfg, wts[i % 3], a, b, residual=a)
             wait()
             if i % 4 == 1:
-                b.mul_(0.5)
+                b.div_(b.float().abs().amax() + 0.25)  # keeps the stream's size
                 wait()
             M.moe_route_topk(rc, b, wr, idx, wt, select_bias=sb, logits_out=logits)
             wait()
@@ -182,6 +182,7 @@ def test_dependent_calls_back_to_back(T, graph):
 
     sb.zero_()
     want = chain(torch.cuda.synchronize)
+    assert all(torch.isfinite(a.float()).all() for a in want)
     for _ in range(5):
         sb.zero_()
         if graph:
