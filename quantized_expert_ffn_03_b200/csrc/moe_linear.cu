@@ -625,7 +625,7 @@ __global__ void __launch_bounds__(kTileThreads, 1)
     prior_wait();
   }
   tc::fence_after_sync();
-  tc::cluster_arrive();  // (1) this CTA runs: its shared memory may be written
+  if (S > 1) tc::cluster_arrive_relaxed();  // (1) this CTA runs: its shared memory may be written
   const uint32_t tmem = tmem_slot;
 
   // units of this warp: the tokens of its TMEM quarter, every other group of features
@@ -660,7 +660,7 @@ __global__ void __launch_bounds__(kTileThreads, 1)
     }
     if (!ok) let_issued_work_end();
     __syncwarp();
-    tc::cluster_wait();  // (1)
+    if (S > 1) tc::cluster_wait();  // (1)
   } else if (warp == kTileEpi + 1) {
     constexpr uint32_t idesc = tc::idesc_f16(128, CN, !F16);
     bool ok = true;
@@ -685,9 +685,9 @@ __global__ void __launch_bounds__(kTileThreads, 1)
     else if (lead)
       tc::commit(accfull);
     __syncwarp();
-    tc::cluster_wait();  // (1)
+    if (S > 1) tc::cluster_wait();  // (1)
   } else {
-    tc::cluster_wait();  // (1)
+    if (S > 1) tc::cluster_wait();  // (1)
     // this warp's first unit: its residual and biases come while the MMAs run
     each_unit([&](int grp, uint32_t unit) {
       if (mine >= 0 || unit % S != rank) return;
@@ -716,8 +716,10 @@ __global__ void __launch_bounds__(kTileThreads, 1)
       });
   }
   __syncwarp();
-  tc::cluster_arrive();  // (2) partial sums are where they belong
-  tc::cluster_wait();
+  if (S > 1) {
+    tc::cluster_arrive();  // (2) partial sums are where they belong
+    tc::cluster_wait();
+  }
   if (warp < kTileEpi) {
     each_unit([&](int grp, uint32_t unit) {
       if (unit % S != rank) return;
