@@ -1059,8 +1059,13 @@ cudaError_t launch_rows(const LinearParams& p, int sms, cudaStream_t st) {
 
 // How long each way of doing a product takes, in ns, from measurements of the
 // parts (steps of 64 columns of K): what a launch and a tile cost besides their
-// steps, a step by what its copies move per SM (about 110 bytes per ns) or by
-// its MMAs, an epilogue unit.
+// steps, a step by what its copies move per SM (about 115 bytes per ns) or by
+// its MMAs, an epilogue unit.  Against every way tried on 50 sizes (20 to 8192
+// tokens, K 64 to 8192, N 512 to 16384) the way it picks is the fastest or
+// mostly within 4 percent of it, at the worst 14; no one way is near the fastest
+// everywhere (64 x 4096 x 4096: 9.8 us by clusters of 4 against 12.5 unsplit;
+// 1024 x 4096 x 4096: 26 us by pairs of 256 columns against 36 by tiles;
+// 2048 x 1024 x 1024 gated: 9.7 us by pairs of 128 columns, 10.8 by 256).
 struct Way {
   int pair, width, S;  // pair: TN; tile: FN, CTAs of a cluster
   float ns;
@@ -1075,9 +1080,10 @@ Way best_way(int T, int K, int N, bool gated, int sms) {
     if (tiles > 8 * sms) continue;
     for (int S = 1; S <= kMaxSplit && S <= KB; S *= 2) {
       const int64_t waves = (tiles * S + (S == 4 ? 127 : sms - 1)) / (S == 4 ? 128 : sms);
-      const float step = max_f(170.f, (float)(BT + na * FN) * 128.f / 110.f);
+      const float step = max_f(170.f, (float)(BT + na * FN) * 128.f / 115.f);
       const int units = (FN / 32 + 1) / 2;  // of a warp
-      const float tail = S == 1 ? 500.f * units : 1100.f + 300.f * (S - 1) + 500.f * ((units + S - 1) / S);
+      const float tail = S == 1 ? 500.f * units
+                                : (S == 4 && BT == 128 ? 2000.f : 1100.f) + 300.f * (S - 1) + 500.f * ((units + S - 1) / S);
       const float ns = (float)waves * (2500.f + (float)((KB + S - 1) / S) * step + na * tail);
       if (ns < best.ns) best = {0, FN, S, ns};
     }
@@ -1086,7 +1092,7 @@ Way best_way(int T, int K, int N, bool gated, int sms) {
     const int FN = TN / na;
     const int64_t tiles = (int64_t)((T + 255) / 256) * ((N + FN - 1) / FN);
     const int64_t waves = (tiles + sms / 2 - 1) / (sms / 2);
-    const float steps = (float)KB * (TN == 256 ? 300.f : 205.f), epilogue = (TN == 256 ? 450.f : 500.f) * FN / 64 * na;
+    const float steps = (float)KB * (TN == 256 ? 310.f : 195.f), epilogue = (TN == 256 ? 450.f : 520.f) * FN / 64 * na;
     const float ns = 3300.f + (float)waves * max_f(steps, epilogue) + epilogue;
     if (ns < best.ns) best = {TN, 0, 1, ns};
   }
