@@ -30,6 +30,13 @@ namespace {
 constexpr unsigned kAll = 0xffffffffu;
 constexpr int kKB = 64;  // columns of K per step: 128 bytes, one swizzle row
 
+// The tensor cores cut what an addition shifts out of the accumulator's 24
+// bits, always towards zero, which over K columns makes a sum too small by
+// about K 10^-9 of its size (measured 9 10^-6 at 16384).  fp32 outputs show
+// that, so for them an accumulator holds kPart steps (512 columns), and the
+// parts are added up in fp32, rounding to nearest: 5 10^-7 at every K.
+constexpr int kPart = 512 / kKB;
+
 // ---- epilogue arithmetic ------------------------------------------------------------
 
 // The activation in fp32, one switch for N values (a switch for each value
@@ -209,38 +216,55 @@ __global__ void __launch_bounds__(32 * W, 32 / W) linear_rows_kernel(const Linea
     }
   };
   if (TM == 8) load_x(0);
+  // parts of kPart units, added up in red (one part up to 4096 columns and 8
+  // warps: the loops are nested since a condition in the inner one costs 0.1
+  // to 0.5 us a call)
 #pragma unroll 1
-  for (int i = 0; i < mine; ++i) {
-    if (TM != 8) load_x(i);
-    uint4 xv[NX][2];
+  for (int i = 0;;) {
+    const int i0 = i, i1 = min(mine, i + kPart);
+#pragma unroll 1
+    for (; i < i1; ++i) {
+      if (TM != 8) load_x(i);
+      uint4 xv[NX][2];
 #pragma unroll
-    for (int j = 0; j < NX; ++j) xv[j][0] = next[j][0], xv[j][1] = next[j][1];
-    if (TM == 8) load_x(i + 1);
-    asm volatile("cp.async.wait_group %0;" ::"n"(kDepth - 2) : "memory");
-    const uint32_t src = ring + (uint32_t)(i % kDepth * NA) * kRowsUnit;
-    uint4 wv[NA][2];
+      for (int j = 0; j < NX; ++j) xv[j][0] = next[j][0], xv[j][1] = next[j][1];
+      if (TM == 8) load_x(i + 1);
+      asm volatile("cp.async.wait_group %0;" ::"n"(kDepth - 2) : "memory");
+      const uint32_t src = ring + (uint32_t)(i % kDepth * NA) * kRowsUnit;
+      uint4 wv[NA][2];
 #pragma unroll
-    for (int a = 0; a < NA; ++a)
+      for (int a = 0; a < NA; ++a)
 #pragma unroll
-      for (int h = 0; h < 2; ++h)
-        asm volatile("ld.shared.v4.u32 {%0,%1,%2,%3}, [%4];"
-                     : "=r"(wv[a][h].x), "=r"(wv[a][h].y), "=r"(wv[a][h].z), "=r"(wv[a][h].w)
-                     : "r"(src + (uint32_t)a * kRowsUnit + 512u * (uint32_t)h)
-                     : "memory");
-    fetch(i + kDepth - 1);  // into the slot that the last turn read
+        for (int h = 0; h < 2; ++h)
+          asm volatile("ld.shared.v4.u32 {%0,%1,%2,%3}, [%4];"
+                       : "=r"(wv[a][h].x), "=r"(wv[a][h].y), "=r"(wv[a][h].z), "=r"(wv[a][h].w)
+                       : "r"(src + (uint32_t)a * kRowsUnit + 512u * (uint32_t)h)
+                       : "memory");
+      fetch(i + kDepth - 1);  // into the slot that the last turn read
 #pragma unroll
-    for (int a = 0; a < NA; ++a)
+      for (int a = 0; a < NA; ++a)
 #pragma unroll
-      for (int h = 0; h < 2; ++h) {
-        const uint4 lo = xv[0][h], hi = NX > 1 ? xv[NX - 1][h] : make_uint4(0u, 0u, 0u, 0u);
-        mma16816<F16>(acc[a], lo.x, hi.x, lo.y, hi.y, wv[a][h].x, wv[a][h].y);
-        mma16816<F16>(acc[a], lo.z, hi.z, lo.w, hi.w, wv[a][h].z, wv[a][h].w);
+        for (int h = 0; h < 2; ++h) {
+          const uint4 lo = xv[0][h], hi = NX > 1 ? xv[NX - 1][h] : make_uint4(0u, 0u, 0u, 0u);
+          mma16816<F16>(acc[a], lo.x, hi.x, lo.y, hi.y, wv[a][h].x, wv[a][h].y);
+          mma16816<F16>(acc[a], lo.z, hi.z, lo.w, hi.w, wv[a][h].z, wv[a][h].w);
+        }
+    }
+#pragma unroll
+    for (int a = 0; a < NA; ++a) {
+#pragma unroll
+      for (int q = 0; q < 2 * NX; ++q) {
+        float& r = red[warp][a][g + 8 * (q >> 1)][2 * t + (q & 1)];
+        if (i0)
+          r += acc[a][q];
+        else
+          r = acc[a][q];
       }
+#pragma unroll
+      for (int q = 0; q < 4; ++q) acc[a][q] = 0.f;
+    }
+    if (i >= mine) break;
   }
-#pragma unroll
-  for (int a = 0; a < NA; ++a)
-#pragma unroll
-    for (int q = 0; q < 2 * NX; ++q) red[warp][a][g + 8 * (q >> 1)][2 * t + (q & 1)] = acc[a][q];
   __syncthreads();
   const int f = threadIdx.x % kRowsFeat, c = threadIdx.x / kRowsFeat;
   if (c < TM && c < p.T && n0 + f < p.N) {
@@ -289,6 +313,9 @@ __device__ __noinline__ void let_issued_work_end() {
 }
 __device__ __forceinline__ void bar_init(uint32_t a, uint32_t n) {
   asm volatile("mbarrier.init.shared::cta.b64 [%0], %1;" ::"r"(a), "r"(n) : "memory");
+}
+__device__ __forceinline__ void bar_arrive(uint32_t a) {
+  asm volatile("mbarrier.arrive.shared::cta.b64 _, [%0];" ::"r"(a) : "memory");
 }
 __device__ __forceinline__ void bar_expect(uint32_t a, uint32_t bytes) {
   asm volatile("mbarrier.arrive.expect_tx.shared::cta.b64 _, [%0], %1;" ::"r"(a), "r"(bytes) : "memory");
@@ -540,6 +567,10 @@ __device__ __forceinline__ void load_unit(uint32_t taddr, float (&v)[32]) {
 // no workspace, and calls on several streams share nothing.
 // With T < 128 only BT rows of x are loaded; the MMA reads whatever lies behind
 // them as its other rows, whose results nobody reads.
+//
+// SUMS (fp32 outputs of more than kPart steps): the parts go to two
+// accumulators in turn, and the epilogue warps add them up in registers while
+// the MMAs go on (64 x 4096 x 4096: 11.5 us, 9.8 without).
 constexpr int kTileEpi = 8;                         // warps that read TMEM
 constexpr int kTileThreads = 32 * (kTileEpi + 2);   // + a loading and an MMA warp
 constexpr int kTileStages = 12;                     // at most
@@ -566,18 +597,20 @@ __host__ __device__ inline TilePlan tile_plan(int BT, int rows, int na, int fn, 
   return q;
 }
 
-template <bool F16, bool GATED, int FN>
+template <bool F16, bool GATED, int FN, bool SUMS>
 __global__ void __launch_bounds__(kTileThreads, 1)
     linear_tile_kernel(const __grid_constant__ CUtensorMap map_w, const __grid_constant__ CUtensorMap map_u,
                        const __grid_constant__ CUtensorMap map_x, const __grid_constant__ CUtensorMap map_out,
                        const LinearParams p, const TilePlan plan) {
   constexpr int NA = GATED ? 2 : 1, CN = NA * FN, G = FN / 32;
-  constexpr uint32_t kCols = CN;  // TMEM columns, a power of two from 32
+  static_assert(!SUMS || G <= 2, "a warp keeps the sums of one unit");
+  constexpr uint32_t kCols = SUMS ? 2 * CN : CN;  // TMEM columns, a power of two from 32
   extern __shared__ uint8_t smem_raw[];
-  __shared__ __align__(8) uint64_t bars[2 * kTileStages + 1];
+  __shared__ __align__(8) uint64_t bars[2 * kTileStages + 4];
   __shared__ uint32_t tmem_slot;
   const uint32_t s0 = (smem_u32(smem_raw) + 1023u) & ~1023u;
   const uint32_t full = smem_u32(bars), empty = full + 8u * kTileStages, accfull = empty + 8u * kTileStages;
+  const uint32_t accfree = accfull + 16u;  // (two of each; one accumulator: the first accfull alone)
   const int tid = threadIdx.x, warp = __shfl_sync(kAll, tid >> 5, 0), lane = tid & 31;
   const uint32_t rank = tc::cluster_rank(), S = (uint32_t)plan.S;  // the cluster spans x
   const int n0 = blockIdx.y * FN, t0 = blockIdx.z * plan.BT;
@@ -603,7 +636,7 @@ __global__ void __launch_bounds__(kTileThreads, 1)
     // about 50 bytes per clock)
     if (lead) {
       for (int s = 0; s < plan.stages; ++s) bar_init(full + 8u * s, 1), bar_init(empty + 8u * s, 1);
-      bar_init(accfull, 1);
+      for (int b = 0; b < 2; ++b) bar_init(accfull + 8u * b, 1), bar_init(accfree + 8u * b, kTileEpi);
       mbar_fence_init();
     }
     __syncwarp();
@@ -644,6 +677,19 @@ __global__ void __launch_bounds__(kTileThreads, 1)
     if constexpr (GATED) load_unit(acc + (uint32_t)(FN + 32 * grp), u);
     tc::wait_ld();
   };
+  // the sums of this CTA's range of K: of the warp's unit in registers, or in TMEM
+  float sum[SUMS ? 32 : 1] = {}, sum_u[SUMS && GATED ? 32 : 1] = {};
+  auto take = [&](int grp, float (&v)[32], float (&u)[GATED ? 32 : 1]) {
+    if constexpr (SUMS) {
+#pragma unroll
+      for (int i = 0; i < 32; ++i) {
+        v[i] = sum[i];
+        if constexpr (GATED) u[i] = sum_u[i];
+      }
+    } else {
+      load(grp, v, u);
+    }
+  };
 
   Epilogue<F16, GATED, true> epi(p, &map_out, lane, s0 + (uint32_t)warp * kSquare);  // (in the stages, once they are done with)
   int mine = -1;
@@ -666,24 +712,35 @@ __global__ void __launch_bounds__(kTileThreads, 1)
     bool ok = true;
     uint32_t s = 0, phase = 0;
 #pragma unroll 1
-    for (int kb = kb0; kb < kb1; ++kb) {
-      ok = __all_sync(kAll, bar_wait(full + 8u * s, phase));
+    for (int k0 = kb0, part = 0; k0 < kb1 && ok; ++part) {
+      const uint32_t b = (uint32_t)part & 1u;
+      if (SUMS && part >= 2) ok = __all_sync(kAll, bar_wait(accfree + 8u * b, (uint32_t)(part / 2 - 1) & 1u));
       if (!ok) break;
       tc::fence_after_sync();
-      const uint32_t st = s0 + s * plan.stage;
-      const uint32_t a = tc::desc_lo(st), w = tc::desc_lo(st + (uint32_t)plan.BT * 128u);
-      if (lead) {
+      const int k1 = SUMS ? min(kb1, k0 + kPart) : kb1;
+      // (a commit at the part's end must not stand inside this loop: under a
+      // condition there it cost 0.7 us of the 8 to 10 us of a call)
+#pragma unroll 1
+      for (int kb = k0; kb < k1; ++kb) {
+        ok = __all_sync(kAll, bar_wait(full + 8u * s, phase));
+        if (!ok) break;
+        tc::fence_after_sync();
+        const uint32_t st = s0 + s * plan.stage;
+        const uint32_t a = tc::desc_lo(st), w = tc::desc_lo(st + (uint32_t)plan.BT * 128u);
+        if (lead) {
 #pragma unroll
-        for (int k = 0; k < 4; ++k) tc::mma_f16_lo(tmem, a + 2u * k, w + 2u * k, idesc, (kb > kb0 || k > 0) ? 1u : 0u);
-        tc::commit(empty + 8u * s);
+          for (int k = 0; k < 4; ++k)
+            tc::mma_f16_lo(tmem + b * CN, a + 2u * k, w + 2u * k, idesc, (kb > k0 || k > 0) ? 1u : 0u);
+          tc::commit(empty + 8u * s);
+        }
+        __syncwarp();
+        if (++s == (uint32_t)plan.stages) s = 0, phase ^= 1u;
       }
+      if (ok && lead) tc::commit(accfull + 8u * b);
       __syncwarp();
-      if (++s == (uint32_t)plan.stages) s = 0, phase ^= 1u;
+      k0 = k1;
     }
-    if (!ok)
-      let_issued_work_end();
-    else if (lead)
-      tc::commit(accfull);
+    if (!ok) let_issued_work_end();
     __syncwarp();
     if (S > 1) tc::cluster_wait();  // (1)
   } else {
@@ -695,14 +752,40 @@ __global__ void __launch_bounds__(kTileThreads, 1)
       epi.fetch(tok0, n0 + 32 * grp);
       epi.touch_bias(n0 + 32 * grp);
     });
-    const bool ok = __all_sync(kAll, bar_wait(accfull, 0));
-    tc::fence_after_sync();
+    bool ok = true;
+    if constexpr (SUMS) {
+      const int parts = (kb1 - kb0 + kPart - 1) / kPart;
+#pragma unroll 1
+      for (int part = 0; part < parts && ok; ++part) {
+        const uint32_t b = (uint32_t)part & 1u;
+        ok = __all_sync(kAll, bar_wait(accfull + 8u * b, (uint32_t)(part / 2) & 1u));
+        if (!ok) break;
+        tc::fence_after_sync();
+        if (busy && half < G) {
+          float v[32], u[GATED ? 32 : 1];
+          load_unit(acc + b * CN + (uint32_t)(32 * half), v);
+          if constexpr (GATED) load_unit(acc + b * CN + (uint32_t)(FN + 32 * half), u);
+          tc::wait_ld();
+#pragma unroll
+          for (int i = 0; i < 32; ++i) {
+            sum[i] += v[i];
+            if constexpr (GATED) sum_u[i] += u[i];
+          }
+        }
+        tc::fence_before_sync();
+        __syncwarp();
+        if (lane == 0) bar_arrive(accfree + 8u * b);
+      }
+    } else {
+      ok = __all_sync(kAll, bar_wait(accfull, 0));
+      tc::fence_after_sync();
+    }
     if (ok && S > 1)
       each_unit([&](int grp, uint32_t unit) {
         const uint32_t owner = unit % S;
         if (owner == rank) return;
         float v[32], u[GATED ? 32 : 1];
-        load(grp, v, u);
+        take(grp, v, u);
         const uint32_t slot = unit / S * (S - 1) + (rank < owner ? rank : rank - 1);
         const uint32_t dst = tc::map_rank(s0 + plan.slots + slot * (NA * kSquare) + 16u * (uint32_t)lane, owner);
         auto push = [&](uint32_t at, const float* w) {
@@ -726,7 +809,7 @@ __global__ void __launch_bounds__(kTileThreads, 1)
       if (grp != mine) epi.fetch(tok0, n0 + 32 * grp);
       const uint32_t src = s0 + plan.slots + unit / S * (S - 1) * (NA * kSquare) + 16u * (uint32_t)lane;
       float v[32], u[GATED ? 32 : 1];
-      load(grp, v, u);
+      take(grp, v, u);
       if (S > 1) {  // the sum over ranks in their order, whichever of them adds
         auto add = [&](uint32_t at, float* w) {
 #pragma unroll
@@ -785,7 +868,9 @@ __device__ __forceinline__ void pair_tile(int tile, int MT, int FT, int& mt, int
   mt = g * kGroup + in - ft * rows;
 }
 
-template <bool F16, bool GATED, int TN>
+// (SUMS: as in linear_tile_kernel, the two accumulators alternating by parts of
+// K; a warp keeps the sums of its units of the tile in registers.)
+template <bool F16, bool GATED, int TN, bool SUMS>
 __global__ void __launch_bounds__(kPairThreads, 1)
     linear_pair_kernel(const __grid_constant__ CUtensorMap map_w, const __grid_constant__ CUtensorMap map_u,
                        const __grid_constant__ CUtensorMap map_x, const __grid_constant__ CUtensorMap map_out,
@@ -802,7 +887,7 @@ __global__ void __launch_bounds__(kPairThreads, 1)
   const uint32_t rank = tc::cluster_rank();
   const int MT = (p.T + 255) / 256, FT = (p.N + FN - 1) / FN;
   const int ntiles = MT * FT, npairs = gridDim.x / 2, pair = blockIdx.x / 2;
-  const int KB = (p.K + kKB - 1) / kKB;
+  const int KB = (p.K + kKB - 1) / kKB, part = SUMS ? kPart : KB;
 
   next_may_start();
   if (warp == kPairEpi && lane == 0) {
@@ -870,13 +955,14 @@ __global__ void __launch_bounds__(kPairThreads, 1)
       bool ok = true;
       uint32_t s = 0, phase = 0, it = 0;
 #pragma unroll 1
-      for (int tile = pair; tile < ntiles && ok; tile += npairs, ++it) {
+      for (int tile = pair, k0 = 0; tile < ntiles && ok; ++it) {
         const uint32_t b = it & 1u;
         if (it >= 2) ok = __all_sync(kAll, bar_wait(accfree + 8u * b, (it / 2 - 1u) & 1u));
         if (!ok) break;
         tc::fence_after_sync();
+        const int k1 = min(KB, k0 + part);
 #pragma unroll 1
-        for (int kb = 0; kb < KB; ++kb) {
+        for (int kb = k0; kb < k1; ++kb) {
           ok = __all_sync(kAll, bar_wait(full + 8u * s, phase));
           if (!ok) break;
           tc::fence_after_sync();
@@ -885,7 +971,7 @@ __global__ void __launch_bounds__(kPairThreads, 1)
           if (lead) {
 #pragma unroll
             for (int k = 0; k < 4; ++k)
-              tc::mma2_f16_lo(tmem + b * TN, a + 2u * k, w + 2u * k, idesc, (kb > 0 || k > 0) ? 1u : 0u);
+              tc::mma2_f16_lo(tmem + b * TN, a + 2u * k, w + 2u * k, idesc, (kb > k0 || k > 0) ? 1u : 0u);
             tc::commit2(empty + 8u * s);
           }
           __syncwarp();
@@ -893,6 +979,8 @@ __global__ void __launch_bounds__(kPairThreads, 1)
         }
         if (ok && lead) tc::commit2(accfull + 8u * b);
         __syncwarp();
+        k0 = k1;
+        if (k0 == KB) k0 = 0, tile += npairs;
       }
       if (!ok) let_issued_work_end();
     }
@@ -906,31 +994,67 @@ __global__ void __launch_bounds__(kPairThreads, 1)
     Epilogue<F16, GATED, false> epi(p, &map_out, lane, op0 + ST * P::kStage + (uint32_t)warp * kSquare);
     uint32_t it = 0;
 #pragma unroll 1
-    for (int tile = pair; tile < ntiles; tile += npairs, ++it) {
+    for (int tile = pair; tile < ntiles; tile += npairs) {
       int mt, ft;
       pair_tile(tile, MT, FT, mt, ft);
-      const uint32_t b = it & 1u;
       const int tok = mt * 256 + (int)rank * 128 + 32 * quarter, c0 = half * (FN / 2), f0 = ft * FN + c0;
       epi.fetch(tok, f0);
-      const bool ok = __all_sync(kAll, bar_wait(accfull + 8u * b, (it / 2) & 1u));
-      if (!ok) break;
-      tc::fence_after_sync();
-      const uint32_t acc = tmem + b * TN + ((uint32_t)(32 * quarter) << 16) + (uint32_t)c0;
+      bool ok = true;
+      if constexpr (SUMS) {
+        float v[UN][32] = {}, u[GATED ? UN : 1][GATED ? 32 : 1] = {};
 #pragma unroll 1
-      for (int j = 0; j < UN; ++j) {
-        const int n = f0 + 32 * j;
-        float v[32], u[GATED ? 32 : 1];
-        load_unit(acc + 32u * (uint32_t)j, v);
-        if constexpr (GATED) load_unit(acc + (uint32_t)(TN / 2 + 32 * j), u);
-        tc::wait_ld();
-        if (j == UN - 1) {
-          // the last read of this accumulator by this warp
+        for (int k0 = 0; k0 < KB; k0 += part, ++it) {
+          const uint32_t b = it & 1u;
+          ok = __all_sync(kAll, bar_wait(accfull + 8u * b, (it / 2) & 1u));
+          if (!ok) break;
+          tc::fence_after_sync();
+          const uint32_t acc = tmem + b * TN + ((uint32_t)(32 * quarter) << 16) + (uint32_t)c0;
+#pragma unroll
+          for (int j = 0; j < UN; ++j) {
+            float q[32], z[GATED ? 32 : 1];
+            load_unit(acc + 32u * (uint32_t)j, q);
+            if constexpr (GATED) load_unit(acc + (uint32_t)(TN / 2 + 32 * j), z);
+            tc::wait_ld();
+#pragma unroll
+            for (int i = 0; i < 32; ++i) {
+              v[j][i] += q[i];
+              if constexpr (GATED) u[j][i] += z[i];
+            }
+          }
           tc::fence_before_sync();
           __syncwarp();
           if (lane == 0) tc::arrive_cluster(accfree0 + 8u * b);
         }
-        if (n < p.N && tok < p.T) epi.unit(tok, n, v, u);
-        if (j + 1 < UN) epi.fetch(tok, n + 32);
+        if (!ok) break;
+#pragma unroll
+        for (int j = 0; j < UN; ++j) {
+          const int n = f0 + 32 * j;
+          if (n < p.N && tok < p.T) epi.unit(tok, n, v[j], u[GATED ? j : 0]);
+          if (j + 1 < UN) epi.fetch(tok, n + 32);
+        }
+      } else {
+        const uint32_t b = it & 1u;
+        ok = __all_sync(kAll, bar_wait(accfull + 8u * b, (it / 2) & 1u));
+        if (!ok) break;
+        ++it;
+        tc::fence_after_sync();
+        const uint32_t acc = tmem + b * TN + ((uint32_t)(32 * quarter) << 16) + (uint32_t)c0;
+#pragma unroll 1
+        for (int j = 0; j < UN; ++j) {
+          const int n = f0 + 32 * j;
+          float v[32], u[GATED ? 32 : 1];
+          load_unit(acc + 32u * (uint32_t)j, v);
+          if constexpr (GATED) load_unit(acc + (uint32_t)(TN / 2 + 32 * j), u);
+          tc::wait_ld();
+          if (j == UN - 1) {
+            // the last read of this accumulator by this warp
+            tc::fence_before_sync();
+            __syncwarp();
+            if (lane == 0) tc::arrive_cluster(accfree0 + 8u * b);
+          }
+          if (n < p.N && tok < p.T) epi.unit(tok, n, v, u);
+          if (j + 1 < UN) epi.fetch(tok, n + 32);
+        }
       }
     }
     epi.drain();
@@ -1017,18 +1141,18 @@ cudaError_t launch_cluster(dim3 grid, int threads, int cluster, uint32_t smem, c
   return e != cudaSuccess ? e : launch_early(Kernel, grid, threads, smem, cluster, st, args...);
 }
 
-template <bool F16, bool GATED, int FN>
+template <bool F16, bool GATED, int FN, bool SUMS>
 cudaError_t launch_tile_t(const LinearParams& p, int BT, int S, cudaStream_t st) {
   Maps m;
   if (!make_maps<F16, GATED>(p, FN, BT, &m)) return cudaErrorInvalidValue;
   constexpr int NA = GATED ? 2 : 1;
   const TilePlan q = tile_plan(BT, NA * FN, NA, FN, S);
   const dim3 grid(S, (p.N + FN - 1) / FN, (p.T + BT - 1) / BT);
-  return launch_cluster<linear_tile_kernel<F16, GATED, FN>>(grid, kTileThreads, S, q.total, st, m.w, m.u, m.x, m.out,
+  return launch_cluster<linear_tile_kernel<F16, GATED, FN, SUMS>>(grid, kTileThreads, S, q.total, st, m.w, m.u, m.x, m.out,
                                                           p, q);
 }
 
-template <bool F16, bool GATED, int TN>
+template <bool F16, bool GATED, int TN, bool SUMS>
 cudaError_t launch_pair_t(const LinearParams& p, int sms, cudaStream_t st) {
   constexpr int FN = GATED ? TN / 2 : TN;
   Maps m;
@@ -1036,7 +1160,7 @@ cudaError_t launch_pair_t(const LinearParams& p, int sms, cudaStream_t st) {
   const int64_t tiles = (int64_t)((p.T + 255) / 256) * ((p.N + FN - 1) / FN);
   if (tiles > 0x3fffffff) return cudaErrorInvalidValue;
   const int pairs = (int)(tiles < sms / 2 ? tiles : sms / 2);
-  return launch_cluster<linear_pair_kernel<F16, GATED, TN>>(dim3(2 * pairs), kPairThreads, 2, PairPlan<TN>::kSmem,
+  return launch_cluster<linear_pair_kernel<F16, GATED, TN, SUMS>>(dim3(2 * pairs), kPairThreads, 2, PairPlan<TN>::kSmem,
                                                                   st, m.w, m.u, m.x, m.out, p);
 }
 
@@ -1071,11 +1195,13 @@ struct Way {
   float ns;
 };
 float max_f(float a, float b) { return a > b ? a : b; }
-Way best_way(int T, int K, int N, bool gated, int sms) {
+// narrow: tiles of at most 64 features, pairs of 128 columns (those that keep
+// sums in registers).
+Way best_way(int T, int K, int N, bool gated, bool narrow, int sms) {
   const int KB = (K + kKB - 1) / kKB, na = gated ? 2 : 1;
   Way best = {0, 0, 0, 1e30f};
   const int BT = T <= 32 ? 32 : T <= 64 ? 64 : 128;
-  for (int FN = 32; FN <= (gated ? 64 : 128); FN *= 2) {
+  for (int FN = 32; FN <= (gated || narrow ? 64 : 128); FN *= 2) {
     const int64_t tiles = (int64_t)((N + FN - 1) / FN) * ((T + BT - 1) / BT);
     if (tiles > 8 * sms) continue;
     for (int S = 1; S <= kMaxSplit && S <= KB; S *= 2) {
@@ -1088,7 +1214,7 @@ Way best_way(int T, int K, int N, bool gated, int sms) {
       if (ns < best.ns) best = {0, FN, S, ns};
     }
   }
-  for (int TN = 128; TN <= 256; TN *= 2) {
+  for (int TN = 128; TN <= (narrow ? 128 : 256); TN *= 2) {
     const int FN = TN / na;
     const int64_t tiles = (int64_t)((T + 255) / 256) * ((N + FN - 1) / FN);
     const int64_t waves = (tiles + sms / 2 - 1) / (sms / 2);
@@ -1101,13 +1227,19 @@ Way best_way(int T, int K, int N, bool gated, int sms) {
 
 template <bool F16, bool GATED>
 cudaError_t launch_tensor(const LinearParams& p, int sms, cudaStream_t st) {
-  const Way w = best_way(p.T, p.K, p.N, GATED, sms);
-  if (w.pair == 256) return launch_pair_t<F16, GATED, 256>(p, sms, st);
-  if (w.pair == 128) return launch_pair_t<F16, GATED, 128>(p, sms, st);
+  const bool sums = p.out_f32 && p.K > kPart * kKB;
+  const Way w = best_way(p.T, p.K, p.N, GATED, sums, sms);
   const int BT = p.T <= 32 ? 32 : p.T <= 64 ? 64 : 128;
-  if (w.width == 32) return launch_tile_t<F16, GATED, 32>(p, BT, w.S, st);
-  if (w.width == 64) return launch_tile_t<F16, GATED, 64>(p, BT, w.S, st);
-  if constexpr (!GATED) return launch_tile_t<F16, GATED, 128>(p, BT, w.S, st);
+  if (sums) {
+    if (w.pair) return launch_pair_t<F16, GATED, 128, true>(p, sms, st);
+    return w.width == 32 ? launch_tile_t<F16, GATED, 32, true>(p, BT, w.S, st)
+                         : launch_tile_t<F16, GATED, 64, true>(p, BT, w.S, st);
+  }
+  if (w.pair == 256) return launch_pair_t<F16, GATED, 256, false>(p, sms, st);
+  if (w.pair == 128) return launch_pair_t<F16, GATED, 128, false>(p, sms, st);
+  if (w.width == 32) return launch_tile_t<F16, GATED, 32, false>(p, BT, w.S, st);
+  if (w.width == 64) return launch_tile_t<F16, GATED, 64, false>(p, BT, w.S, st);
+  if constexpr (!GATED) return launch_tile_t<F16, GATED, 128, false>(p, BT, w.S, st);
   return cudaErrorInvalidValue;
 }
 

@@ -142,6 +142,23 @@ def test_activations_and_types(act, T, K, N, dtype, out):
 
 
 @pytest.mark.gpu
+@pytest.mark.parametrize("T", [1, 7, 12, 20, 64, 130, 300, 1500])
+@pytest.mark.parametrize("K,N", [(4100, 520), (16384, 200), (16384, 4096), (40000, 264)])
+@pytest.mark.parametrize("gated", [False, True])
+def test_long_sums_in_fp32(T, K, N, gated):
+    """The tensor cores cut each step of 16 columns towards zero, which loses
+    2^-24 of the running sum on the average; a sum that is finished every 512
+    columns loses at most 32 such steps of it, 2^-19, whatever K (the running
+    sum is smaller than the last one on the average, which leaves more than
+    the additions of the parts, rounded to nearest, take).  A gated output is
+    the product of two such sums.  In the 2-norm over all outputs."""
+    d = make(T, K, N, "bf16", "f32", "none", gated, bias=True, res=False, seed=9)
+    out = run_guarded(d, T, N, "f32")
+    ref = d["ref"][0]
+    assert (out.double() - ref).norm() <= (2 if gated else 1) * 2.0 ** -19 * ref.norm()
+
+
+@pytest.mark.gpu
 @pytest.mark.parametrize("T", [1, 20, 150, 1300])
 @pytest.mark.parametrize("out", ["bf16", "f32"])
 def test_residual_in_place_and_out_of_place_agree(T, out):
