@@ -1,5 +1,14 @@
 // moe_route.cu -- expert choice from router logits (moe_route_from_logits):
-// scores, selection bias, groups, top-K, weights.  One warp per token.
+//   s = softmax(l) or sigmoid(l), v = s + bias; the topk_groups groups of the
+//   largest value (their largest v, or the sum of their two largest); the top_k
+//   of v within them, ties to the lower index; w = scale * s [/ sum of s].
+// One warp per token, the row in its registers: lane holds E / 32 values, and
+// each choice is one integer maximum over the warp.  A row is read once (DRAM
+// 16.8 MB for 16384 x 512 bf16, its size), so what bounds the kernel is its
+// instructions, 0.6 to 0.7 issued per cycle and scheduler: top_k rounds of
+// choosing and, with groups, their ranking.  16384 tokens, 512 experts, top 10:
+// 12.3 us; 4096 tokens, top 8 of 4 of 16 groups: 9.4 us; one token: 3.0 us, of
+// which all but some hundred ns is the launch and the way of one load.
 #include <cuda_bf16.h>
 #include <cuda_fp16.h>
 #include <float.h>
