@@ -105,16 +105,17 @@ __device__ __forceinline__ int rank_candidates64(const RouteParams& p, const T* 
   return rank;
 }
 
-// Whether this lane's group is kept, where lo (the least value kept) and hi (the
-// largest left out) are within tol: fp64 values for the groups that close, in
-// the rank order of the others.  x: the lane's group's fp32 value; first: the
-// lane stands for its group.
+// Whether this lane's group is kept, where the fp32 values leave it open: the
+// group's value lies in [least, most], lo is the smallest `least` of the groups
+// kept in fp32 and hi the largest `most` of those left out.  fp64 values for
+// the groups that these bounds do not decide; first: the lane stands for its
+// group.
 template <typename T>
-__device__ __forceinline__ bool keep_group64(const RouteParams& p, const T* row, float top, float x, bool first, float lo,
-                                          float hi, float tol) {
+__device__ __forceinline__ bool keep_group64(const RouteParams& p, const T* row, float top, float least, float most,
+                                             bool first, float lo, float hi) {
   const int lane = threadIdx.x & 31, grp = lane >> p.lane_shift;
   const Scorer64 score = scorer64(p, row, top);
-  const bool sure = first && x > hi + tol, near = first && !sure && !(x < lo - tol);
+  const bool sure = first && least > hi, near = first && !sure && !(most < lo);
   const int left = p.topk_groups - __popc(__ballot_sync(kAll, sure));
   const uint32_t nears = __ballot_sync(kAll, near);
   double mine = 0.0;
@@ -440,7 +441,9 @@ __global__ void __launch_bounds__(32 * kRouteWarps, NV <= 16 ? 7 : NV == 32 ? 5 
       b = fmaxf(fmaxf(b, b2), fminf(a, a2));
       a = fmaxf(a, a2);
     }
-    const float x = p.top2 && p.per > 1 ? rank32(a + b) : a;
+    // (half the sum, which does not overflow; +inf and -inf together rank as -inf)
+    const bool two = p.top2 && p.per > 1;
+    const float x = two ? rank32(0.5f * a + 0.5f * b) : a;
     int rank = 0;  // of this lane's group among all
     for (int g = 0; g < p.n_groups; ++g) {
       const float o = __shfl_sync(kAll, x, g << p.lane_shift);
@@ -449,12 +452,19 @@ __global__ void __launch_bounds__(32 * kRouteWarps, NV <= 16 ? 7 : NV == 32 ? 5 
     const bool first = sub == 0 && grp < p.n_groups;
     bool in = first && rank < p.topk_groups;
     if (by_value || p.top2) {
-      // the last kept group has to lead the first one left out by more than
-      // twice the error of a sum of two values
-      const float lo = from_order32(__reduce_min_sync(kAll, in ? order32(x) : ~0u));
-      const float hi = from_order32(__reduce_max_sync(kAll, first && !in ? order32(x) : 0u));
-      const float tol = 4.f * eps + 0x1p-21f * fmaxf(fabsf(lo), fabsf(hi));
-      if (!(lo - hi > tol)) in = keep_group64(p, row, top, x, first, lo, hi, tol);
+      // A group's value in fp64 is within `err` of x: a and b are each off by
+      // eps and by the rounding of s + bias, 2^-24 |a| and 2^-24 |b|, which do
+      // not shrink where a and b cancel, and so the rounding of their sum (the
+      // factor of two left over takes in that of the bounds themselves).  An
+      // infinite value is exact.  The kept groups have to lead those left out
+      // by more than these errors; equal infinities are in their order already.
+      float err = eps + 0x1p-22f * fabsf(a);
+      if (two) err += 0x1p-22f * fabsf(b);
+      if (fabsf(x) == INFINITY) err = 0.f;
+      const float least = x - err, most = x + err;
+      const float lo = from_order32(__reduce_min_sync(kAll, in ? order32(least) : ~0u));
+      const float hi = from_order32(__reduce_max_sync(kAll, first && !in ? order32(most) : 0u));
+      if (!(lo > hi || (lo == hi && fabsf(lo) == INFINITY))) in = keep_group64(p, row, top, least, most, first, lo, hi);
     }
     const uint32_t kept = __ballot_sync(kAll, in);
     if (in) cand[__popc(kept & ((1u << lane) - 1u))] = grp;

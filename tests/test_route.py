@@ -298,3 +298,37 @@ def test_refusals_on_the_host():
     assert topk(good, T=0) == 0
     assert topk(good, hidden=60) == 2 and topk(good, x=None) == 1 and topk(good, x=1032) == 1
     assert topk(good, ws=None) == M.MOE_ERR_WORKSPACE and topk(good, nb=100) == M.MOE_ERR_WORKSPACE
+
+
+# ---- values that cancel, and far scores ------------------------------------------------
+
+@pytest.mark.gpu
+@pytest.mark.parametrize("score", ["softmax", "sigmoid"])
+@pytest.mark.parametrize("B", [1e3, 1e5, 1e6, 3e38])
+@pytest.mark.parametrize("per,rest", [(2, 0.0), (8, -1.0), (8, -4.0), (32, -1.0)])
+def test_groups_whose_two_values_cancel(score, B, per, rest):
+    """Biases +B and -B in every group (the others at rest * B): the sum of the
+    two largest is small, the fp32 roundings of its summands are not.  Logits
+    so far apart that these roundings decide most rows."""
+    import torch
+    G, keep = 8, 4
+    bias = np.full((G, per), max(rest * B, -3.4e38), np.float32)
+    bias[:, 0], bias[:, 1] = B, -B
+    r = np.random.RandomState(per)
+    bias = np.stack([r.permutation(b) for b in bias]).reshape(-1)
+    spread = min(4.0 * 2.0 ** -24 * B * (2 * G if score == "softmax" else 1), 2.0)
+    l = torch.from_numpy((0.1 + spread * r.standard_normal((200, G * per))).astype(np.float32)).cuda()
+    for K in (1, 6):
+        check(l, K, bias, score=score, groups=G, keep=keep, group_score="top2")
+
+
+@pytest.mark.gpu
+def test_cancelling_groups_by_hand():
+    """Sigmoid scores (.50004, .5) and (.500029, .500029) under biases (1000, -1000): the second group's sum is larger."""
+    import torch
+    s = np.array([[0.50004, 0.5, 0.500029, 0.500029]])
+    l = torch.from_numpy(np.log(s / (1 - s)).astype(np.float32)).cuda()
+    bias = np.array([1000, -1000, 1000, -1000], np.float32)
+    idx, _ = run(l, 1, bias, score="sigmoid", groups=2, keep=1, group_score="top2")
+    assert idx[0, 0] == 2
+    check(l, 2, bias, score="sigmoid", groups=2, keep=1, group_score="top2")
