@@ -164,8 +164,9 @@ moe_status moe_topk_from_logits(const moe_config* cfg, const float* logits, int 
  *              renormalise (0 when that sum is 0, as for a row of -inf)
  * The choice is that of values compared in fp64 (without a bias experts, and
  * groups of MOE_GROUP_MAX, are ordered by their logits), so it does not hang
- * on how an fp32 sigmoid rounds.  Weights are fp32: within 2^-18 of the
- * formula (typically 2^-23), or within 2^-126.
+ * on how an fp32 sigmoid rounds.  Weights are fp32: within 2^-19 of the
+ * formula (2^-18 for softmax without renormalise; typically 2^-23), or within
+ * 2^-126.
  * Limits: E <= 2048, K <= 32, n_groups <= 32, K <= topk_groups * E / n_groups,
  * T <= 2^30. */
 enum { MOE_SCORE_SOFTMAX = 0, MOE_SCORE_SIGMOID = 1 };

@@ -261,15 +261,26 @@ __device__ __forceinline__ void route_exact(const RouteParams& p, int64_t t, uin
 
 // ---- one warp per token ------------------------------------------------------------------
 // Values are fp32 here.  With s' the fp32 score of s (fast_exp is off by at most
-// 2 + 1.16 |x| ulp, a fast division by 2):
+// 2 + 1.16 |x| ulp, a fast division by 2) and u = 2^-24:
 //   sigmoid   |s' - s| <= 2^-23 ((1 - s) (2 + 1.16 |l|) s + 1/2 + 2 s) < 2^-21
-//   softmax   e^(l - max) is off by at most 2^-22; the row's sum by 20 + ulp,
-//             so |s' - s| <= 2^-18 / sum (no score is larger than 1 / sum)
+//   softmax   with x = l - max rounded (u |x|), e^x is off by at most 4 u; the
+//             terms of the row's sum together by (4 + 3.3 * 4.9) u of it (4.9:
+//             the largest mean |x| that 2048 terms can have, weighted by
+//             themselves), its additions by 15 u, the reciprocal and the
+//             product by 3 u: 44 u in all, so |s' - s| <= 2^-18 / sum (no score
+//             is larger than 1 / sum)
 // and v' = s' + bias adds 2^-24 |v'|.  A choice that holds by more than these
 // bounds is the fp64 choice; where candidates or groups are closer (a token in
 // some hundreds), theirs alone are computed in fp64.  A row with more candidates
 // than lanes goes to route_exact.  Without a bias experts are ordered by their
 // logits, which needs no bound.
+// Weights come from the accurate exponential (2 ulp: 4 u), l - max with its
+// rounding made good and divisions to the nearest: under 23 u of the formula.
+// Softmax weights that are not renormalised take the sum above, 42 u in all
+// (accurate exponentials there would make it 31 and cost 16384 tokens 13.8 us
+// instead of 12.6); renormalised ones do not see it, a constant factor.
+// Measured in the 2-norm: 6 10^-8 for both.  A chosen score below 2^-100 is no
+// longer sure to keep its bits through this, and its row goes to fp64.
 //
 // Top-K without K rounds over E: each lane's largest value; the K-th largest
 // of those 32 is a bound that at least K values reach; the values
@@ -391,11 +402,17 @@ __global__ void __launch_bounds__(32 * kRouteWarps, NV <= 16 ? 7 : NV == 32 ? 5 
     top = warp_maxf(top);
     if (top == -INFINITY) top = 0.f;  // a row of -inf: every score is 0
     if (by_value || !p.renorm) {
-      float sum = 0.f;
+      // (partial sums: at most 10 additions of a lane stand behind each other)
+      constexpr int PS = NV <= 16 ? 4 : 8;
+      float part[PS] = {};
 #pragma unroll
-      for (int i = 0; i < NV; ++i) sum += fast_exp(v[i] - top);
-      sum = warp_sum(sum);
-      inv = sum > 0.f ? __fdividef(1.f, sum) : 1.f;
+      for (int i = 0; i < NV; ++i) part[i % PS] += fast_exp(v[i] - top);
+#pragma unroll
+      for (int o = PS / 2; o; o >>= 1)
+#pragma unroll
+        for (int i = 0; i < o; ++i) part[i] += part[i + o];
+      const float sum = warp_sum(part[0]);
+      inv = sum > 0.f ? __fdiv_rn(1.f, sum) : 1.f;
     }
   }
   const float eps = p.sigmoid || !by_value ? 0x1p-21f : 0x1p-18f * inv;  // bound of a score's error
@@ -538,12 +555,23 @@ __global__ void __launch_bounds__(32 * kRouteWarps, NV <= 16 ? 7 : NV == 32 ? 5 
       if (__any_sync(kAll, close)) rank = rank_candidates64(p, row, top, e, count);
     }
     const bool in = live && rank < p.K;
-    // weights from the accurate exponential
-    float w = p.sigmoid ? __fdiv_rn(1.f, 1.f + expf(-l)) : expf(l - top) * inv;
+    // weights from the accurate exponential; sigmoid by e^-|l|, which does not
+    // overflow, softmax with what the rounding of l - top lost put back
+    float w;
+    if (p.sigmoid) {
+      const float q = expf(-fabsf(l));
+      w = __fdiv_rn(l < 0.f ? q : 1.f, 1.f + q);
+    } else {
+      const float d = l - top, back = d - l, lost = (l - (d - back)) - (top + back);
+      const float q = expf(d);
+      w = (q > 0.f ? fmaf(q, lost, q) : 0.f) * inv;
+    }
+    // a score of 0 is exact for a logit of -inf alone
+    open = __any_sync(kAll, in && w < 0x1p-100f && l > -INFINITY);
     if (p.renorm) {
       const float total = warp_sum(in ? w : 0.f);
       w = __fdiv_rn(w, total);
-      open = open || !(total >= 0x1p-100f);  // scores near or below fp32's range (or none): fp64
+      open = open || !(total > 0.f);  // none left
     }
     if (!open) {
       if (in) {

@@ -332,3 +332,47 @@ def test_cancelling_groups_by_hand():
     idx, _ = run(l, 1, bias, score="sigmoid", groups=2, keep=1, group_score="top2")
     assert idx[0, 0] == 2
     check(l, 2, bias, score="sigmoid", groups=2, keep=1, group_score="top2")
+
+
+# Weights against the formula, u = 2^-24.  A chosen exponential is within 2 ulp
+# (4 u), a sigmoid by its division and 1 + e within 8 u; the sum of the chosen
+# adds 8 + 5 u, division and scale 2 u: 23 u.  Softmax without renormalising
+# divides by the sum over all experts instead: its fast exponentials 2 + 1.66 |x|
+# ulp, where |x| is 4.9 at most on the average weighted by them (20 u), 15
+# additions, reciprocal, product and scale, and the chosen one's own 4 u: 42 u.
+WEIGHT_RTOL = {True: 2.0 ** -19, False: 2.0 ** -18}  # by "sum of the chosen, or sigmoid"
+
+
+@pytest.mark.gpu
+@pytest.mark.parametrize("score", ["softmax", "sigmoid"])
+@pytest.mark.parametrize("renorm", [True, False])
+@pytest.mark.parametrize("scale", [1.0, 2.5, 1e6, 1e-6])
+@pytest.mark.parametrize("dtype", ["f32", "bf16", "f16"])
+def test_weights_hold_their_bound(score, renorm, scale, dtype):
+    """Every weight within its bound of the formula (or 2^-126): chosen scores
+    from the largest to far below fp32's range, forced by the bias."""
+    import torch
+    r = np.random.RandomState(5)
+    for E, low in ((24, -100.0), (512, -30.0), (1000, -60.0), (2048, -8.0)):
+        l = np.where(r.rand(40, E) < 0.5, low * r.rand(40, E), 1.3 * r.standard_normal((40, E)))
+        l[0], l[1] = -69.0, -88.8
+        l[2, :] = np.linspace(-105.0, -60.0, E)
+        l[3, 0], l[3, 1:] = 80.0, -60.0
+        l = torch.from_numpy(l.astype(np.float32)).to(
+            {"f32": torch.float32, "bf16": torch.bfloat16, "f16": torch.float16}[dtype]).cuda()
+        for bias in (None, (2.0 * r.rand(E)).astype(np.float32)):
+            gi, gw = run(l, 16, bias, score=score, renorm=renorm, scale=scale)
+            wi, ww = plain(l.double().cpu().numpy(), bias, 16, score=score, renorm=renorm, scale=scale)
+            assert np.array_equal(gi, wi)
+            np.testing.assert_allclose(gw, ww, rtol=WEIGHT_RTOL[renorm or score == "sigmoid"], atol=ATOL)
+
+
+@pytest.mark.gpu
+def test_a_weight_whose_score_leaves_the_range_of_fp32():
+    """Sigmoid scores of -69 and -88.8 (the second is below fp32's normal range) renormalised: 2.5e-9, not 0."""
+    import torch
+    l = torch.tensor([[-69.0, -88.8, -200.0, -300.0]], device="cuda")
+    _, w = run(l, 2, None, score="sigmoid")
+    want = np.exp(-88.8 + 69.0)
+    np.testing.assert_allclose(w[0, 1], np.exp(np.float64(np.float32(-88.8)) + 69.0), rtol=WEIGHT_RTOL[True])
+    assert abs(w[0, 1] / want - 1) < 1e-5
