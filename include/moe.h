@@ -210,6 +210,9 @@ moe_status moe_route_topk(const moe_route_config* cfg, int hidden, const void* x
  * fp32 accumulation and epilogue, one rounding to the output type.
  *   act: MOE_ACT_NONE v; SILU v / (1 + e^-v); GELU v * Phi(v) (normal CDF);
  *        GELU_TANH 0.5 v (1 + tanh(sqrt(2/pi) (v + 0.044715 v^3))); RELU max(v, 0)
+ *        each of its fp32 argument to within 2^-126 or relative 2^-20 (GELU),
+ *        2^-20 (1 + |v| / 8) (SILU), 2^-20 (1 + sqrt(2/pi) |v + 0.044715 v^3|)
+ *        (GELU_TANH)
  * x [T][K] and w, w_up [N][K] of one 16-bit type (dtype MOE_BF16 or MOE_F16);
  * bias, bias_up fp32 [N] or NULL; residual and out [T][N] of out_dtype (dtype
  * or MOE_F32).  Rows are ldx, ldw, ldw_up, ldr, ldo elements apart.  x, w and

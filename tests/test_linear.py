@@ -319,3 +319,45 @@ def test_refusals_on_the_host():
     gated = M.linear_config(64, 32, gated=True)
     assert call(gated, w_up=24, ldw_up=64) == 1 and call(gated, w_up=32, ldw_up=60) == 1
     assert lib.moe_linear_forward(None, None, None, 0, None, 0, 0, None, 0, None) == 1
+
+
+# ---- the activation alone -------------------------------------------------------------
+
+@pytest.mark.gpu
+@pytest.mark.parametrize("act", ["silu", "gelu", "gelu_tanh"])
+@pytest.mark.parametrize("T,N", [(1, 5), (12, 33), (60, 64), (300, 96), (2500, 512)])
+@pytest.mark.parametrize("gated", [False, True])
+def test_activations_alone_in_fp32(act, T, N, gated):
+    """K = 1 and x = 1: the sum is the weight itself, so the output is the
+    activation of it.  With u = 2^-24: SiLU's e^-v is off by 1.3 |v| u (the
+    rounded v log2 e, about what half a step of v makes of it) and 6 u, the rest
+    by 5 u.  GELU: the normal CDF (5 ulp: 10 u) and the product.  The tanh
+    form's exponent z = 2 sqrt(2/pi) (v + 0.044715 v^3) is off by 6 u of it more
+    (two constants and four steps).  So 2^-20 of the value, for SiLU
+    2^-20 (1 + |v| / 8), for the tanh form 2^-20 (1 + |z| / 2), or 2^-126; a gate's
+    product rounds once more."""
+    import torch
+    v = torch.cat([torch.linspace(-130, 130, 257), torch.linspace(-12, 12, 129), -torch.logspace(-30, 2, 65),
+                   torch.linspace(-89, -87, 17)])
+    v = v.repeat((N + len(v) - 1) // len(v) + 1)[:N + 468]
+    worst = 0.0
+    for first in range(0, 468, max(1, min(N, 64))):
+        w = v[first:first + N].bfloat16().cuda().view(N, 1)
+        x = torch.ones(T, 1, dtype=torch.bfloat16, device="cuda")
+        x = torch.cat([x, torch.zeros(T, 7, dtype=torch.bfloat16, device="cuda")], 1)[:, :1]
+        wpad = torch.zeros(N, 8, dtype=torch.bfloat16, device="cuda")
+        wpad[:, :1] = w
+        up = torch.zeros(N, 8, dtype=torch.bfloat16, device="cuda")
+        up[:, :1] = 3.0
+        cfg = M.linear_config(1, N, act=ACTS[act], gated=gated, out_dtype=M.MOE_F32)
+        wts = M.linear_weights(cfg, wpad[:, :1], w_up=up[:, :1] if gated else None)
+        out = torch.empty(T, N, device="cuda")
+        M.moe_linear_forward(cfg, wts, x, out)
+        d = w.double().view(1, N)
+        # (the normal CDF of large negative v by erfc: 1 + erf cancels there)
+        ref = (d * 0.5 * torch.special.erfc(-d * 0.5 ** 0.5) if act == "gelu" else act64(d, act)) * (3.0 if gated else 1.0)
+        far = {"silu": d.abs() / 8, "gelu": 0.0,
+               "gelu_tanh": (2 / np.pi) ** 0.5 * (d + 0.044715 * d ** 3).abs()}[act]
+        lim = (2.0 ** -20 * (1 + far) + 2.0 ** -24) * ref.abs() + 2.0 ** -126
+        worst = max(worst, ((out.double() - ref).abs() / lim).max().item())
+    assert worst <= 1.0, worst
