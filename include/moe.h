@@ -207,7 +207,10 @@ moe_status moe_route_topk(const moe_route_config* cfg, int hidden, const void* x
  *   y[t][n] = act(sum_k x[t][k] w[n][k] + bias[n])
  *               [* (sum_k x[t][k] w_up[n][k] + bias_up[n])   when gated]
  *               [+ residual[t][n]]
- * fp32 accumulation and epilogue, one rounding to the output type.
+ * fp32 accumulation and epilogue, one rounding to the output type.  (The tensor
+ * cores add towards zero; sums are split over K so that what this takes from
+ * them stays below 10^-6 for fp32 outputs and below 1/16 of half a step for
+ * 16-bit ones.)
  *   act: MOE_ACT_NONE v; SILU v / (1 + e^-v); GELU v * Phi(v) (normal CDF);
  *        GELU_TANH 0.5 v (1 + tanh(sqrt(2/pi) (v + 0.044715 v^3))); RELU max(v, 0)
  *        each of its fp32 argument to within 2^-126 or relative 2^-20 (GELU),

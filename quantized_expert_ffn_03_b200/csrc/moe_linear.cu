@@ -31,11 +31,21 @@ constexpr unsigned kAll = 0xffffffffu;
 constexpr int kKB = 64;  // columns of K per step: 128 bytes, one swizzle row
 
 // The tensor cores cut what an addition shifts out of the accumulator's 24
-// bits, always towards zero, which over K columns makes a sum too small by
-// about K 10^-9 of its size (measured 9 10^-6 at 16384).  fp32 outputs show
-// that, so for them an accumulator holds kPart steps (512 columns), and the
-// parts are added up in fp32, rounding to nearest: 5 10^-7 at every K.
+// bits, always towards zero, which makes a sum over many columns too small:
+// for operands of one sign by 7.9 10^-6 of its size after 4096 columns of one
+// accumulator, 6.5 10^-5 after 16384, 3.4 10^-4 after 65536, 1.5 10^-3 after
+// 2^18 (measured; mixed signs a quarter of that, but 4.4 10^-6 after 4096).
+// Where the output shows that, an accumulator holds kPart steps (512 columns),
+// and the parts are added up in fp32, rounding to nearest: 2.4 10^-7 (mixed
+// signs 4.8 10^-7) up to K = 16384, below 7.5 10^-7 at 2^20.
 constexpr int kPart = 512 / kKB;
+// The longest K that one accumulator takes: 512 columns for fp32 outputs, and
+// for 16-bit ones what keeps the loss below 1/16 of half a step of the type
+// (2^-11 for fp16, 2^-8 for bf16).  Parts need narrower tiles: fp16 2048 x 16384
+// x 4096 takes 254 us with them, 193 without.
+__host__ __device__ constexpr int longest_sum(bool out_f32, bool f16) {
+  return out_f32 ? kPart * kKB : f16 ? 1 << 13 : 1 << 15;
+}
 
 // ---- epilogue arithmetic ------------------------------------------------------------
 
@@ -591,7 +601,7 @@ __device__ __forceinline__ void load_unit(uint32_t taddr, float (&v)[32]) {
 // once) and keeps the tensor cores busy 19 percent of it; 250 x 1024 x 4096
 // takes 5.7 us, 64 x 4096 x 1024 gated 8.1.
 //
-// SUMS (fp32 outputs of more than kPart steps): the parts go to two
+// SUMS (K beyond longest_sum): the parts go to two
 // accumulators in turn, and the epilogue warps add them up in registers while
 // the MMAs go on (64 x 4096 x 4096: 11.5 us, 9.8 without).
 constexpr int kTileEpi = 8;                         // warps that read TMEM
@@ -1255,7 +1265,7 @@ Way best_way(int T, int K, int N, bool gated, bool narrow, int sms) {
 
 template <bool F16, bool GATED>
 cudaError_t launch_tensor(const LinearParams& p, int sms, cudaStream_t st) {
-  const bool sums = p.out_f32 && p.K > kPart * kKB;
+  const bool sums = p.K > longest_sum(p.out_f32, F16);
   const Way w = best_way(p.T, p.K, p.N, GATED, sums, sms);
   const int BT = p.T <= 32 ? 32 : p.T <= 64 ? 64 : 128;
   if (sums) {

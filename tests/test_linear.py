@@ -361,3 +361,30 @@ def test_activations_alone_in_fp32(act, T, N, gated):
         lim = (2.0 ** -20 * (1 + far) + 2.0 ** -24) * ref.abs() + 2.0 ** -126
         worst = max(worst, ((out.double() - ref).abs() / lim).max().item())
     assert worst <= 1.0, worst
+
+
+@pytest.mark.gpu
+@pytest.mark.parametrize("T,N", [(12, 72), (40, 64), (200, 96), (600, 512), (1500, 2048)])
+@pytest.mark.parametrize("dtype,K", [("f16", 8192), ("f16", 16384), ("f16", 16448), ("f16", 1 << 18),
+                                     ("f16", 1 << 20), ("bf16", 1 << 15), ("bf16", 1 << 17), ("bf16", 1 << 20)])
+@pytest.mark.parametrize("gated", [False, True])
+def test_long_sums_in_16_bits(T, N, dtype, K, gated):
+    """Operands of one sign: what the tensor cores cut off adds up over K.  A
+    16-bit output is within half a step of its type of the sum, and 1/16 of
+    that half step for the sum's own error (twice for the product of two)."""
+    import torch
+    g = torch.Generator(device="cuda").manual_seed(K + T)
+    dt = torch_type(dtype)
+    x = (0.5 + torch.rand(T, K, generator=g, device="cuda")).to(dt)
+    w = ((0.5 + torch.rand(N, K, generator=g, device="cuda")) * (100.0 / K)).to(dt)
+    wu = ((0.5 + torch.rand(N, K, generator=g, device="cuda")) * (100.0 / K)).to(dt) if gated else None
+    cfg = M.linear_config(K, N, gated=gated, dtype=CODES[dtype])
+    out = torch.empty(T, N, dtype=dt, device="cuda")
+    M.moe_linear_forward(cfg, M.linear_weights(cfg, w, w_up=wu), x, out)
+
+    def product(m):  # in fp64, a slice of K at a time
+        return sum(x[:, k:k + 65536].double() @ m[:, k:k + 65536].double().T for k in range(0, K, 65536))
+
+    ref = product(w) * (product(wu) if gated else 1.0)
+    half = torch.finfo(dt).eps / 2
+    assert ((out.double() - ref).abs() <= (1 + (2 if gated else 1) / 16) * half * ref.abs()).all()
