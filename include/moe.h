@@ -381,8 +381,9 @@ moe_status moe_layer_forward_routed(const moe_config* cfg, const moe_layer_weigh
  * prompt-side call behind a router of the caller's own (moe_route_topk).
  * Arguments as moe_layer_forward_routed, workspace
  * moe_layer_batched_workspace_bytes; the router weights are not read and may be
- * NULL.  A token may name one expert more than once.  An id outside [0, E) or a
- * bad pointer for a chosen expert leaves MOE_ERR_DEVICE in the workspace
+ * NULL.  idx and w must be 4-byte aligned (as for moe_layer_forward_routed).  A
+ * token may name one expert more than once.  An id outside [0, E) or a bad
+ * pointer for a chosen expert leaves MOE_ERR_DEVICE in the workspace
  * (moe_device_error) and the outputs unspecified. */
 moe_status moe_layer_forward_routed_batched(const moe_config* cfg, const moe_layer_weights* wts,
                                             const void* x_bf16, const void* residual_bf16, int T,

@@ -691,12 +691,22 @@ int moe_layer_tokens_per_launch(const moe_config* cfg) {
   return tokens_per_launch(L, di.sms < kMaxGrid ? di.sms : kMaxGrid, chunk_tokens(L));
 }
 
+// A routing given by the caller: the kernels read whole elements.
+static moe_status check_routing(const int32_t* idx, const float* w) {
+  if (!idx || !w) return fail(MOE_ERR_INVALID_ARG, "NULL routing");
+  if (!aligned(idx, 4) || !aligned(w, 4)) return fail(MOE_ERR_INVALID_ARG, "idx and w must be aligned to their elements");
+  return MOE_OK;
+}
+
 moe_status moe_layer_forward_routed(const moe_config* cfg, const moe_layer_weights* wts,
                                     const void* x_bf16, const void* residual_bf16, int T,
                                     const int32_t* idx, const float* w, void* h_out_bf16,
                                     void* y_norm_bf16, void* workspace, size_t ws_bytes,
                                     cudaStream_t stream) {
-  if (T > 0 && (!idx || !w)) return fail(MOE_ERR_INVALID_ARG, "NULL routing");
+  if (T > 0) {
+    const moe_status s = check_routing(idx, w);
+    if (s != MOE_OK) return s;
+  }
   return layer_forward_impl(cfg, wts, x_bf16, residual_bf16, T, h_out_bf16, y_norm_bf16, nullptr, nullptr,
                             workspace, ws_bytes, nullptr, 0, stream, idx, w);
 }
@@ -745,7 +755,10 @@ moe_status moe_layer_forward_routed_batched(const moe_config* cfg, const moe_lay
                                             const void* residual_bf16, int T, const int32_t* idx, const float* w,
                                             void* h_out_bf16, void* y_norm_bf16, void* workspace, size_t ws_bytes,
                                             cudaStream_t stream) {
-  if (T > 0 && (!idx || !w)) return fail(MOE_ERR_INVALID_ARG, "NULL routing");
+  if (T > 0) {
+    const moe_status s = check_routing(idx, w);
+    if (s != MOE_OK) return s;
+  }
   return layer_forward_batched(cfg, wts, x_bf16, residual_bf16, T, h_out_bf16, y_norm_bf16, nullptr, nullptr,
                                workspace, ws_bytes, stream, idx, w);
 }

@@ -197,3 +197,14 @@ def test_dependent_calls_back_to_back(T, graph):
         torch.cuda.synchronize()
         assert all(torch.equal(a, b) for a, b in zip(want, got))
     assert M.moe_linear_device_error() == (M.MOE_OK, 0)
+
+
+@pytest.mark.parametrize("fn", ["moe_layer_forward_routed", "moe_layer_forward_routed_batched"])
+def test_a_given_routing_off_its_elements_is_refused_on_the_host(fn):
+    """Kernels read idx and w as 4-byte elements: other addresses never reach them."""
+    import ctypes as C
+    lib, cfg, wts = M.lib(), M.config(256, 128, 16, 2), M.MoeLayerWeights()
+    for idx, w in ((18, 16), (16, 17), (17, 18)):
+        assert getattr(lib, fn)(C.byref(cfg), C.byref(wts), 16, 16, 40, idx, w, 16, 16, 256, 1 << 20, None) == 1
+        assert "aligned to their elements" in M.last_error(), (idx, w)
+    assert getattr(lib, fn)(C.byref(cfg), C.byref(wts), 16, 16, 0, 18, 17, 16, 16, 256, 0, None) == 0
