@@ -246,10 +246,20 @@ moe_status moe_linear_forward(const moe_linear_config* cfg, const moe_linear_wei
                               const void* residual, int64_t ldr, int T, void* out, int64_t ldo, cudaStream_t stream);
 
 /* The device-side error of the moe_linear_forward calls (and moe_route_topk's
- * products) on the current device since the last read: synchronises the
- * stream, returns MOE_OK or MOE_ERR_TIMEOUT and clears the word; *detail (may
- * be NULL) gets the raw code. */
+ * products) that were made on this stream of the current device since the last
+ * read: synchronises the stream, returns MOE_OK or MOE_ERR_TIMEOUT and clears
+ * the stream's word; *detail (may be NULL) gets the raw code.  Other streams'
+ * words stay as they are.  A captured call reports to the stream that it was
+ * captured on, wherever its graph runs; a stream made after another was
+ * destroyed may have its handle and so its word.  (1023 streams have words of
+ * their own; later ones share that of the default stream.) */
 moe_status moe_linear_device_error(uint32_t* detail, cudaStream_t stream);
+
+/* Self-test of the bounded waits of the dense product: a tiny kernel that
+ * waits, with the given limit in nanoseconds (at most 10^9), for an arrival
+ * that never comes.  The wait must give up, record MOE_ERR_TIMEOUT in the
+ * stream's word and return, leaving the GPU context usable. */
+moe_status moe_linear_selftest_bounded_wait(uint64_t timeout_ns, cudaStream_t stream);
 
 /* ------------------------------------------------------------------------
  * Whole layer.

@@ -120,6 +120,7 @@ EXPORTS = {
     "moe_linear_forward": (C.c_int, [C.c_void_p, C.c_void_p, C.c_void_p, C.c_int64, C.c_void_p, C.c_int64, C.c_int,
                                      C.c_void_p, C.c_int64, C.c_void_p]),
     "moe_linear_device_error": (C.c_int, [C.c_void_p, C.c_void_p]),
+    "moe_linear_selftest_bounded_wait": (C.c_int, [C.c_uint64, C.c_void_p]),
     "moe_stream_create": (C.c_int, [C.c_void_p, C.c_int, C.c_void_p, C.c_size_t, C.c_int, C.c_void_p]),
     "moe_stream_inject_fault": (C.c_int, [C.c_void_p, C.c_int, C.c_int]),
     "moe_stream_create_file": (C.c_int, [C.c_void_p, C.c_int, C.c_char_p, C.c_int, C.c_int, C.c_int,
@@ -482,10 +483,14 @@ def moe_linear_forward(cfg, wts, x, out, residual=None, stream=None):
 
 
 def moe_linear_device_error(stream=None):
-    """Returns (status, detail) of the dense products on the current device and clears it."""
+    """Returns (status, detail) of the dense products made on this stream and clears it."""
     detail = C.c_uint32(0)
     st = _lib.moe_linear_device_error(C.byref(detail), _stream(stream))
     return st, detail.value
+
+
+def moe_linear_selftest_bounded_wait(timeout_ns, stream=None):
+    _check(_lib.moe_linear_selftest_bounded_wait(int(timeout_ns), _stream(stream)))
 
 
 def route_config(n_experts, top_k, score=MOE_SCORE_SOFTMAX, n_groups=1, topk_groups=1, group_score=MOE_GROUP_MAX,

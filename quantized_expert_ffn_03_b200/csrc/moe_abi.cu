@@ -1003,6 +1003,12 @@ moe_status moe_linear_device_error(uint32_t* detail, cudaStream_t stream) {
   return fail(MOE_ERR_TIMEOUT, "a bounded device-side wait of a dense product expired");
 }
 
+moe_status moe_linear_selftest_bounded_wait(uint64_t timeout_ns, cudaStream_t stream) {
+  if (timeout_ns > 1000000000ull) return fail(MOE_ERR_INVALID_ARG, "timeout_ns must be at most 10^9");
+  CUDA_TRY(launch_linear_wait_probe(timeout_ns, stream));
+  return ok();
+}
+
 static moe_status check_route(const moe_route_config* cfg) {
   if (!cfg) return fail(MOE_ERR_INVALID_ARG, "cfg is NULL");
   const int E = cfg->n_experts, K = cfg->top_k, G = cfg->n_groups, kg = cfg->topk_groups;

@@ -15,6 +15,8 @@
 #include <cuda_bf16.h>
 #include <cuda_fp16.h>
 
+#include <atomic>
+
 #include "../../include/moe.h"
 #include "moe_device.cuh"
 #include "moe_linear.h"
@@ -22,8 +24,9 @@
 
 namespace moe {
 
-// The error word of the calls on a device: the first expired wait's code.
-__device__ uint32_t g_linear_err;
+// Error words of the calls on a device, one per stream (error_slot): the code
+// of the first expired wait.
+__device__ uint32_t g_linear_err[kLinearErrSlots];
 
 namespace {
 
@@ -319,19 +322,22 @@ __device__ __forceinline__ bool bar_try(uint32_t bar, uint32_t parity) {
       : "memory");
   return ok != 0;
 }
-__device__ __noinline__ bool bar_wait_slow(uint32_t bar, uint32_t parity) {
+__device__ __forceinline__ bool bar_wait_until(uint32_t slot, uint32_t bar, uint32_t parity, uint64_t limit_ns) {
   const uint64_t t0 = globaltimer_ns();
   for (uint32_t it = 1;; ++it) {
     if (bar_try(bar, parity)) return true;
-    if ((it & 63u) == 0u && globaltimer_ns() - t0 > kLinearTimeoutNs) {
-      atomicCAS(&g_linear_err, 0u, 1u);
+    if ((it & 63u) == 0u && globaltimer_ns() - t0 > limit_ns) {
+      atomicCAS(&g_linear_err[slot], 0u, 1u);
       return false;
     }
   }
 }
-// Waits for phase `parity` of an mbarrier; false (and the error word set) on timeout.
-__device__ __forceinline__ bool bar_wait(uint32_t bar, uint32_t parity) {
-  return bar_try(bar, parity) || bar_wait_slow(bar, parity);
+__device__ __noinline__ bool bar_wait_slow(uint32_t slot, uint32_t bar, uint32_t parity) {
+  return bar_wait_until(slot, bar, parity, kLinearTimeoutNs);
+}
+// Waits for phase `parity` of an mbarrier; false (and the error word `slot` set) on timeout.
+__device__ __forceinline__ bool bar_wait(uint32_t slot, uint32_t bar, uint32_t parity) {
+  return bar_try(bar, parity) || bar_wait_slow(slot, bar, parity);
 }
 // After a wait has expired: time for copies and MMAs already issued to end
 // before the block leaves its shared memory and TMEM.
@@ -731,7 +737,7 @@ __global__ void __launch_bounds__(kTileThreads, 1)
     uint32_t s = 0, phase = 0;
 #pragma unroll 1
     for (int kb = kb0 + first; kb < kb1; ++kb) {
-      ok = __all_sync(kAll, bar_wait(empty + 8u * s, phase));
+      ok = __all_sync(kAll, bar_wait(p.err_slot, empty + 8u * s, phase));
       if (!ok) break;
       if (lead) copy(kb, s);
       __syncwarp();
@@ -747,7 +753,7 @@ __global__ void __launch_bounds__(kTileThreads, 1)
 #pragma unroll 1
     for (int k0 = kb0, part = 0; k0 < kb1 && ok; ++part) {
       const uint32_t b = (uint32_t)part & 1u;
-      if (SUMS && part >= 2) ok = __all_sync(kAll, bar_wait(accfree + 8u * b, (uint32_t)(part / 2 - 1) & 1u));
+      if (SUMS && part >= 2) ok = __all_sync(kAll, bar_wait(p.err_slot, accfree + 8u * b, (uint32_t)(part / 2 - 1) & 1u));
       if (!ok) break;
       tc::fence_after_sync();
       const int k1 = SUMS ? min(kb1, k0 + kPart) : kb1;
@@ -755,7 +761,7 @@ __global__ void __launch_bounds__(kTileThreads, 1)
       // condition there it cost 0.7 us of the 8 to 10 us of a call)
 #pragma unroll 1
       for (int kb = k0; kb < k1; ++kb) {
-        ok = __all_sync(kAll, bar_wait(full + 8u * s, phase));
+        ok = __all_sync(kAll, bar_wait(p.err_slot, full + 8u * s, phase));
         if (!ok) break;
         tc::fence_after_sync();
         const uint32_t st = s0 + s * plan.stage;
@@ -791,7 +797,7 @@ __global__ void __launch_bounds__(kTileThreads, 1)
 #pragma unroll 1
       for (int part = 0; part < parts && ok; ++part) {
         const uint32_t b = (uint32_t)part & 1u;
-        ok = __all_sync(kAll, bar_wait(accfull + 8u * b, (uint32_t)(part / 2) & 1u));
+        ok = __all_sync(kAll, bar_wait(p.err_slot, accfull + 8u * b, (uint32_t)(part / 2) & 1u));
         if (!ok) break;
         tc::fence_after_sync();
         if (busy && half < G) {
@@ -810,7 +816,7 @@ __global__ void __launch_bounds__(kTileThreads, 1)
         if (lane == 0) bar_arrive(accfree + 8u * b);
       }
     } else {
-      ok = __all_sync(kAll, bar_wait(accfull, 0));
+      ok = __all_sync(kAll, bar_wait(p.err_slot, accfull, 0));
       tc::fence_after_sync();
     }
     if (ok && S > 1)
@@ -965,7 +971,7 @@ __global__ void __launch_bounds__(kPairThreads, 1)
 #pragma unroll 1
       for (int kb = 0; kb < KB; ++kb) {
         if (filled == ST)
-          ok = __all_sync(kAll, bar_wait(empty + 8u * s, phase));
+          ok = __all_sync(kAll, bar_wait(p.err_slot, empty + 8u * s, phase));
         else
           ++filled;
         if (!ok) break;
@@ -982,7 +988,7 @@ __global__ void __launch_bounds__(kPairThreads, 1)
     // the last stages' arrivals from the even CTA, before this block may leave
     if (filled < ST) s = 0, phase = 0;
     for (uint32_t j = 0; j < filled && ok; ++j) {
-      ok = __all_sync(kAll, bar_wait(empty + 8u * s, phase));
+      ok = __all_sync(kAll, bar_wait(p.err_slot, empty + 8u * s, phase));
       if (++s == ST) s = 0, phase ^= 1u;
     }
     if (!ok) let_issued_work_end();
@@ -995,13 +1001,13 @@ __global__ void __launch_bounds__(kPairThreads, 1)
 #pragma unroll 1
       for (int tile = pair, k0 = 0; tile < ntiles && ok; ++it) {
         const uint32_t b = it & 1u;
-        if (it >= 2) ok = __all_sync(kAll, bar_wait(accfree + 8u * b, (it / 2 - 1u) & 1u));
+        if (it >= 2) ok = __all_sync(kAll, bar_wait(p.err_slot, accfree + 8u * b, (it / 2 - 1u) & 1u));
         if (!ok) break;
         tc::fence_after_sync();
         const int k1 = min(KB, k0 + part);
 #pragma unroll 1
         for (int kb = k0; kb < k1; ++kb) {
-          ok = __all_sync(kAll, bar_wait(full + 8u * s, phase));
+          ok = __all_sync(kAll, bar_wait(p.err_slot, full + 8u * s, phase));
           if (!ok) break;
           tc::fence_after_sync();
           const uint32_t st = op0 + s * P::kStage;
@@ -1043,7 +1049,7 @@ __global__ void __launch_bounds__(kPairThreads, 1)
 #pragma unroll 1
         for (int k0 = 0; k0 < KB; k0 += part, ++it) {
           const uint32_t b = it & 1u;
-          ok = __all_sync(kAll, bar_wait(accfull + 8u * b, (it / 2) & 1u));
+          ok = __all_sync(kAll, bar_wait(p.err_slot, accfull + 8u * b, (it / 2) & 1u));
           if (!ok) break;
           tc::fence_after_sync();
           const uint32_t acc = tmem + b * TN + ((uint32_t)(32 * quarter) << 16) + (uint32_t)c0;
@@ -1072,7 +1078,7 @@ __global__ void __launch_bounds__(kPairThreads, 1)
         }
       } else {
         const uint32_t b = it & 1u;
-        ok = __all_sync(kAll, bar_wait(accfull + 8u * b, (it / 2) & 1u));
+        ok = __all_sync(kAll, bar_wait(p.err_slot, accfull + 8u * b, (it / 2) & 1u));
         if (!ok) break;
         ++it;
         tc::fence_after_sync();
@@ -1292,22 +1298,56 @@ cudaError_t launch_any(const LinearParams& p, int sms, cudaStream_t st) {
   return launch_tensor<F16, GATED>(p, sms, st);
 }
 
+// A wait on a barrier that nothing arrives at.
+__global__ void linear_wait_probe_kernel(uint32_t slot, uint64_t limit_ns) {
+  __shared__ __align__(8) uint64_t bar;
+  if (threadIdx.x == 0) {
+    bar_init(smem_u32(&bar), 1);
+    mbar_fence_init();
+    bar_wait_until(slot, smem_u32(&bar), 0, limit_ns);
+  }
+}
+
+// The error word of a stream's calls.  Each stream handle that calls gets a word
+// of its own, for good; the default stream, and streams beyond the last free
+// word, have the first.
+uint32_t error_slot(cudaStream_t st) {
+  static std::atomic<uintptr_t> taken[kLinearErrSlots];
+  const uintptr_t key = reinterpret_cast<uintptr_t>(st);
+  if (st == nullptr || st == cudaStreamLegacy) return 0;
+  uint32_t at = (uint32_t)((key >> 4) * 0x9e3779b97f4a7c15ull >> 32);
+  for (int n = 0; n < kLinearErrSlots; ++n, ++at) {
+    const uint32_t i = at % kLinearErrSlots;
+    if (i == 0) continue;
+    uintptr_t was = 0;
+    if (taken[i].load() == key || taken[i].compare_exchange_strong(was, key) || was == key) return i;
+  }
+  return 0;
+}
+
 }  // namespace
 
-cudaError_t launch_linear(const LinearParams& p, bool f16, int sms, cudaStream_t st) {
+cudaError_t launch_linear(LinearParams p, bool f16, int sms, cudaStream_t st) {
+  p.err_slot = error_slot(st);
   if (p.w_up) return f16 ? launch_any<true, true>(p, sms, st) : launch_any<false, true>(p, sms, st);
   return f16 ? launch_any<true, false>(p, sms, st) : launch_any<false, false>(p, sms, st);
 }
 
 cudaError_t read_linear_error(uint32_t* code, cudaStream_t st) {
   uint32_t zero = 0;
-  cudaError_t e = cudaMemcpyFromSymbolAsync(code, g_linear_err, 4, 0, cudaMemcpyDeviceToHost, st);
+  const size_t at = 4 * error_slot(st);
+  cudaError_t e = cudaMemcpyFromSymbolAsync(code, g_linear_err, 4, at, cudaMemcpyDeviceToHost, st);
   if (e == cudaSuccess) e = cudaStreamSynchronize(st);
   if (e == cudaSuccess && *code) {
-    e = cudaMemcpyToSymbolAsync(g_linear_err, &zero, 4, 0, cudaMemcpyHostToDevice, st);
+    e = cudaMemcpyToSymbolAsync(g_linear_err, &zero, 4, at, cudaMemcpyHostToDevice, st);
     if (e == cudaSuccess) e = cudaStreamSynchronize(st);
   }
   return e;
+}
+
+cudaError_t launch_linear_wait_probe(uint64_t limit_ns, cudaStream_t st) {
+  linear_wait_probe_kernel<<<1, 32, 0, st>>>(error_slot(st), limit_ns);
+  return cudaGetLastError();
 }
 
 }  // namespace moe

@@ -14,6 +14,7 @@ struct LinearParams {
   int out_f32;   // output (and residual) fp32, else the 16-bit input type
   int vec;       // every row of out (and residual) starts on a 16-byte boundary
   int bias_vec;  // the biases start on 16-byte boundaries
+  uint32_t err_slot;  // the error word of the call's stream (set by launch_linear)
   const uint16_t* x;
   const uint16_t* w;
   const uint16_t* w_up;  // null: not gated
@@ -48,8 +49,11 @@ cudaError_t launch_early(void (*kernel)(P...), dim3 grid, int threads, size_t sm
 }
 
 // f16: the 16-bit type is fp16, else bf16.  sms: the device's SM count.
-cudaError_t launch_linear(const LinearParams& p, bool f16, int sms, cudaStream_t st);
+cudaError_t launch_linear(LinearParams p, bool f16, int sms, cudaStream_t st);
+// Error words of the calls on a device; the word of the stream `st` is read and cleared.
+constexpr int kLinearErrSlots = 1024;
 cudaError_t read_linear_error(uint32_t* code, cudaStream_t st);
+cudaError_t launch_linear_wait_probe(uint64_t limit_ns, cudaStream_t st);
 
 // Expert choice from logits (moe_route.cu).
 struct RouteParams {

@@ -388,3 +388,30 @@ def test_long_sums_in_16_bits(T, N, dtype, K, gated):
     ref = product(w) * (product(wu) if gated else 1.0)
     half = torch.finfo(dt).eps / 2
     assert ((out.double() - ref).abs() <= (1 + (2 if gated else 1) / 16) * half * ref.abs()).all()
+
+
+@pytest.mark.gpu
+def test_an_expired_wait_is_reported_to_its_stream_alone():
+    """A wait that runs out on one stream: reads on other streams neither show nor clear it, its own does both once."""
+    import torch
+    a, b = torch.cuda.Stream(), torch.cuda.Stream()
+    M.moe_linear_selftest_bounded_wait(2_000_000, stream=a)
+    torch.cuda.synchronize()
+    assert M.moe_linear_device_error(b) == (M.MOE_OK, 0)
+    assert M.moe_linear_device_error() == (M.MOE_OK, 0)
+    assert M.moe_linear_device_error(a) == (6, 1)  # MOE_ERR_TIMEOUT
+    assert M.moe_linear_device_error(a) == (M.MOE_OK, 0)
+    M.moe_linear_selftest_bounded_wait(2_000_000)  # the default stream's own
+    assert M.moe_linear_device_error(a) == (M.MOE_OK, 0)
+    assert M.moe_linear_device_error() == (6, 1)
+    d = make(40, 256, 64)
+    for st in (a, b, None):  # and products run as before
+        out = torch.empty(40, 64, dtype=torch.bfloat16, device="cuda")
+        torch.cuda.synchronize()
+        M.moe_linear_forward(d["cfg"], d["wts"], d["x"], out, stream=st)
+        assert M.moe_linear_device_error(st) == (M.MOE_OK, 0)
+        check(out, *d["ref"])
+
+
+def test_selftest_limit_is_refused_on_the_host():
+    assert M.lib().moe_linear_selftest_bounded_wait(1 << 40, None) == M.MOE_ERR_INVALID_ARG
