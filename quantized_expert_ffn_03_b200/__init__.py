@@ -400,10 +400,11 @@ def _types():
     """Looks torch up, once; the package imports without it."""
     global _torch_c, _int32
     import torch
+    torch.cuda.current_stream()  # initialises CUDA
     _dtype_sets.update({c: frozenset(getattr(torch, n) for n in names) for c, names in _DTYPE_NAMES.items()})
     _logit_codes.update({torch.float32: MOE_F32, torch.bfloat16: MOE_BF16, torch.float16: MOE_F16})
-    _int32, _torch_c = torch.int32, torch._C
-    torch.cuda.current_stream()  # initialises CUDA
+    _int32 = torch.int32
+    _torch_c = torch._C  # last: what other threads look at
 
 
 def _bad(what):

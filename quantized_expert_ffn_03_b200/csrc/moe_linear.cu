@@ -1141,15 +1141,16 @@ bool make_map(CUtensorMap* m, bool f16, const void* base, int K, int rows, int64
                    CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
 }
 
-// Allows a kernel `smem` bytes of dynamic shared memory, once per device.
+// Allows a kernel `smem` bytes of dynamic shared memory, once per device.  Host
+// threads that meet here set the same value.
 template <auto Kernel>
 cudaError_t allow_smem(uint32_t smem) {
-  static bool set[64] = {};
+  static std::atomic<bool> set[64];
   int dev = 0;
   cudaError_t e = cudaGetDevice(&dev);
-  if (e != cudaSuccess || (dev >= 0 && dev < 64 && set[dev])) return e;
+  if (e != cudaSuccess || (dev >= 0 && dev < 64 && set[dev].load(std::memory_order_acquire))) return e;
   e = cudaFuncSetAttribute(Kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)smem);
-  if (e == cudaSuccess && dev >= 0 && dev < 64) set[dev] = true;
+  if (e == cudaSuccess && dev >= 0 && dev < 64) set[dev].store(true, std::memory_order_release);
   return e;
 }
 

@@ -415,3 +415,50 @@ def test_an_expired_wait_is_reported_to_its_stream_alone():
 
 def test_selftest_limit_is_refused_on_the_host():
     assert M.lib().moe_linear_selftest_bounded_wait(1 << 40, None) == M.MOE_ERR_INVALID_ARG
+
+
+@pytest.mark.gpu
+def test_first_calls_from_many_host_threads():
+    """Eight host threads whose first calls of every kernel meet, each on its own stream, in a fresh process."""
+    import subprocess
+    import sys
+    code = """
+import sys, threading
+sys.path[:0] = %r
+import torch
+import quantized_expert_ffn_03_b200 as M
+torch.cuda.init()
+sizes = [(1, 512, 200), (12, 512, 200), (20, 512, 96), (64, 1024, 256), (300, 512, 512), (2100, 256, 1024)]
+data = []
+for i in range(8):
+    for T, K, N in sizes:
+        x, w = (torch.randn(n, K, device="cuda").bfloat16() for n in (T, N))
+        data.append((i, x, w, torch.zeros(T, N, device="cuda"), x.double() @ w.double().T))
+torch.cuda.synchronize()
+meet, bad = threading.Barrier(8), []
+def work(i):
+    try:
+        st = torch.cuda.Stream()
+        meet.wait()
+        for j, x, w, out, _ in data:
+            if j == i:
+                cfg = M.linear_config(x.shape[1], w.shape[0], out_dtype=M.MOE_F32)
+                M.moe_linear_forward(cfg, M.linear_weights(cfg, w), x, out, stream=st)
+        if M.moe_linear_device_error(st) != (M.MOE_OK, 0):
+            bad.append("device error")
+    except Exception as e:
+        bad.append(repr(e))
+ts = [threading.Thread(target=work, args=(i,)) for i in range(8)]
+[t.start() for t in ts]
+[t.join() for t in ts]
+torch.cuda.synchronize()
+# a sum of K products of 8-bit significands in fp32: 2 K 2^-24 of their magnitudes
+for _, x, w, out, ref in data:
+    lim = 2 * x.shape[1] * 2.0 ** -24 * (x.double().abs() @ w.double().abs().T)
+    if not ((out.double() - ref).abs() <= lim).all():
+        bad.append(tuple(out.shape))
+print(bad)
+sys.exit(1 if bad else 0)
+""" % ([p for p in sys.path if p],)
+    r = subprocess.run([sys.executable, "-c", code], capture_output=True, text=True, timeout=300)
+    assert r.returncode == 0, r.stdout + r.stderr
