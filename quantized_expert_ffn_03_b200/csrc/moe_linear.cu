@@ -373,8 +373,9 @@ constexpr uint32_t kTile = 128u * 128u;  // bytes of a 128-row operand tile of o
 // XOR-ed by the row as the tensor map's swizzle has it, and leave by a TMA
 // store, which also cuts off what lies behind T and N (4096 tokens x 256 ->
 // 8192 features: 21 us, of which the bare writing takes 18; with rows written
-// by the lanes from accumulator fragments 55).  Rows that do not start on
-// 16-byte boundaries are written by the lanes, from the square in row order.
+// by the lanes from accumulator fragments 55).  It cuts off whole 16-byte pieces
+// only, so a unit whose rows end inside one, and rows that do not start on
+// 16-byte boundaries, are written by the lanes, from the square in row order.
 constexpr uint32_t kSquare = 4096u;  // bytes per warp: 32 x 32 fp32, or two of 16 bits
 
 // DIRECT: the lanes write their tokens' 64 bytes themselves, which takes more
@@ -432,9 +433,9 @@ struct Epilogue {
 #pragma unroll
       for (int i = 0; i < 32; ++i) v[i] *= u[i];
     }
-    if (p.vec) {
-      // a piece of the residual behind N is not there to be read in 16 bytes
-      const bool whole = n0 + 32 <= p.N, live = t0 + lane < p.T;
+    // a piece of the residual behind N is not there to be read in 16 bytes
+    const bool whole = n0 + 32 <= p.N, live = t0 + lane < p.T;
+    if (p.vec && (whole || p.whole_end)) {
       if (!p.out_f32) {
         if (p.res) {
           if (whole) {
@@ -490,6 +491,10 @@ struct Epilogue {
         send(square, t0, n0);
       }
       return;
+    }
+    if (p.vec) {  // stores of units before this one may still read the square
+      if (lane == 0) tc::store_wait_read<0>();
+      __syncwarp();
     }
     if (p.out_f32) {
       __syncwarp();

@@ -13,6 +13,7 @@ struct LinearParams {
   int act;       // MOE_ACT_*
   int out_f32;   // output (and residual) fp32, else the 16-bit input type
   int vec;       // every row of out (and residual) starts on a 16-byte boundary
+  int whole_end;  // and N features end on one
   int bias_vec;  // the biases start on 16-byte boundaries
   uint32_t err_slot;  // the error word of the call's stream (set by launch_linear)
   const uint16_t* x;

@@ -462,3 +462,30 @@ sys.exit(1 if bad else 0)
 """ % ([p for p in sys.path if p],)
     r = subprocess.run([sys.executable, "-c", code], capture_output=True, text=True, timeout=300)
     assert r.returncode == 0, r.stdout + r.stderr
+
+
+@pytest.mark.gpu
+@pytest.mark.parametrize("T", [3, 12, 17, 70, 200, 2600])
+@pytest.mark.parametrize("N", [1, 33, 50, 129, 250, 1003])
+@pytest.mark.parametrize("dtype,out", [("bf16", "bf16"), ("f16", "f32")])
+@pytest.mark.parametrize("gated", [False, True])
+def test_ragged_features_in_rows_on_16_byte_boundaries(T, N, dtype, out, gated):
+    """N features that end inside 16 bytes of rows that start on them: what lies behind N in the row stays as it was,
+    whether the residual is laid out alike, otherwise, or is the output itself."""
+    import torch
+    ldo = (N + 7) // 8 * 8 + 8
+    d = make(T, 200, N, dtype, out, "silu", gated, bias=True, res=True, seed=12)
+    ref, apart = d["ref"], d["res"]
+    check(run_guarded(d, T, N, out, ldo=ldo), *ref)
+    alike = torch.full((T, ldo), float("nan"), dtype=apart.dtype, device="cuda")
+    alike[:, :N] = apart
+    d["res"] = alike[:, :N]
+    check(run_guarded(d, T, N, out, ldo=ldo), *ref)
+    place = torch.full((T, ldo), SENTINEL, dtype=apart.dtype, device="cuda")
+    place[:, :N] = apart
+    M.moe_linear_forward(d["cfg"], d["wts"], d["x"], place[:, :N], residual=place[:, :N])
+    check(place[:, :N], *ref)
+    assert (place[:, N:] == SENTINEL).all()
+    d["res"] = None
+    y = reference(d["x"], d["w"], d["bias"], "silu", d["wu"], d["bias_u"])
+    check(run_guarded(d, T, N, out, ldo=ldo), *y)
