@@ -17,7 +17,7 @@ LIB = os.path.join(HERE, "libmoe.so")
 SOURCES = ["moe_abi.cu", "moe_decode.cu", "moe_router.cu", "moe_pack.cu", "moe_noalloc.cu", "moe_stream.cu",
            "moe_grouped.cu", "moe_linear.cu", "moe_route.cu"]
 HEADERS = ["moe_device.cuh", "moe_kernels.h", "moe_layout.h", "moe_stream_policy.h", "moe_tc.cuh", "moe_grouped.h",
-           "moe_linear.h"]
+           "moe_linear.h", "moe_linear_way.h"]
 NVCC = os.environ.get("NVCC", "/usr/local/cuda/bin/nvcc")
 ARCH = ["-gencode", "arch=compute_100a,code=sm_100a"]
 

@@ -2,7 +2,7 @@
 //   y[t][n] = act(x[t] . w[n] + bias[n]) [* (x[t] . w_up[n] + bias_up[n])] [+ res[t][n]]
 // fp32 accumulation and epilogue, one rounding to the output type.
 //
-// Three kernels, by how many tokens there are (launch_any, best_way):
+// Three kernels, by how many tokens there are (linear_way):
 //   rows   up to 16: the weights stream once through shared memory into
 //          m16n8k16 steps (HBM bound);
 //   tile   some hundreds: tiles of up to 128 tokens x 32 to 128 features,
@@ -20,6 +20,7 @@
 #include "../../include/moe.h"
 #include "moe_device.cuh"
 #include "moe_linear.h"
+#include "moe_linear_way.h"
 #include "moe_tc.cuh"
 
 namespace moe {
@@ -31,25 +32,6 @@ __device__ uint32_t g_linear_err[kLinearErrSlots];
 namespace {
 
 constexpr unsigned kAll = 0xffffffffu;
-constexpr int kKB = 64;  // columns of K per step: 128 bytes, one swizzle row
-
-// The tensor cores cut what an addition shifts out of the accumulator's 24
-// bits, always towards zero, which makes a sum over many columns too small:
-// for operands of one sign by 7.9 10^-6 of its size after 4096 columns of one
-// accumulator, 6.5 10^-5 after 16384, 3.4 10^-4 after 65536, 1.5 10^-3 after
-// 2^18 (measured; mixed signs a quarter of that, but 4.4 10^-6 after 4096).
-// Where the output shows that, an accumulator holds kPart steps (512 columns),
-// and the parts are added up in fp32, rounding to nearest: 2.4 10^-7 (mixed
-// signs 4.8 10^-7) up to K = 16384, below 7.5 10^-7 at 2^20.
-constexpr int kPart = 512 / kKB;
-// The longest K that one accumulator takes: 512 columns for fp32 outputs, and
-// for 16-bit ones what keeps the loss below 1/16 of half a step of the type
-// (2^-11 for fp16, 2^-8 for bf16).  Parts need narrower tiles: fp16 2048 x 16384
-// x 4096 takes 254 us with them, 193 without.
-__host__ __device__ constexpr int longest_sum(bool out_f32, bool f16) {
-  return out_f32 ? kPart * kKB : f16 ? 1 << 13 : 1 << 15;
-}
-
 // ---- epilogue arithmetic ------------------------------------------------------------
 
 // 1 / (1 + e^-z), as 2^-64 / (2^-64 + (g 2^-32)^2) with g = e^(-z/2): g stays in
@@ -174,7 +156,7 @@ __device__ __forceinline__ void mma16816(float (&c)[4], uint32_t a0, uint32_t a1
 // weights, each byte read once; the rest is the launch and the first loads' way.  With few blocks a
 // block takes more warps, so that an SM has its 32 all the same (512 features:
 // 3.5 us with 32, 4.4 with 8).
-constexpr int kRowsFeat = 8, kRowsTok = 16;
+constexpr int kRowsFeat = 8;
 constexpr uint32_t kRowsUnit = 1024u;  // bytes of a warp's unit: 8 rows x 64 columns
 __host__ __device__ constexpr int rows_depth(int na) { return na == 1 ? 4 : 3; }
 __host__ __device__ constexpr uint32_t rows_smem(int na, int warps) { return (uint32_t)(warps * rows_depth(na) * na) * kRowsUnit; }
@@ -618,7 +600,6 @@ __device__ __forceinline__ void load_unit(uint32_t taddr, float (&v)[32]) {
 constexpr int kTileEpi = 8;                         // warps that read TMEM
 constexpr int kTileThreads = 32 * (kTileEpi + 2);   // + a loading and an MMA warp
 constexpr int kTileStages = 12;                     // at most
-constexpr int kMaxSplit = 4;                        // CTAs of a cluster (16 clusters of 8 do not fit the GPCs at once)
 constexpr uint32_t kMaxSmem = 227u * 1024u - 512u;  // dynamic shared memory next to the static
 
 // Shared-memory plan of a tile: stages, their bytes, and the slots for other
@@ -1231,77 +1212,28 @@ cudaError_t launch_rows(const LinearParams& p, int sms, cudaStream_t st) {
   return launch_rows_w<F16, GATED, TM, 8>(p, st);
 }
 
-// How long each way of doing a product takes, in ns, from measurements of the
-// parts (steps of 64 columns of K): what a launch and a tile cost besides their
-// steps, a step by what its copies move per SM (about 115 bytes per ns) or by
-// its MMAs, an epilogue unit.  Against every way tried on 50 sizes (20 to 8192
-// tokens, K 64 to 8192, N 512 to 16384) the way it picks is the fastest or
-// mostly within 4 percent of it, at the worst 14; no one way is near the fastest
-// everywhere (64 x 4096 x 4096: 9.8 us by clusters of 4 against 12.5 unsplit;
-// 1024 x 4096 x 4096: 26 us by pairs of 256 columns against 36 by tiles;
-// 2048 x 1024 x 1024 gated: 9.7 us by pairs of 128 columns, 10.8 by 256).
-struct Way {
-  int pair, width, S;  // pair: TN; tile: FN, CTAs of a cluster
-  float ns;
-};
-float max_f(float a, float b) { return a > b ? a : b; }
-// narrow: tiles of at most 64 features, pairs of 128 columns (those that keep
-// sums in registers).
-Way best_way(int T, int K, int N, bool gated, bool narrow, int sms) {
-  const int KB = (K + kKB - 1) / kKB, na = gated ? 2 : 1;
-  Way best = {0, 0, 0, 1e30f};
-  const int BT = T <= 32 ? 32 : T <= 64 ? 64 : 128;
-  for (int FN = 32; FN <= (gated || narrow ? 64 : 128); FN *= 2) {
-    const int64_t tiles = (int64_t)((N + FN - 1) / FN) * ((T + BT - 1) / BT);
-    if (tiles > 8 * sms) continue;
-    for (int S = 1; S <= kMaxSplit && S <= KB; S *= 2) {
-      const int64_t waves = (tiles * S + (S == 4 ? 127 : sms - 1)) / (S == 4 ? 128 : sms);
-      const float step = max_f(170.f, (float)(BT + na * FN) * 128.f / 115.f);
-      const int units = (FN / 32 + 1) / 2;  // of a warp
-      const float tail = S == 1 ? 500.f * units
-                                : (S == 4 && BT == 128 ? 2000.f : 1100.f) + 300.f * (S - 1) + 500.f * ((units + S - 1) / S);
-      const float ns = (float)waves * (2500.f + (float)((KB + S - 1) / S) * step + na * tail);
-      if (ns < best.ns) best = {0, FN, S, ns};
-    }
-  }
-  for (int TN = 128; TN <= (narrow ? 128 : 256); TN *= 2) {
-    const int FN = TN / na;
-    const int64_t tiles = (int64_t)((T + 255) / 256) * ((N + FN - 1) / FN);
-    const int64_t waves = (tiles + sms / 2 - 1) / (sms / 2);
-    const float steps = (float)KB * (TN == 256 ? 310.f : 195.f), epilogue = (TN == 256 ? 450.f : 520.f) * FN / 64 * na;
-    const float ns = 3300.f + (float)waves * max_f(steps, epilogue) + epilogue;
-    if (ns < best.ns) best = {TN, 0, 1, ns};
-  }
-  return best;
-}
-
-template <bool F16, bool GATED>
-cudaError_t launch_tensor(const LinearParams& p, int sms, cudaStream_t st) {
-  const bool sums = p.K > longest_sum(p.out_f32, F16);
-  const Way w = best_way(p.T, p.K, p.N, GATED, sums, sms);
-  const int BT = p.T <= 32 ? 32 : p.T <= 64 ? 64 : 128;
-  if (sums) {
-    if (w.pair) return launch_pair_t<F16, GATED, 128, true>(p, sms, st);
-    return w.width == 32 ? launch_tile_t<F16, GATED, 32, true>(p, BT, w.S, st)
-                         : launch_tile_t<F16, GATED, 64, true>(p, BT, w.S, st);
-  }
-  if (w.pair == 256) return launch_pair_t<F16, GATED, 256, false>(p, sms, st);
-  if (w.pair == 128) return launch_pair_t<F16, GATED, 128, false>(p, sms, st);
-  if (w.width == 32) return launch_tile_t<F16, GATED, 32, false>(p, BT, w.S, st);
-  if (w.width == 64) return launch_tile_t<F16, GATED, 64, false>(p, BT, w.S, st);
-  if constexpr (!GATED) return launch_tile_t<F16, GATED, 128, false>(p, BT, w.S, st);
-  return cudaErrorInvalidValue;
-}
-
 template <bool F16, bool GATED>
 cudaError_t launch_any(const LinearParams& p, int sms, cudaStream_t st) {
-  // 9 to 16 tokens: weights beyond about 40 MB stream faster by TMA (8192 x 8192:
-  // 27 us against 35; 4096 x 4096: 9.5 against 9.3)
-  const bool heavy = (int64_t)p.N * p.K * (GATED ? 2 : 1) > (20 << 20) && encoder();
-  if (p.T <= 8) return launch_rows<F16, GATED, 8>(p, sms, st);
-  if (p.T <= kRowsTok && !heavy) return launch_rows<F16, GATED, 16>(p, sms, st);
-  if (!encoder()) return cudaErrorNotSupported;
-  return launch_tensor<F16, GATED>(p, sms, st);
+  LinearWay w = linear_way(p.T, p.K, p.N, GATED, F16, p.out_f32, sms);
+  if (w.tokens > kRowsTok && !encoder()) {
+    if (p.T > kRowsTok) return cudaErrorNotSupported;
+    w.tokens = kRowsTok;
+  }
+  if (w.tokens == 8) return launch_rows<F16, GATED, 8>(p, sms, st);
+  if (w.tokens == 16) return launch_rows<F16, GATED, 16>(p, sms, st);
+  const bool pair = w.tokens == 256;
+  if (w.sums) {
+    if (pair) return launch_pair_t<F16, GATED, 128, true>(p, sms, st);
+    return w.width == 32 ? launch_tile_t<F16, GATED, 32, true>(p, w.tokens, w.split, st)
+                         : launch_tile_t<F16, GATED, 64, true>(p, w.tokens, w.split, st);
+  }
+  if (pair)
+    return w.width == 256 ? launch_pair_t<F16, GATED, 256, false>(p, sms, st)
+                          : launch_pair_t<F16, GATED, 128, false>(p, sms, st);
+  if (w.width == 32) return launch_tile_t<F16, GATED, 32, false>(p, w.tokens, w.split, st);
+  if (w.width == 64) return launch_tile_t<F16, GATED, 64, false>(p, w.tokens, w.split, st);
+  if constexpr (!GATED) return launch_tile_t<F16, GATED, 128, false>(p, w.tokens, w.split, st);
+  return cudaErrorInvalidValue;
 }
 
 // A wait on a barrier that nothing arrives at.

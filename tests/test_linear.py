@@ -489,3 +489,82 @@ def test_ragged_features_in_rows_on_16_byte_boundaries(T, N, dtype, out, gated):
     d["res"] = None
     y = reference(d["x"], d["w"], d["bias"], "silu", d["wu"], d["bias_u"])
     check(run_guarded(d, T, N, out, ldo=ldo), *y)
+
+
+# ---- every kernel and tile that the sizes can choose --------------------------------------
+
+# T, K, N, gated, 16-bit type, output type; tokens and width of a tile, CTAs that
+# split its K, sums of parts: linear_way's choice on 148 SMs.  Ragged ends in
+# every dimension; pairs beyond 2048 tokens number their tiles in groups of 8,
+# the last one shorter.
+WAYS = [
+    (5, 1100, 90, 0, "bf16", "bf16", (8, 8, 1, 0)), (11, 1100, 90, 1, "f16", "f32", (16, 8, 1, 0)),
+    (17, 90, 50, 0, "bf16", "f32", (32, 32, 1, 0)), (19, 300, 90, 1, "bf16", "bf16", (32, 32, 1, 0)),
+    (12, 11000, 2050, 0, "f16", "f16", (32, 32, 2, 1)), (18, 2100, 100, 0, "bf16", "bf16", (32, 32, 4, 0)),
+    (20, 2200, 70, 1, "f16", "f32", (32, 32, 4, 1)), (17, 1150, 2080, 0, "f16", "f32", (32, 32, 2, 1)),
+    (17, 2327, 2080, 1, "bf16", "bf16", (32, 32, 2, 0)), (17, 40, 4850, 0, "bf16", "bf16", (32, 64, 1, 0)),
+    (18, 1133, 2478, 0, "f16", "f32", (32, 64, 2, 1)), (17, 2242, 2531, 1, "f16", "f16", (32, 64, 2, 0)),
+    (17, 2116, 1075, 1, "bf16", "f32", (32, 64, 4, 1)), (19, 1123, 4757, 0, "bf16", "bf16", (32, 128, 2, 0)),
+    (17, 1100, 2135, 0, "f16", "f16", (32, 128, 4, 0)),
+    (44, 5400, 5430, 0, "bf16", "bf16", (64, 128, 2, 0)), (57, 1690, 2105, 0, "f16", "f16", (64, 128, 4, 0)),
+    (33, 1089, 2122, 0, "f16", "f16", (64, 32, 2, 0)), (36, 2454, 1061, 1, "f16", "f32", (64, 64, 4, 1)),
+    (40, 100, 4817, 1, "bf16", "bf16", (64, 64, 1, 0)), (33, 531, 4959, 0, "f16", "f32", (64, 64, 1, 1)),
+    (67, 100, 90, 0, "bf16", "bf16", (128, 32, 1, 0)), (70, 1900, 90, 1, "f16", "f32", (128, 32, 2, 1)),
+    (69, 2400, 70, 0, "bf16", "f32", (128, 32, 4, 1)), (70, 4000, 70, 1, "f16", "f16", (128, 32, 4, 0)),
+    (135, 1261, 1223, 0, "f16", "f32", (128, 64, 2, 1)), (131, 40, 2421, 1, "f16", "f32", (128, 64, 1, 0)),
+    (69, 2650, 2391, 1, "bf16", "bf16", (128, 64, 2, 0)), (70, 2850, 1071, 0, "f16", "f32", (128, 64, 4, 1)),
+    (132, 36, 4764, 0, "bf16", "bf16", (128, 128, 1, 0)), (67, 1247, 4894, 0, "f16", "f16", (128, 128, 2, 0)),
+    (820, 2740, 402, 0, "bf16", "bf16", (128, 128, 4, 0)), (131, 2740, 1269, 0, "bf16", "bf16", (128, 128, 4, 0)),
+    (262, 40, 6476, 0, "bf16", "bf16", (256, 128, 1, 0)), (6406, 40, 257, 0, "f16", "f32", (256, 128, 1, 0)),
+    (6328, 40, 132, 1, "bf16", "bf16", (256, 128, 1, 0)), (130, 100, 4780, 1, "f16", "f32", (256, 128, 1, 0)),
+    (6385, 1030, 133, 0, "f16", "f32", (256, 128, 1, 1)), (6824, 1090, 65, 1, "bf16", "f32", (256, 128, 1, 1)),
+    (6407, 620, 257, 0, "f16", "f16", (256, 256, 1, 0)), (2500, 700, 1301, 0, "bf16", "bf16", (256, 256, 1, 0)),
+    (4000, 500, 2000, 0, "bf16", "f32", (256, 256, 1, 0)), (6285, 623, 135, 1, "bf16", "bf16", (256, 256, 1, 0)),
+    (2300, 700, 1000, 1, "f16", "f16", (256, 256, 1, 0)), (2300, 510, 2001, 1, "f16", "f32", (256, 256, 1, 0)),
+    (14, 9000, 4400, 0, "f16", "f16", (32, 64, 2, 1))]
+WAY_DRIVER = """
+#include <cstdio>
+#include "moe_linear_way.h"
+int main() {
+  int T, K, N, gated, f16, f32;
+  while (scanf("%d %d %d %d %d %d", &T, &K, &N, &gated, &f16, &f32) == 6) {
+    const moe::LinearWay w = moe::linear_way(T, K, N, gated, f16, f32, 148);
+    printf("%d %d %d %d\\n", w.tokens, w.width, w.split, (int)w.sums);
+  }
+}
+"""
+
+
+def test_ways_that_the_sizes_choose(tmp_path):
+    """The table below is what linear_way chooses, so that the GPU test reaches every kernel and tile."""
+    import os
+    import subprocess
+    src, exe = tmp_path / "ways.cpp", tmp_path / "ways"
+    src.write_text(WAY_DRIVER)
+    csrc = os.path.join(os.path.dirname(M.LIB_PATH), "csrc")
+    subprocess.check_call(["g++", "-std=c++17", "-O1", "-I", csrc, str(src), "-o", str(exe)])
+    text = "".join("%d %d %d %d %d %d\n" % (*c[:4], c[4] == "f16", c[5] == "f32") for c in WAYS)
+    out = subprocess.run([str(exe)], input=text, capture_output=True, text=True, check=True).stdout.splitlines()
+    got = [tuple(int(v) for v in line.split()) for line in out]
+    assert [(c[:6], w) for c, w in zip(WAYS, got) if w != c[6]] == []
+    tiles = {(w[0], w[1]) for w in got}
+    assert tiles == {(8, 8), (16, 8), (256, 128), (256, 256)} | {(t, f) for t in (32, 64, 128) for f in (32, 64, 128)}
+
+
+@pytest.mark.gpu
+@pytest.mark.parametrize("case", WAYS, ids=lambda c: "x".join(map(str, c[:3])) + "-" + "-".join(map(str, c[6])))
+def test_every_way_matches_formula(case):
+    """Against 64 bits with bias, activation and residual, rows of the output on 16-byte boundaries and anywhere; a
+    second run gives the same bits."""
+    T, K, N, gated, dtype, out, _ = case
+    d = make(T, K, N, dtype, out, "silu" if gated else "gelu", bool(gated), bias=True, res=True, pad=8, seed=11)
+    wide = (N + 7) // 8 * 8 + 8
+    a = run_guarded(d, T, N, out, ldo=wide)
+    check(a, *d["ref"])
+    assert (run_guarded(d, T, N, out, ldo=wide) == a).all()
+    check(run_guarded(d, T, N, out, ldo=wide + 1), *d["ref"])
+    import torch
+    far = torch.zeros(T, wide, dtype=d["res"].dtype, device="cuda")  # the residual on such boundaries as well
+    far[:, :N] = d["res"]
+    d["res"] = far[:, :N]
+    assert (run_guarded(d, T, N, out, ldo=wide) == a).all()
