@@ -978,8 +978,7 @@ moe_status moe_linear_forward(const moe_linear_config* cfg, const moe_linear_wei
            (!residual || (aligned(residual, bytes) && (T == 1 || ldr * osz % bytes == 0)));
   };
   p.bias_vec = aligned(wts->bias, 16) && aligned(cfg->gated ? wts->bias_up : nullptr, 16);
-  p.vec = starts_on(16);
-  p.whole_end = N * osz % 16 == 0;
+  p.vec = !starts_on(16) ? 0 : N * osz % 16 == 0 ? 2 : 1;
   p.x = static_cast<const uint16_t*>(x);
   p.w = static_cast<const uint16_t*>(wts->w);
   p.w_up = cfg->gated ? static_cast<const uint16_t*>(wts->w_up) : nullptr;

@@ -417,7 +417,7 @@ struct Epilogue {
     }
     // a piece of the residual behind N is not there to be read in 16 bytes
     const bool whole = n0 + 32 <= p.N, live = t0 + lane < p.T;
-    if (p.vec && (whole || p.whole_end)) {
+    if (p.vec == 2 || (p.vec && whole)) {
       if (!p.out_f32) {
         if (p.res) {
           if (whole) {

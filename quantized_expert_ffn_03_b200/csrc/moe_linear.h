@@ -8,12 +8,12 @@
 namespace moe {
 
 // y[t][n] = act(x[t] . w[n] + bias[n]) [* (x[t] . w_up[n] + bias_up[n])] [+ res[t][n]]
+// (8 bytes more of it cost calls of 3 to 8 us 3 to 4 percent.)
 struct LinearParams {
   int T, K, N;
   int act;       // MOE_ACT_*
   int out_f32;   // output (and residual) fp32, else the 16-bit input type
-  int vec;       // every row of out (and residual) starts on a 16-byte boundary
-  int whole_end;  // and N features end on one
+  int vec;       // every row of out (and residual) starts on a 16-byte boundary (1), and N features end on one (2)
   int bias_vec;  // the biases start on 16-byte boundaries
   uint32_t err_slot;  // the error word of the call's stream (set by launch_linear)
   const uint16_t* x;
