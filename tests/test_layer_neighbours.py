@@ -208,3 +208,84 @@ def test_a_given_routing_off_its_elements_is_refused_on_the_host(fn):
         assert getattr(lib, fn)(C.byref(cfg), C.byref(wts), 16, 16, 40, idx, w, 16, 16, 256, 1 << 20, None) == 1
         assert "aligned to their elements" in M.last_error(), (idx, w)
     assert getattr(lib, fn)(C.byref(cfg), C.byref(wts), 16, 16, 0, 18, 17, 16, 16, 256, 0, None) == 0
+
+
+@pytest.mark.gpu
+@pytest.mark.parametrize("T", [2, 14, 50, 300, 2200])
+def test_biases_that_start_between_16_byte_boundaries(T):
+    """Biases cut out of a longer vector: products, and choices with and without groups."""
+    import torch
+    from test_linear import check, make
+    from test_route import draw, plain
+    for gated in (False, True):
+        d = make(T, 136, 200, "bf16", "bf16", "silu", gated, bias=True, seed=14)
+        cut = lambda b: None if b is None else torch.cat([b.new_full((1,), float("nan")), b])[1:]  # noqa: E731
+        wts = M.linear_weights(d["cfg"], d["w"], cut(d["bias"]), d["wu"], cut(d["bias_u"]))
+        out = torch.empty(T, 200, dtype=torch.bfloat16, device="cuda")
+        M.moe_linear_forward(d["cfg"], wts, d["x"], out)
+        check(out, *d["ref"])
+    l = draw(T, 128, 15)
+    sb = torch.randn(131, generator=torch.Generator(device="cuda").manual_seed(1), device="cuda")[3:] * 0.1
+    for groups, keep in ((1, 1), (8, 3)):
+        cfg = M.route_config(128, 6, M.MOE_SCORE_SIGMOID, groups, keep, M.MOE_GROUP_TOP2)
+        idx, w = torch.empty(T, 6, dtype=torch.int32, device="cuda"), torch.empty(T, 6, device="cuda")
+        M.moe_route_from_logits(cfg, l, idx, w, select_bias=sb)
+        wi, _ = plain(l.double().cpu().numpy(), sb.cpu().numpy(), 6, score="sigmoid", groups=groups, keep=keep,
+                      group_score="top2")
+        assert np.array_equal(idx.cpu().numpy(), wi)
+
+
+@pytest.mark.gpu
+@pytest.mark.parametrize("T", [1, 40, 700])
+def test_captured_between_copies_and_forks(T):
+    """A graph whose calls stand behind a host copy, a memset, a fork and a join, replayed on new inputs: each call
+    waits for all that is ahead of it."""
+    import torch
+    g = torch.Generator().manual_seed(T)
+    H, E = 512, 64
+    w = [(torch.randn(H, H, generator=g) * 0.05).bfloat16().cuda() for _ in range(3)]
+    wr = (torch.randn(E, H, generator=g) * 0.05).bfloat16().cuda()
+    cfg = M.linear_config(H, H)
+    wts = [M.linear_weights(cfg, a) for a in w]
+    rc = M.route_config(E, 4, M.MOE_SCORE_SIGMOID, 8, 3, M.MOE_GROUP_TOP2)
+    host = torch.empty(T, H, dtype=torch.bfloat16, pin_memory=True)
+    x, a, b, y = (torch.zeros(T, H, dtype=torch.bfloat16, device="cuda") for _ in range(4))
+    logits = torch.empty(T, E, device="cuda")
+    idx, wt = torch.empty(T, 4, dtype=torch.int32, device="cuda"), torch.empty(T, 4, device="cuda")
+    back = torch.empty(T, 4, dtype=torch.int32, pin_memory=True)
+    side = torch.cuda.Stream()
+
+    def step():
+        main = torch.cuda.current_stream()
+        x.copy_(host, non_blocking=True)
+        y.zero_()
+        M.moe_linear_forward(cfg, wts[0], x, a)
+        side.wait_stream(main)
+        with torch.cuda.stream(side):
+            M.moe_linear_forward(cfg, wts[1], a, b)
+        M.moe_linear_forward(cfg, wts[2], a, y, residual=y)
+        main.wait_stream(side)
+        M.moe_linear_forward(cfg, wts[0], b, y, residual=y)
+        M.moe_route_topk(rc, y, wr, idx, wt, logits_out=logits)
+        back.copy_(idx, non_blocking=True)
+
+    ins = [torch.randn(T, H, generator=g).bfloat16() for _ in range(6)]
+    host.copy_(ins[0])
+    step()
+    torch.cuda.synchronize()
+    graph = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(graph):
+        step()
+    for v in ins:
+        host.copy_(v)
+        step()
+        torch.cuda.synchronize()
+        want = y.clone(), wt.clone(), back.clone()
+        for t in (x, a, b, y, logits):
+            t.fill_(float("nan"))
+        back.zero_()
+        torch.cuda.synchronize()
+        graph.replay()
+        torch.cuda.synchronize()
+        assert torch.equal(y, want[0]) and torch.equal(wt, want[1]) and torch.equal(back, want[2])
+    assert M.moe_linear_device_error() == (M.MOE_OK, 0)
