@@ -376,3 +376,15 @@ def test_a_weight_whose_score_leaves_the_range_of_fp32():
     want = np.exp(-88.8 + 69.0)
     np.testing.assert_allclose(w[0, 1], np.exp(np.float64(np.float32(-88.8)) + 69.0), rtol=WEIGHT_RTOL[True])
     assert abs(w[0, 1] / want - 1) < 1e-5
+
+
+@pytest.mark.gpu
+@pytest.mark.parametrize("E", [1280, 1281, 1472, 1473, 1500, 1536, 1537, 1984, 2047])
+@pytest.mark.parametrize("bias", [False, True])
+def test_numbers_of_experts_around_the_shared_memory_limit(E, bias):
+    """A row's fp64 keys take 8 bytes of shared memory per expert and warp, next to some static ones; a row of equal
+    logits and one of nothing need them."""
+    l = draw(6, E, E)
+    l[1], l[2] = 0.5, -float("inf")
+    for K in (1, 9):
+        check(l, K, bias_of(E, 2) if bias else None, score="sigmoid")
