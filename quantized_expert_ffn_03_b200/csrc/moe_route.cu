@@ -4,11 +4,12 @@
 //   of v within them, ties to the lower index; w = scale * s [/ sum of s].
 // One warp per token, the row in its registers: lane holds E / 32 values, and
 // each choice is one integer maximum over the warp.  A row is read once (DRAM
-// 16.8 MB for 16384 x 512 bf16, its size), so what bounds the kernel is its
-// instructions, 0.6 to 0.7 issued per cycle and scheduler: top_k rounds of
-// choosing and, with groups, their ranking.  16384 tokens, 512 experts, top 10:
-// 12.3 us; 4096 tokens, top 8 of 4 of 16 groups: 9.4 us; one token: 3.0 us, of
-// which all but some hundred ns is the launch and the way of one load.
+// 16.8 MB for 16384 x 512 bf16, its size), so what bounds the kernel is the
+// chain of a row's dependent steps, top_k rounds of choosing and, with groups,
+// their ranking, which the 28 warps of an SM cover in part (0.56 to 0.7
+// instructions issued per cycle and scheduler).  16384 tokens, 512 experts, top
+// 10: 12.6 us; 4096 tokens, top 8 of 4 of 16 groups: 8.8 us; one token: 2.2 us,
+// of which all but some hundred ns is the launch and the way of one load.
 #include <cuda_bf16.h>
 #include <cuda_fp16.h>
 #include <float.h>
